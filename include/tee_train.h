@@ -1,0 +1,88 @@
+/*
+ * tee_train.h -- the operators a training step of the encoder adds to the
+ * forward pass (same library as tee.h): the LayerNorm, the scaled token lookup
+ * and the softmax cross entropy over the vocabulary, each forward and backward.
+ *
+ * As in tee_ops.h every call runs on caller-provided DEVICE buffers,
+ * asynchronously on `stream` (a cudaStream_t, NULL = legacy default stream), on
+ * the device of `ctx`, which also supplies the status word and the error
+ * message; the current device of the caller is left as it was.  The context's
+ * weights are not used (they need not be loaded): a training program owns its
+ * parameters, so tables, gains and gradients are arguments.  No call allocates
+ * device memory, synchronises or keeps anything between calls, so all of them
+ * can be captured into a CUDA graph; scratch memory is the caller's (d_ws,
+ * ws_bytes, at least what the operator's *_workspace function returns; its
+ * contents need no initialisation and mean nothing afterwards).  Calls that may
+ * overlap on the GPU need a workspace each.
+ *
+ * Buffers are row-major and contiguous.  Element types are given as TEE_F32
+ * (float) or TEE_BF16 (bfloat16, uint16 bit patterns); any other value is
+ * TEE_EINVAL.  Buffers are 16-byte aligned (int32 and statistics arrays and the
+ * per-position floats: 4-byte aligned, statistics 8); a NULL or misaligned
+ * buffer or a workspace that is too small returns TEE_EINVAL before anything is
+ * launched.  Outputs must not overlap inputs except where stated.  Results do
+ * not depend on the order in which thread blocks run: the same inputs give the
+ * same bits.
+ *
+ * Arithmetic: inputs are widened to fp32, sums and statistics are fp32 (the
+ * products of the vocabulary loss take bf16 operands into fp32 accumulators),
+ * outputs are rounded once to their type.
+ */
+#ifndef TEE_TRAIN_H
+#define TEE_TRAIN_H
+
+#include <stddef.h>
+#include <stdint.h>
+#include "tee.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* ---- LayerNorm (bias-free, as tee_op_layernorm) ---------------------------
+ *   mean_t = sum_h x[t,h] / H,  rstd_t = 1 / sqrt(sum_h (x[t,h] - mean_t)^2 / H + eps)
+ *   y[t,h] = (x[t,h] - mean_t) rstd_t gamma[h]
+ * 1 <= H <= TEE_LN_MAX_HIDDEN; T >= 0 rows. */
+#define TEE_LN_MAX_HIDDEN 8192
+
+/* y y_type[T*H], stats float[T*2] ({mean, rstd} per row, for the backward pass;
+ * NULL if not wanted) from x x_type[T*H] and gamma float[H].  d_y may be d_x
+ * where the types are the same. */
+int tee_op_layernorm_forward(tee_ctx* ctx, const void* d_x, int x_type, const float* d_gamma, void* d_y, int y_type,
+                             float* d_stats, int T, int H, float eps, void* stream);
+
+/* With xhat = (x - mean) rstd and u = dy gamma:
+ *   dx[t,h]   = rstd_t (u[t,h] - sum_h u[t,h] / H - xhat[t,h] sum_h u[t,h] xhat[t,h] / H) + dres[t,h]
+ *   dgamma[h] = sum_t dy[t,h] xhat[t,h]
+ * dy y_type[T*H]; x, dres (the gradient that reaches x past the norm, as on a
+ * residual branch; NULL for none) and dx x_type[T*H]; stats as the forward pass
+ * wrote them.  d_dx may be d_dres, or d_x or d_dy where the types are the same.
+ * With T == 0 dgamma is set to zero. */
+int tee_op_layernorm_backward(tee_ctx* ctx, const void* d_dy, int y_type, const void* d_x, int x_type,
+                              const float* d_gamma, const float* d_stats, const void* d_dres, void* d_dx,
+                              float* d_dgamma, int T, int H, void* d_ws, size_t ws_bytes, void* stream);
+long long tee_layernorm_backward_workspace(int T, int H);
+
+/* ---- token lookup with scaling ---------------------------------------------
+ *   y[t] = scale E[id[t]],   E table_type[V*H], ids int32[T], y y_type[T*H]
+ * An id outside [0, V) gives a zero row and sets the context's device status
+ * (tee_device_status), as in tee_op_embed.  1 <= H <= 65536, V >= 1. */
+int tee_op_embed_forward(tee_ctx* ctx, const void* d_table, int table_type, const int32_t* d_ids, void* d_y, int y_type,
+                         int T, int V, int H, float scale, void* stream);
+
+/* The table's gradient:  dE[v] (+)= scale sum_{t: id[t] = v} dy[t], the tokens
+ * of a row added in a fixed order (the tokens are sorted by id, stably).
+ * dy y_type[T*H], dE table_type[V*H].  accumulate 0: every row of dE is written,
+ * rows without a token with zeros; 1: rows with tokens are added to (in fp32,
+ * rounded once) and the others left alone, as for a table that also has the
+ * gradient of the vocabulary loss.  A token whose id is outside [0, V) adds
+ * nothing and sets the device status. */
+int tee_op_embed_backward(tee_ctx* ctx, const void* d_dy, int y_type, const int32_t* d_ids, void* d_dtable,
+                          int table_type, int T, int V, int H, float scale, int accumulate, void* d_ws,
+                          size_t ws_bytes, void* stream);
+long long tee_embed_backward_workspace(int T, int V, int H);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* TEE_TRAIN_H */

@@ -1,0 +1,35 @@
+"""The training operators' host side, without a GPU: workspace sizes, and NULL contexts."""
+import pytest
+
+from test_abi import built_lib  # noqa: F401
+from text_embedding_encoder_gb300 import binding
+
+
+def test_workspace_sizes(built_lib):  # noqa: F811
+    ln, em = built_lib.tee_layernorm_backward_workspace, built_lib.tee_embed_backward_workspace
+    assert ln(0, 768) == 0
+    assert ln(1, 768) == 768 * 4 and ln(8, 768) == 768 * 4 and ln(9, 768) == 2 * 768 * 4
+    assert ln(1 << 30, 768) == ln(65536, 768) == 640 * 768 * 4        # the grid is bounded
+    assert ln(1 << 30, 8192) == 640 * 8192 * 4
+    assert em(0, 1, 1) == 0
+    # two pair arrays, a state and two fp32 rows for each block of 256 tokens, rounded up to 256 bytes each
+    assert em(257, 1000, 768) == 2 * 2304 + 256 + 2 * (2 * 768 * 4)
+    assert em(1 << 30, 1, 1) > 1 << 33                               # past 32 bits
+
+
+@pytest.mark.parametrize("name,sizes", [
+    ("layernorm_backward", (-1, 8)), ("layernorm_backward", (1, 0)), ("layernorm_backward", (1, 8193)),
+    ("layernorm_backward", ((1 << 30) + 1, 8)), ("embed_backward", (-1, 5, 8)), ("embed_backward", (1, 0, 8)),
+    ("embed_backward", (1, 5, 0)), ("embed_backward", (1, 5, 65537)),
+])
+def test_workspace_refusals(built_lib, name, sizes):  # noqa: F811
+    assert getattr(built_lib, f"tee_{name}_workspace")(*sizes) == binding.TEE_EINVAL
+    assert name in built_lib.tee_last_error(None).decode()
+
+
+def test_null_context(built_lib):  # noqa: F811
+    E = binding.TEE_EINVAL
+    assert built_lib.tee_op_layernorm_forward(None, None, 0, None, None, 0, None, 0, 8, 1e-5, None) == E
+    assert built_lib.tee_op_layernorm_backward(None, None, 0, None, 0, None, None, None, None, None, 0, 8, None, 0, None) == E
+    assert built_lib.tee_op_embed_forward(None, None, 0, None, None, 0, 0, 1, 8, 1.0, None) == E
+    assert built_lib.tee_op_embed_backward(None, None, 0, None, None, 0, 0, 1, 8, 1.0, 0, None, 0, None) == E

@@ -1,4 +1,4 @@
-"""Thin ctypes binding of the C ABI (include/tee.h, include/tee_ops.h).
+"""Thin ctypes binding of the C ABI (include/tee.h, include/tee_ops.h, include/tee_train.h).
 
 Argument marshalling only: every step of the encoder runs in the CUDA
 library.  There is no fallback: if the compiled library is missing, loading
@@ -60,6 +60,7 @@ class TeeKernelStat(ctypes.Structure):
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _ctx = ctypes.c_void_p
+_sz = ctypes.c_size_t
 _I32P = ctypes.POINTER(ctypes.c_int32)
 
 # name -> (restype, argtypes), for every function declared in include/*.h
@@ -99,6 +100,12 @@ SIGNATURES = {
     "tee_unigram_destroy": (None, [_vp]),
     "tee_similarity": (_i, [_vp, _i, _i, _vp]),
     "tee_plan_gemm": (_i, [_i, _i, _i, _i, _i, ctypes.POINTER(_i), ctypes.POINTER(_i)]),
+    "tee_op_layernorm_forward": (_i, [_ctx, _vp, _i, _vp, _vp, _i, _vp, _i, _i, ctypes.c_float, _vp]),
+    "tee_op_layernorm_backward": (_i, [_ctx, _vp, _i, _vp, _i, _vp, _vp, _vp, _vp, _vp, _i, _i, _vp, _sz, _vp]),
+    "tee_layernorm_backward_workspace": (ctypes.c_longlong, [_i, _i]),
+    "tee_op_embed_forward": (_i, [_ctx, _vp, _i, _vp, _vp, _i, _i, _i, _i, ctypes.c_float, _vp]),
+    "tee_op_embed_backward": (_i, [_ctx, _vp, _i, _vp, _vp, _i, _i, _i, _i, ctypes.c_float, _i, _vp, _sz, _vp]),
+    "tee_embed_backward_workspace": (ctypes.c_longlong, [_i, _i, _i]),
 }
 
 _LIB = None
@@ -258,6 +265,16 @@ class Encoder:
     def op(self, name, *args):
         return self.check(getattr(self.lib, name)(self.ctx, *[_ptr(a) if not isinstance(a, (int, float)) else a
                                                               for a in args]))
+
+
+def workspace_bytes(name: str, *sizes: int) -> int:
+    """Bytes of scratch memory that the training operator ``tee_op_<name>`` needs for these sizes
+    (tee_<name>_workspace, include/tee_train.h)."""
+    lib = load()
+    n = getattr(lib, f"tee_{name}_workspace")(*sizes)
+    if n < 0:
+        raise TeeError(int(n), lib.tee_last_error(None).decode())
+    return int(n)
 
 
 # ---------------------------------------------------------------------------

@@ -1,0 +1,297 @@
+// LayerNorm for training: forward with the rows' statistics, and the backward
+// pass with the reduction of the gain's gradient (tee_train.h has the formulas).
+//
+// Both are bound by HBM: forward reads x and writes y once, backward reads x,
+// dy (and the residual gradient) and writes dx once.  A row is held in the
+// registers of WPR warps (one up to 1024 columns), eight consecutive columns
+// per lane and chunk, so the variance is taken around the mean without reading
+// the row again.
+#include "train_internal.cuh"
+
+namespace {
+
+constexpr int THREADS = 256, WARPS = THREADS / 32;
+// Backward: most thread blocks, each with a partial sum of the gain's gradient
+// (four per SM on 152 SMs, rounded up).
+constexpr int BWD_MAX_GRID = 640;
+
+// How a row of H elements is spread over a group of G = 32 WPR lanes, VPL
+// chunks of eight elements each.  VEC (H % 8 == 0): a chunk is eight consecutive
+// elements, moved as 16-byte vectors; otherwise element by element, lanes
+// interleaved.
+template <bool VEC, int VPL, int WPR>
+struct Row {
+    static constexpr int G = 32 * WPR, N = 8 * VPL;
+    static __device__ __forceinline__ int col(int k, int lg) { return VEC ? ((k >> 3) * G + lg) * 8 + (k & 7) : k * G + lg; }
+    static __device__ __forceinline__ bool has(int k, int lg, int H) { return col(VEC ? k & ~7 : k, lg) < H; }
+    template <typename T>
+    static __device__ __forceinline__ void load(const T* row, int H, int lg, float (&v)[N]) {
+        if constexpr (VEC) {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                if (has(8 * i, lg, H)) load8(row + col(8 * i, lg), v + 8 * i);
+                else
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[8 * i + j] = 0.f;
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; ++k) v[k] = has(k, lg, H) ? elem_to_f32(row[col(k, lg)]) : 0.f;
+        }
+    }
+    template <typename T>
+    static __device__ __forceinline__ void store(T* row, int H, int lg, const float (&v)[N]) {
+        if constexpr (VEC) {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                if (has(8 * i, lg, H)) store8(row + col(8 * i, lg), v + 8 * i);
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                if (has(k, lg, H)) f32_to_elem(v[k], row[col(k, lg)]);
+        }
+    }
+};
+
+// Sum over the group's lanes; every thread of the block calls it.  `red` holds
+// one slot per warp and must not be reused before the next block barrier after
+// this call's own.
+template <int WPR>
+__device__ __forceinline__ float2 group_sum(float a, float b, float2* red) {
+    a = warp_sum_f32(a);
+    b = warp_sum_f32(b);
+    if constexpr (WPR > 1) {
+        const int warp = threadIdx.x >> 5;
+        if ((threadIdx.x & 31) == 0) red[warp] = make_float2(a, b);
+        __syncthreads();
+        const int w0 = warp / WPR * WPR;
+        a = b = 0.f;
+#pragma unroll
+        for (int w = 0; w < WPR; ++w) {
+            a += red[w0 + w].x;
+            b += red[w0 + w].y;
+        }
+    }
+    return make_float2(a, b);
+}
+
+template <typename TX, typename TY, bool VEC, int VPL, int WPR>
+__global__ void __launch_bounds__(THREADS) ln_forward_kernel(const TX* x, const float* __restrict__ gamma, TY* y,
+                                                             float2* __restrict__ stats, int T, int H, float eps) {
+    using R = Row<VEC, VPL, WPR>;
+    pdl_wait();
+    pdl_trigger();
+    __shared__ float2 red[2][WARPS];
+    const int lg = threadIdx.x % R::G;
+    const int t = blockIdx.x * (THREADS / R::G) + threadIdx.x / R::G;
+    if (WPR == 1 && t >= T) return;
+    const bool live = t < T;
+    const size_t base = (size_t)(live ? t : T - 1) * H;
+    float v[R::N];
+    R::load(x + base, H, lg, v);
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < R::N; ++k) s += v[k];
+    const float mean = group_sum<WPR>(s, 0.f, red[0]).x / (float)H;
+    float ss = 0.f;
+#pragma unroll
+    for (int k = 0; k < R::N; ++k) {
+        const float d = R::has(k, lg, H) ? v[k] - mean : 0.f;
+        ss += d * d;
+    }
+    const float rstd = 1.0f / sqrtf(group_sum<WPR>(ss, 0.f, red[1]).x / (float)H + eps);
+    if (!live) return;
+    float g[R::N];
+    R::load(gamma, H, lg, g);
+#pragma unroll
+    for (int k = 0; k < R::N; ++k) v[k] = (v[k] - mean) * rstd * g[k];
+    R::store(y + base, H, lg, v);
+    if (stats && lg == 0) stats[t] = make_float2(mean, rstd);
+}
+
+// Groups take rows blockIdx-strided; each lane keeps the gain's gradient of its
+// columns over all its rows, the block adds its groups' sums and writes one row
+// of partials, which ln_dgamma_kernel adds up in a fixed order.
+template <typename TX, typename TY, bool VEC, int VPL, int WPR>
+__global__ void __launch_bounds__(THREADS)
+    ln_backward_kernel(const TY* dy, const TX* x, const float* __restrict__ gamma, const float2* __restrict__ stats,
+                       const TX* dres, TX* dx, float* __restrict__ partial, int T, int H) {
+    using R = Row<VEC, VPL, WPR>;
+    constexpr int GROUPS = THREADS / R::G;
+    extern __shared__ __align__(16) float acc[];   // GROUPS > 1: [GROUPS][H]
+    pdl_wait();
+    pdl_trigger();
+    __shared__ float2 red[2][WARPS];
+    const int lg = threadIdx.x % R::G, grp = threadIdx.x / R::G;
+    const float inv_h = 1.0f / (float)H;
+    float dg[R::N];
+#pragma unroll
+    for (int k = 0; k < R::N; ++k) dg[k] = 0.f;
+    int par = 0;
+    for (int t0 = blockIdx.x * GROUPS; t0 < T; t0 += gridDim.x * GROUPS, par ^= 1) {
+        const int t = t0 + grp;
+        if (WPR == 1 && t >= T) break;
+        const size_t base = (size_t)t * H;   // WPR > 1: GROUPS rows exist whenever a block enters the loop with one
+        const bool live = t < T;
+        float xh[R::N], d[R::N], g[R::N];
+        if (live) {
+            R::load(x + base, H, lg, xh);
+            R::load(dy + base, H, lg, d);
+        } else {
+#pragma unroll
+            for (int k = 0; k < R::N; ++k) xh[k] = d[k] = 0.f;
+        }
+        const float2 st = live ? stats[t] : make_float2(0.f, 0.f);
+        R::load(gamma, H, lg, g);
+        float su = 0.f, sux = 0.f;
+#pragma unroll
+        for (int k = 0; k < R::N; ++k) {
+            xh[k] = (xh[k] - st.x) * st.y;
+            if (R::has(k, lg, H)) dg[k] += d[k] * xh[k];   // a column past H has xh = -mean rstd, d = 0
+            d[k] *= g[k];
+            su += d[k];
+            sux += d[k] * xh[k];
+        }
+        const float2 sums = group_sum<WPR>(su, sux, red[par]);
+        if (!live) continue;
+        const float mu = sums.x * inv_h, mux = sums.y * inv_h;
+#pragma unroll
+        for (int k = 0; k < R::N; ++k) d[k] = st.y * (d[k] - mu - xh[k] * mux);
+        if (dres) {
+            R::load(dres + base, H, lg, xh);
+#pragma unroll
+            for (int k = 0; k < R::N; ++k) d[k] += xh[k];
+        }
+        R::store(dx + base, H, lg, d);
+    }
+    float* out = partial + (size_t)blockIdx.x * H;
+    if constexpr (GROUPS == 1) {
+        R::store(out, H, lg, dg);
+    } else {
+        R::store(acc + (size_t)grp * H, H, lg, dg);
+        __syncthreads();
+        for (int h = threadIdx.x; h < H; h += THREADS) {
+            float s = 0.f;
+#pragma unroll
+            for (int w = 0; w < GROUPS; ++w) s += acc[(size_t)w * H + h];
+            out[h] = s;
+        }
+    }
+}
+
+// dgamma[h] = sum over the blocks' partials: 32 columns per block, 32 slices of
+// the partials, added slice by slice.
+__global__ void __launch_bounds__(1024) ln_dgamma_kernel(const float* __restrict__ partial, int n, int H,
+                                                         float* __restrict__ dgamma) {
+    pdl_wait();
+    pdl_trigger();
+    __shared__ float red[32][33];
+    const int cx = threadIdx.x & 31, sl = threadIdx.x >> 5;
+    const int h = blockIdx.x * 32 + cx;
+    float s = 0.f;
+    if (h < H) {
+#pragma unroll 4
+        for (int i = sl; i < n; i += 32) s += partial[(size_t)i * H + h];
+    }
+    red[sl][cx] = s;
+    __syncthreads();
+    const float v = warp_sum_f32(red[cx][sl]);   // column sl of this block, over its 32 slices
+    if (cx == 0 && blockIdx.x * 32 + sl < H) dgamma[blockIdx.x * 32 + sl] = v;
+}
+
+// Calls f.template operator()<VEC, VPL, WPR>() with the row layout for H: the
+// fewest chunks per lane that hold the row in one warp up to 1024 columns, then
+// the fewest warps.
+template <typename F>
+cudaError_t with_layout(int H, F&& f) {
+    if (H % 8 == 0) {
+        if (H <= 256) return f.template operator()<true, 1, 1>();
+        if (H <= 512) return f.template operator()<true, 2, 1>();
+        if (H <= 768) return f.template operator()<true, 3, 1>();
+        if (H <= 1024) return f.template operator()<true, 4, 1>();
+        if (H <= 2048) return f.template operator()<true, 4, 2>();
+        if (H <= 4096) return f.template operator()<true, 4, 4>();
+        return f.template operator()<true, 4, 8>();
+    }
+    if (H <= 256) return f.template operator()<false, 1, 1>();
+    if (H <= 1024) return f.template operator()<false, 4, 1>();
+    if (H <= 2048) return f.template operator()<false, 4, 2>();
+    if (H <= 4096) return f.template operator()<false, 4, 4>();
+    return f.template operator()<false, 4, 8>();
+}
+
+template <typename TX, typename TY>
+struct Forward {
+    const void* x;
+    const float* gamma;
+    void* y;
+    float* stats;
+    int T, H;
+    float eps;
+    cudaStream_t s;
+    template <bool VEC, int VPL, int WPR>
+    cudaError_t operator()() const {
+        const int rows = WARPS / WPR;
+        return launch_pdl(ln_forward_kernel<TX, TY, VEC, VPL, WPR>, dim3((T - 1) / rows + 1), dim3(THREADS), 0, s,
+                          (const TX*)x, gamma, (TY*)y, reinterpret_cast<float2*>(stats), T, H, eps);
+    }
+};
+
+template <typename TX, typename TY>
+struct Backward {
+    const void *dy, *x;
+    const float *gamma, *stats;
+    const void* dres;
+    void* dx;
+    float *dgamma, *partial;
+    int T, H, num_sms;
+    cudaStream_t s;
+    template <bool VEC, int VPL, int WPR>
+    cudaError_t operator()() const {
+        constexpr int GROUPS = WARPS / WPR;
+        // two resident blocks per SM: the three row buffers and the gradient sums fill half the registers each
+        const int grid = min(min((T - 1) / GROUPS + 1, 2 * num_sms), BWD_MAX_GRID);
+        const size_t smem = GROUPS > 1 ? (size_t)GROUPS * H * sizeof(float) : 0;   // at most 32 KB
+        cudaError_t e = launch_pdl(ln_backward_kernel<TX, TY, VEC, VPL, WPR>, dim3(grid), dim3(THREADS), smem, s,
+                                   (const TY*)dy, (const TX*)x, gamma, reinterpret_cast<const float2*>(stats),
+                                   (const TX*)dres, (TX*)dx, partial, T, H);
+        if (e != cudaSuccess) return e;
+        return launch_pdl(ln_dgamma_kernel, dim3((H + 31) / 32), dim3(1024), 0, s, (const float*)partial, grid, H,
+                          dgamma);
+    }
+};
+
+}  // namespace
+
+size_t layernorm_backward_ws(int T, int H) {
+    const int groups = H <= 1024 ? 8 : H <= 2048 ? 4 : H <= 4096 ? 2 : 1;
+    const int grid = T < 1 ? 0 : min((T - 1) / groups + 1, BWD_MAX_GRID);
+    WsCarve ws(nullptr);
+    ws.take<float>((size_t)grid * H);
+    return ws.off;
+}
+
+cudaError_t launch_layernorm_forward(const void* x, bool x_bf16, const float* gamma, void* y, bool y_bf16, float* stats,
+                                     int T, int H, float eps, cudaStream_t s) {
+    if (T == 0) return cudaSuccess;
+    if (x_bf16)
+        return y_bf16 ? with_layout(H, Forward<bf16, bf16>{x, gamma, y, stats, T, H, eps, s})
+                      : with_layout(H, Forward<bf16, float>{x, gamma, y, stats, T, H, eps, s});
+    return y_bf16 ? with_layout(H, Forward<float, bf16>{x, gamma, y, stats, T, H, eps, s})
+                  : with_layout(H, Forward<float, float>{x, gamma, y, stats, T, H, eps, s});
+}
+
+cudaError_t launch_layernorm_backward(const void* dy, bool y_bf16, const void* x, bool x_bf16, const float* gamma,
+                                      const float* stats, const void* dres, void* dx, float* dgamma, int T, int H,
+                                      void* ws, cudaStream_t s) {
+    if (T == 0) return cudaMemsetAsync(dgamma, 0, (size_t)H * sizeof(float), s);
+    int dev = 0, num_sms = 0;
+    cudaError_t e = tee_current_device(&dev, &num_sms);
+    if (e != cudaSuccess) return e;
+    float* partial = (float*)ws;
+    if (x_bf16)
+        return y_bf16 ? with_layout(H, Backward<bf16, bf16>{dy, x, gamma, stats, dres, dx, dgamma, partial, T, H, num_sms, s})
+                      : with_layout(H, Backward<bf16, float>{dy, x, gamma, stats, dres, dx, dgamma, partial, T, H, num_sms, s});
+    return y_bf16 ? with_layout(H, Backward<float, bf16>{dy, x, gamma, stats, dres, dx, dgamma, partial, T, H, num_sms, s})
+                  : with_layout(H, Backward<float, float>{dy, x, gamma, stats, dres, dx, dgamma, partial, T, H, num_sms, s});
+}

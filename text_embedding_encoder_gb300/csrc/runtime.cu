@@ -343,6 +343,8 @@ int prepare_attention_items(tee_ctx* ctx, const int32_t* h_cu, int n_texts, cuda
 }  // namespace
 
 int tee_set_global_error(int code, const char* msg) { return fail(nullptr, code, "%s", msg); }
+int tee_set_error(tee_ctx* ctx, int code, const char* msg) { return fail(ctx, code, "%s", msg); }
+int tee_set_cuda_error(tee_ctx* ctx, cudaError_t e, const char* what) { return cuda_fail(ctx, e, what); }
 
 cudaError_t tee_current_device(int* dev, int* num_sms) {
     static std::mutex mu;
@@ -622,22 +624,6 @@ int check_dev(tee_ctx* ctx, long long n, int align, std::initializer_list<const 
     }
     return TEE_OK;
 }
-
-// Makes the context's device current for one entry point and restores the
-// caller's current device on the way out, so a process may interleave
-// contexts on several devices.
-struct DeviceScope {
-    int prev = -1;
-    cudaError_t err = cudaSuccess;
-    explicit DeviceScope(int dev) {
-        if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
-        if (prev != dev) err = cudaSetDevice(dev);
-    }
-    ~DeviceScope() {
-        int cur = -1;
-        if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
-    }
-};
 
 #define ON_DEVICE(ctx)                                                            \
     DeviceScope _dscope((ctx)->device);                                           \

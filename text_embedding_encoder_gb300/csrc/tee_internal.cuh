@@ -131,6 +131,25 @@ inline int layer_is_global(const tee_ctx* c, int l) { return (l % c->cfg.global_
 
 // Record the message returned by tee_last_error(NULL) for context-free calls; returns `code`.
 int tee_set_global_error(int code, const char* msg);
+// The same for a context's own error message; a CUDA error gives TEE_ENOMEM or TEE_ECUDA.
+int tee_set_error(tee_ctx* ctx, int code, const char* msg);
+int tee_set_cuda_error(tee_ctx* ctx, cudaError_t e, const char* what);
+
+// Makes the context's device current for one entry point and restores the
+// caller's current device on the way out, so a process may interleave
+// contexts on several devices.
+struct DeviceScope {
+    int prev = -1;
+    cudaError_t err = cudaSuccess;
+    explicit DeviceScope(int dev) {
+        if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
+        if (prev != dev) err = cudaSetDevice(dev);
+    }
+    ~DeviceScope() {
+        int cur = -1;
+        if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
+    }
+};
 
 // One process may drive several devices (one context each), so everything the
 // launchers cache about a device -- its SM count, the kernels' shared-memory
