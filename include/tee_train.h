@@ -82,6 +82,41 @@ int tee_op_embed_backward(tee_ctx* ctx, const void* d_dy, int y_type, const int3
                           size_t ws_bytes, void* stream);
 long long tee_embed_backward_workspace(int T, int V, int H);
 
+/* ---- softmax cross entropy over the vocabulary -------------------------------
+ * Masked-token prediction with the token table as the output weight.  For the
+ * counted positions i (those whose target is not ignore_id):
+ *   logit[i,v] = x[i] . w[v],   lse[i] = log sum_v exp logit[i,v],
+ *   loss[i] = lse[i] - logit[i, target[i]]
+ * and loss[i] = lse[i] = 0 for the others, which cost no products and whose
+ * states are not looked at.  The logits are not kept, not even for one position:
+ * both passes work through them tile by tile.  A target that is neither
+ * ignore_id nor in [0, V) is treated as ignored and sets the device status.
+ *   x bf16[N*H], w bf16[V*H], targets int32[N], loss and lse float[N];
+ *   H a multiple of 8 in [8, TEE_VOCAB_MAX_HIDDEN]; 0 <= N <= 2^24,
+ *   1 <= V <= 2^24, and ceil(N / 256) ceil(V / 256) <= 2^30.
+ * A wait inside the products that does not end gives TEE_ETIMEOUT from the next
+ * tee_device_status, as in the tensor-core projections. */
+#define TEE_VOCAB_MAX_HIDDEN 8192
+int tee_op_vocab_loss_forward(tee_ctx* ctx, const void* d_x, const void* d_w, const int32_t* d_targets, float* d_loss,
+                              float* d_lse, int N, int V, int H, int ignore_id, void* d_ws, size_t ws_bytes,
+                              void* stream);
+long long tee_vocab_loss_forward_workspace(int N, int V, int H);
+
+/* With g[i] the gradient that reaches loss[i] (1 / their number for the mean over
+ * the counted positions) and D[i,v] = g[i] (exp(logit[i,v] - lse[i]) - [v == target[i]]):
+ *   dx[i] = sum_v D[i,v] w[v]   (0 for positions that are not counted),
+ *   dw[v] = sum_i D[i,v] x[i]
+ * gloss float[N], lse as the forward pass wrote it, dx bf16[N*H], dw bf16[V*H];
+ * d_dx or d_dw may be NULL where that gradient is not wanted (not both).  D is
+ * rounded to bf16, as the other operands of these products are (its rows first
+ * divided by the largest |g|).  Every row of dw is written, zeros where nothing
+ * reaches it, also with N == 0; a table that is also looked up gets the lookup's
+ * gradient added by tee_op_embed_backward with accumulate 1. */
+int tee_op_vocab_loss_backward(tee_ctx* ctx, const void* d_x, const void* d_w, const int32_t* d_targets,
+                               const float* d_lse, const float* d_gloss, void* d_dx, void* d_dw, int N, int V, int H,
+                               int ignore_id, void* d_ws, size_t ws_bytes, void* stream);
+long long tee_vocab_loss_backward_workspace(int N, int V, int H);
+
 #ifdef __cplusplus
 }
 #endif

@@ -33,3 +33,19 @@ def test_null_context(built_lib):  # noqa: F811
     assert built_lib.tee_op_layernorm_backward(None, None, 0, None, 0, None, None, None, None, None, 0, 8, None, 0, None) == E
     assert built_lib.tee_op_embed_forward(None, None, 0, None, None, 0, 0, 1, 8, 1.0, None) == E
     assert built_lib.tee_op_embed_backward(None, None, 0, None, None, 0, 0, 1, 8, 1.0, 0, None, 0, None) == E
+
+
+def test_vocab_loss_workspace(built_lib):  # noqa: F811
+    f, b = built_lib.tee_vocab_loss_forward_workspace, built_lib.tee_vocab_loss_backward_workspace
+    assert f(0, 100, 64) == 0 and b(0, 100, 64) == 0
+    # far less than the logits, and D in pieces once all of it would be larger than 256 MB
+    assert f(32768, 102400, 768) < 4 * 32768 * 102400 / 16
+    assert b(32768, 102400, 768) < 2 * 32768 * 102400 / 4
+    assert f(1 << 24, 16384, 8) > 1 << 32
+    for bad in ((-1, 5, 8), (1 << 25, 5, 8), (5, 0, 8), (5, 1 << 25, 8), (5, 5, 0), (5, 5, 12), (5, 5, 8200)):
+        for fn in (f, b):
+            assert fn(*bad) == binding.TEE_EINVAL
+            assert "vocab_loss" in built_lib.tee_last_error(None).decode()
+    E = binding.TEE_EINVAL
+    assert built_lib.tee_op_vocab_loss_forward(None, None, None, None, None, None, 1, 1, 8, -100, None, 0, None) == E
+    assert built_lib.tee_op_vocab_loss_backward(None, *[None] * 7, 1, 1, 8, -100, None, 0, None) == E

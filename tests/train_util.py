@@ -77,3 +77,20 @@ def embed_backward(enc, dy, ids, V, e_dtype, scale, into=None):
     enc.op("tee_op_embed_backward", dy, KIND[dy.dtype], ids, grad, KIND[grad.dtype], T, V, H, scale,
            int(into is not None), ws, n, stream())
     return grad
+
+
+def loss_forward(enc, x, w, targets, ignore=-100):
+    (N, H), V = x.shape, len(w)
+    loss, lse = (torch.full((N,), float("nan"), device="cuda") for _ in range(2))
+    ws, n = workspace("vocab_loss_forward", N, V, H)
+    enc.op("tee_op_vocab_loss_forward", x, w, targets, loss, lse, N, V, H, ignore, ws, n, stream())
+    return loss, lse
+
+
+def loss_backward(enc, x, w, targets, lse, gloss, ignore=-100, want_dx=True, want_dw=True):
+    (N, H), V = x.shape, len(w)
+    dx = torch.full((N, H), float("nan"), dtype=torch.bfloat16, device="cuda") if want_dx else None
+    dw = torch.full((V, H), float("nan"), dtype=torch.bfloat16, device="cuda") if want_dw else None
+    ws, n = workspace("vocab_loss_backward", N, V, H)
+    enc.op("tee_op_vocab_loss_backward", x, w, targets, lse, gloss, dx, dw, N, V, H, ignore, ws, n, stream())
+    return dx, dw

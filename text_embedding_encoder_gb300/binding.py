@@ -106,6 +106,10 @@ SIGNATURES = {
     "tee_op_embed_forward": (_i, [_ctx, _vp, _i, _vp, _vp, _i, _i, _i, _i, ctypes.c_float, _vp]),
     "tee_op_embed_backward": (_i, [_ctx, _vp, _i, _vp, _vp, _i, _i, _i, _i, ctypes.c_float, _i, _vp, _sz, _vp]),
     "tee_embed_backward_workspace": (ctypes.c_longlong, [_i, _i, _i]),
+    "tee_op_vocab_loss_forward": (_i, [_ctx, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _sz, _vp]),
+    "tee_vocab_loss_forward_workspace": (ctypes.c_longlong, [_i, _i, _i]),
+    "tee_op_vocab_loss_backward": (_i, [_ctx, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _sz, _vp]),
+    "tee_vocab_loss_backward_workspace": (ctypes.c_longlong, [_i, _i, _i]),
 }
 
 _LIB = None

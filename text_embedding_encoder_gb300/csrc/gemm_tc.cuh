@@ -1,6 +1,7 @@
 // Interface of the tcgen05 (5th-generation tensor core) bf16 GEMM.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -38,3 +39,10 @@ inline int geglu_source_row(int r, int I) {
     const int tile = r / 256, within = r % 256;
     return within < 128 ? tile * 128 + within : I + tile * 128 + (within - 128);
 }
+
+// Tensor map of a row-major matrix [rows, cols] of fp32 (is_f32) or bf16
+// elements, read or written in boxes of box_rows x box_cols with the 128-byte
+// swizzle (box_cols x element size = 128 bytes).  The base is 16-byte aligned and
+// a row (row_elems elements) a multiple of 16 bytes.
+cudaError_t make_tensor_map_2d(CUtensorMap* map, bool is_f32, const void* base, uint64_t rows, uint64_t cols,
+                               uint64_t row_elems, uint32_t box_rows, uint32_t box_cols);

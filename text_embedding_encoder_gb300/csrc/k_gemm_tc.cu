@@ -532,6 +532,21 @@ cudaError_t launch_t(const CUtensorMap& ma, const CUtensorMap& mb, const CUtenso
 
 }  // namespace
 
+cudaError_t make_tensor_map_2d(CUtensorMap* map, bool is_f32, const void* base, uint64_t rows, uint64_t cols,
+                               uint64_t row_elems, uint32_t box_rows, uint32_t box_cols) {
+    std::call_once(g_once, init_once);
+    if (g_init_err != cudaSuccess) return g_init_err;
+    cuuint64_t dims[2] = {cols, rows};
+    cuuint64_t strides[1] = {row_elems * (is_f32 ? 4 : 2)};
+    cuuint32_t box[2] = {box_cols, box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    const CUresult r = g_encode(map, is_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                                const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 void gemm_tc_choose_tiles(int M, int N, int K, int epi, int num_sms, int* bn, int* pair) {
     const int num_m = (M + BM - 1) / BM;
     // Residual add, short K: one CTA per tile (paired CTAs wait on each

@@ -61,6 +61,15 @@ int launch(tee_ctx* ctx, const char* op, int kclass, double flops, double bytes,
     return e == cudaSuccess ? TEE_OK : tee_set_cuda_error(ctx, e, op);
 }
 
+// Sizes of the vocabulary loss; the message of what is wrong with them, or NULL.
+const char* vocab_sizes(int N, int V, int H) {
+    if (N < 0 || N > (1 << 24)) return "N out of range";
+    if (V < 1 || V > (1 << 24)) return "V out of range";
+    if (H < 8 || H % 8 || H > TEE_VOCAB_MAX_HIDDEN) return "H must be a multiple of 8 within range";
+    if (((long long)N + 255) / 256 * (((long long)V + 255) / 256) > (1LL << 30)) return "N times V out of range";
+    return nullptr;
+}
+
 size_t type_size(int t) { return t == TEE_BF16 ? 2 : 4; }
 
 }  // namespace
@@ -162,6 +171,53 @@ int tee_op_embed_backward(tee_ctx* ctx, const void* d_dy, int y_type, const int3
                       return launch_embed_backward(d_dy, y_type == TEE_BF16, d_ids, d_dtable, table_type == TEE_BF16, T, V,
                                                    H, scale, accumulate != 0, d_ws, ctx->d_status, s);
                   });
+}
+
+long long tee_vocab_loss_forward_workspace(int N, int V, int H) {
+    if (vocab_sizes(N, V, H)) return tee_set_global_error(TEE_EINVAL, "vocab_loss_forward_workspace: N, V or H out of range");
+    return N ? (long long)vocab_loss_ws(N, V, H, false) : 0;
+}
+
+int tee_op_vocab_loss_forward(tee_ctx* ctx, const void* d_x, const void* d_w, const int32_t* d_targets, float* d_loss,
+                              float* d_lse, int N, int V, int H, int ignore_id, void* d_ws, size_t ws_bytes,
+                              void* stream) {
+    static const char* op = "vocab_loss_forward";
+    if (!ctx) return TEE_EINVAL;
+    if (const char* what = vocab_sizes(N, V, H)) return bad(ctx, op, what);
+    if (N == 0) return TEE_OK;
+    int rc = check_bufs(ctx, op, {{"d_x", d_x, 16}, {"d_w", d_w, 16}, {"d_targets", d_targets, 4}, {"d_loss", d_loss, 4},
+                                  {"d_lse", d_lse, 4}});
+    if (rc || (rc = check_ws(ctx, op, d_ws, ws_bytes, vocab_loss_ws(N, V, H, false)))) return rc;
+    return launch(ctx, op, TEE_K_GEMM, 2.0 * N * V * H, 2.0 * ((double)N + V) * H, stream, [&](cudaStream_t s) {
+        return launch_vocab_loss_forward(d_x, d_w, d_targets, d_loss, d_lse, N, V, H, ignore_id, d_ws, ctx->d_status, s);
+    });
+}
+
+long long tee_vocab_loss_backward_workspace(int N, int V, int H) {
+    if (vocab_sizes(N, V, H)) return tee_set_global_error(TEE_EINVAL, "vocab_loss_backward_workspace: N, V or H out of range");
+    return N ? (long long)vocab_loss_ws(N, V, H, true) : 0;
+}
+
+int tee_op_vocab_loss_backward(tee_ctx* ctx, const void* d_x, const void* d_w, const int32_t* d_targets,
+                               const float* d_lse, const float* d_gloss, void* d_dx, void* d_dw, int N, int V, int H,
+                               int ignore_id, void* d_ws, size_t ws_bytes, void* stream) {
+    static const char* op = "vocab_loss_backward";
+    if (!ctx) return TEE_EINVAL;
+    if (const char* what = vocab_sizes(N, V, H)) return bad(ctx, op, what);
+    if (!d_dx && !d_dw) return bad(ctx, op, "d_dx and d_dw are both NULL");
+    int rc = TEE_OK;
+    if (d_dw && (rc = check_bufs(ctx, op, {{"d_dw", d_dw, 16}}))) return rc;
+    if (N > 0) {
+        if ((rc = check_bufs(ctx, op, {{"d_x", d_x, 16}, {"d_w", d_w, 16}, {"d_targets", d_targets, 4}, {"d_lse", d_lse, 4},
+                                       {"d_gloss", d_gloss, 4}})))
+            return rc;
+        if (d_dx && (rc = check_bufs(ctx, op, {{"d_dx", d_dx, 16}}))) return rc;
+        if ((rc = check_ws(ctx, op, d_ws, ws_bytes, vocab_loss_ws(N, V, H, true)))) return rc;
+    }
+    return launch(ctx, op, TEE_K_GEMM, 6.0 * N * V * H, 4.0 * ((double)N + V) * H, stream, [&](cudaStream_t s) {
+        return launch_vocab_loss_backward(d_x, d_w, d_targets, d_lse, d_gloss, d_dx, d_dw, N, V, H, ignore_id, d_ws,
+                                          ctx->d_status, s);
+    });
 }
 
 }  // extern "C"

@@ -159,6 +159,19 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// Descriptor of an MN-major operand of more than 64 MN elements: 64-element
+// groups laid out as below (8 K rows of 128 bytes to an atom, atoms 1024 bytes
+// apart along K), the groups `group_bytes` apart.  16 K rows are 2048 bytes.
+__device__ __forceinline__ uint64_t sw128_desc_mn_groups(uint32_t saddr, uint32_t group_bytes) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(group_bytes >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
 // Descriptor of an MN-major operand in the 128-byte swizzle layout: each
 // 128-byte row holds 64 consecutive MN elements of one K index, 8 K rows form
 // a 1024-byte atom, consecutive atoms along K are 1024 bytes apart.  (The
@@ -174,7 +187,8 @@ __device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t saddr) {
     return d;
 }
 
-// Instruction descriptor bit selecting an MN-major B operand.
+// Instruction descriptor bits selecting an MN-major A or B operand.
+constexpr uint32_t IDESC_A_MN_MAJOR = 1u << 15;
 constexpr uint32_t IDESC_B_MN_MAJOR = 1u << 16;
 
 }  // namespace tc
@@ -271,6 +285,12 @@ namespace tc {
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];"
                  ::"l"(reinterpret_cast<uint64_t>(map)), "r"(src), "r"(x), "r"(y)
+                 : "memory");
+}
+// The same, adding the fp32 box to what the tensor holds.
+__device__ __forceinline__ void tma_reduce_add_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
+    asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];"
+                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(src)
                  : "memory");
 }
 // Prefetch the tensor box at (x, y) into L2 (no shared memory, no completion).

@@ -73,3 +73,12 @@ cudaError_t launch_embed_backward(const void* dy, bool y_bf16, const int32_t* id
                                   int V, int H, float scale, bool accumulate, void* ws, unsigned int* status,
                                   cudaStream_t s);
 size_t embed_backward_ws(int T, int V, int H);
+
+// Softmax cross entropy over the vocabulary: x bf16[N, H], wt bf16[V, H], H % 8 == 0.
+cudaError_t launch_vocab_loss_forward(const void* x, const void* wt, const int32_t* targets, float* loss, float* lse, int N,
+                                      int V, int H, int ignore_id, void* ws, unsigned int* status, cudaStream_t s);
+// dx and dw may each be NULL.
+cudaError_t launch_vocab_loss_backward(const void* x, const void* wt, const int32_t* targets, const float* lse,
+                                       const float* gloss, void* dx, void* dw, int N, int V, int H, int ignore_id, void* ws,
+                                       unsigned int* status, cudaStream_t s);
+size_t vocab_loss_ws(int N, int V, int H, bool backward);
