@@ -158,7 +158,8 @@ __device__ void sort_pass(SortSmem& sm, const int32_t* __restrict__ ids, const P
             __syncwarp(live);
             if (lane == 31 - __clz(peers)) sm.hist[warp][d] = at + __popc(peers);
             __syncwarp(live);
-            out[at + __popc(peers & ((1u << lane) - 1))] = kv;
+            const uint32_t to = at + __popc(peers & ((1u << lane) - 1));
+            if (to < (uint32_t)T) out[to] = kv;   // always, unless another call writes to this workspace
         }
         __syncwarp();
     }
@@ -298,7 +299,7 @@ __global__ void __launch_bounds__(SUM_WARPS * 32)
             for (int q = 0; q < BATCH; ++q) {
                 const uint32_t k = __shfl_sync(0xffffffffu, kv.x, i0 + q), t = __shfl_sync(0xffffffffu, kv.y, i0 + q);
                 const TY* row = dy + (size_t)t * H + col0;
-                const bool ok = k < (uint32_t)V;   // false past the end as well (NO_KEY)
+                const bool ok = k < (uint32_t)V && t < (uint32_t)T;   // false past the end as well (NO_KEY)
                 if constexpr (VEC) {
                     if (ok && col0 + lane * 8 < H) load8(row + lane * 8, v[q]);
                     else

@@ -10,16 +10,15 @@
 // Work: 2 n V H flops forward, 6 n V H backward, n the counted positions.  Both
 // are bound by the tensor cores.
 //
-//   * Positions that are not counted cost nothing: their rows are left out first
-//     (vocab_rows_kernel lists the others in order, vocab_gather_kernel copies
-//     them together), and every later kernel takes their number from device
-//     memory, so nothing waits on the host.
+//   * Positions that are not counted cost nothing: vocab_rows_kernel lists the
+//     others in order and copies their states together, and every later kernel
+//     takes their number from device memory, so nothing waits on the host.
 //   * One persistent kernel of CTA pairs (tcgen05 cta_group::2, 256 x 256 tiles,
 //     K steps of 64, TMA-fed ring) runs every product.  The transposed operands
 //     (W in D W, both in D^T X) are read as they lie, as MN-major tiles.
 //   * A backward launch holds three kinds of independent tiles: D^T X and D W of
-//     one piece and the logits of the next, so there are always tiles to fill
-//     the SMs with; D is double-buffered.
+//     one piece and the logits of the next, shared out among the CTA pairs by
+//     their length (vocab_share_kernel); D is double-buffered.
 //   * D is rounded to bf16 for the tensor cores, as the states and the table are.
 //     The upstream gradients enter it divided by their largest magnitude (put
 //     back in fp32 at the end), so that a gradient that all positions share does
@@ -38,19 +37,23 @@ using namespace tc;
 
 constexpr int TILE = 256;              // rows and columns of a tile (a CTA holds 128 of the rows)
 constexpr int BK = 64;
-constexpr int NUM_THREADS = 192;
+constexpr int EPI_WARPS = 8;           // two per quarter of the accumulator's rows, 128 columns each
+constexpr int NUM_THREADS = 64 + 32 * EPI_WARPS;
+constexpr int MAX_PAIRS = 128;         // CTA pairs of a launch
 constexpr uint32_t HALF_BYTES = 128 * BK * 2;          // this CTA's half of one operand's K step
 constexpr uint32_t STAGE_BYTES = 2 * HALF_BYTES;
 constexpr int STAGES = 6;
-constexpr uint32_t OUT_OFF = STAGES * STAGE_BYTES;     // two 4 KB staging boxes per epilogue warp
-constexpr uint32_t BAR_OFF = OUT_OFF + 4 * 2 * 4096;
-constexpr int N_BARS = 2 * STAGES + 5;
+constexpr uint32_t OUT_OFF = STAGES * STAGE_BYTES;     // a 4 KB staging box per epilogue warp
+constexpr uint32_t BAR_OFF = OUT_OFF + EPI_WARPS * 4096;
+constexpr int N_BARS = 2 * STAGES + 5 + 16;
 constexpr uint32_t SMEM_BYTES = BAR_OFF + N_BARS * 8 + 16 + 1024;   // + alignment slack
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
 constexpr uint32_t TMEM_COLS = 512;    // two accumulators of 256 columns
 constexpr float LOG2E = 1.4426950408889634f;
+// A tile's epilogue, in K steps of products.
+constexpr int EPILOGUE_K_STEPS = 6;
 
-// What the rows and gather kernels prepare, and the kernels after them read.
+// What vocab_rows_kernel prepares, and the kernels after it read.
 struct Rows {
     int* count;             // counted positions
     float* gmax;            // largest finite magnitude of their upstream gradients, 1 if that is 0 (backward)
@@ -66,34 +69,37 @@ struct Rows {
 // before the products
 // ---------------------------------------------------------------------------
 
-// Lists the counted positions.  One block: each warp counts its slice, then
-// writes it behind the slices before it.  Forward (gloss NULL) also zeroes the
-// outputs of the positions that are not counted.
-__global__ void __launch_bounds__(1024) vocab_rows_kernel(const int32_t* __restrict__ targets, int N, int V, int ignore_id,
-                                                          const float* __restrict__ gloss, float* loss, float* lse, Rows r,
-                                                          unsigned int* status) {
-    __shared__ int warp_n[32];
-    __shared__ float warp_g[32];
+// Lists the counted positions and copies their states together.  Each block has
+// a slice of the positions; it counts what is counted before its slice by
+// itself, so that no block waits for another (the targets are a few hundred KB
+// out of L2).  The last block also writes their number and zeroes the rest of
+// the last tile.  Forward (gloss NULL) zeroes the outputs of the positions that
+// are not counted; backward divides the upstream gradients by the largest.
+constexpr int ROWS_THREADS = 512, ROWS_WARPS = ROWS_THREADS / 32;
+__global__ void __launch_bounds__(ROWS_THREADS)
+    vocab_rows_kernel(const bf16* __restrict__ x, const int32_t* __restrict__ targets, const float* __restrict__ lse_in,
+                      const float* __restrict__ gloss, int N, int V, int H, int ignore_id, int slice, float* loss, float* lse,
+                      Rows r, unsigned int* status) {
+    __shared__ int warp_n[ROWS_WARPS];
+    __shared__ float warp_g[ROWS_WARPS];
     pdl_wait();
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int slice = ((N + 1023) / 1024) * 32;
-    const int lo = min(N, warp * slice), hi = min(N, lo + slice);
+    const int lo = blockIdx.x * slice, hi = min(N, lo + slice);
+    auto counted = [&](int t) { return t >= 0 && t < V && t != ignore_id; };
+    // the counted positions before the slice, and (backward) the largest gradient of all
     int n = 0;
     float g = 0.f;
-    bool out_of_range = false;
-#pragma unroll 4
-    for (int i = lo + lane; i < hi; i += 32) {
-        const int t = targets[i];
-        const bool live = t >= 0 && t < V && t != ignore_id;
-        out_of_range |= !live && t != ignore_id;
-        n += live;
-        if (live && gloss) {
+    const int upto = gloss ? N : lo;
+#pragma unroll 8
+    for (int i = threadIdx.x; i < upto; i += ROWS_THREADS) {
+        const bool live = counted(targets[i]);
+        n += live && i < lo;
+        if (gloss) {
             const float a = fabsf(gloss[i]);
-            if (a < INFINITY) g = fmaxf(g, a);
+            if (live && a < INFINITY) g = fmaxf(g, a);
         }
     }
-    if (out_of_range) atomicOr(status, TEE_STATUS_BAD_ID);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         n += __shfl_xor_sync(0xffffffffu, n, o);
@@ -102,49 +108,70 @@ __global__ void __launch_bounds__(1024) vocab_rows_kernel(const int32_t* __restr
     if (lane == 0) warp_n[warp] = n, warp_g[warp] = g;
     __syncthreads();
     int at = 0;
-    for (int w = 0; w < warp; ++w) at += warp_n[w];
-    if (threadIdx.x == 1023) *r.count = at + n;
-    if (threadIdx.x == 0 && gloss) {
-        for (int w = 0; w < 32; ++w) g = fmaxf(g, warp_g[w]);
-        *r.gmax = g > 0.f ? g : 1.f;
-    }
-    for (int i0 = lo; i0 < hi; i0 += 32) {
-        const int i = i0 + lane;
+#pragma unroll
+    for (int w = 0; w < ROWS_WARPS; ++w) at += warp_n[w], g = fmaxf(g, warp_g[w]);
+    const float gmax = g > 0.f ? g : 1.f;
+    __syncthreads();
+    for (int i0 = lo; i0 < hi; i0 += ROWS_THREADS) {   // (uniform: the block's barriers are inside)
+        const int i = i0 + threadIdx.x;
         const int t = i < hi ? targets[i] : ignore_id;
-        const bool live = i < hi && t >= 0 && t < V && t != ignore_id;
+        const bool live = counted(t);
+        if (!live && t != ignore_id) atomicOr(status, TEE_STATUS_BAD_ID);
         const unsigned m = __ballot_sync(0xffffffffu, live);
-        const int place = at + __popc(m & ((1u << lane) - 1));
-        if (live) r.list[place] = i;
-        if (gloss) {
-            if (i < hi) r.index[i] = live ? place : -1;
-        } else if (i < hi && !live) {
-            loss[i] = 0.f;
-            lse[i] = 0.f;
+        if (lane == 0) warp_n[warp] = __popc(m);
+        __syncthreads();
+        int place = at + __popc(m & ((1u << lane) - 1));
+#pragma unroll
+        for (int w = 0; w < ROWS_WARPS; ++w) {
+            place += w < warp ? warp_n[w] : 0;
+            at += warp_n[w];
         }
-        at += __popc(m);
+        if (live) {
+            r.list[place] = i;
+            r.target[place] = t;
+            if (gloss) {
+                r.lse2[place] = lse_in[i] * LOG2E;
+                r.ratio[place] = gloss[i] / gmax;
+            }
+        }
+        if (i < hi) {
+            if (gloss) r.index[i] = live ? place : -1;
+            else if (!live) loss[i] = lse[i] = 0.f;
+        }
+        // each warp copies the states of its own 32 positions, four at a time
+        const int first = __shfl_sync(0xffffffffu, place - __popc(m & ((1u << lane) - 1)), 0);
+        unsigned left = m;
+        for (int c = first; left; c += 4) {
+            int from[4];
+            const int rows = min(4, __popc(left));
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                from[q] = left ? i0 + warp * 32 + __ffs(left) - 1 : 0;
+                left &= left - 1;
+            }
+            for (int k = lane; k < H / 8; k += 32) {
+                uint4 v[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (q < rows) v[q] = reinterpret_cast<const uint4*>(x + (size_t)from[q] * H)[k];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (q < rows) reinterpret_cast<uint4*>(r.x + (size_t)(c + q) * H)[k] = v[q];
+            }
+        }
+        __syncthreads();
     }
-}
-
-// Copies the listed rows together, one warp per row, and zeroes the rest of the last tile.
-__global__ void __launch_bounds__(256) vocab_gather_kernel(const bf16* __restrict__ x, const int32_t* __restrict__ targets,
-                                                           const float* __restrict__ lse, const float* __restrict__ gloss,
-                                                           int H, Rows r) {
-    pdl_wait();
-    pdl_trigger();
-    const int c = (blockIdx.x * 256 + threadIdx.x) >> 5, lane = threadIdx.x & 31;
-    const int n = *r.count;
-    if (c >= (n + TILE - 1) / TILE * TILE) return;
-    const bool live = c < n;
-    const int i = live ? r.list[c] : 0;
-    const uint4* src = reinterpret_cast<const uint4*>(x + (size_t)i * H);
-    uint4* dst = reinterpret_cast<uint4*>(r.x + (size_t)c * H);
-#pragma unroll 4
-    for (int k = lane; k < H / 8; k += 32) dst[k] = live ? src[k] : make_uint4(0, 0, 0, 0);
-    if (lane == 0) {
-        r.target[c] = live ? targets[i] : -1;
-        if (gloss) {
-            r.lse2[c] = live ? lse[i] * LOG2E : 0.f;
-            r.ratio[c] = live ? gloss[i] / *r.gmax : 0.f;
+    if (blockIdx.x != gridDim.x - 1) return;
+    if (threadIdx.x == 0) {
+        *r.count = at;
+        if (gloss) *r.gmax = gmax;
+    }
+    const int end = (at + TILE - 1) / TILE * TILE;
+    for (int c = at + warp; c < end; c += ROWS_WARPS) {
+        for (int k = lane; k < H / 8; k += 32) reinterpret_cast<uint4*>(r.x + (size_t)c * H)[k] = make_uint4(0, 0, 0, 0);
+        if (lane == 0) {
+            r.target[c] = -1;
+            if (gloss) r.lse2[c] = r.ratio[c] = 0.f;
         }
     }
 }
@@ -162,6 +189,8 @@ struct Maps {
     CUtensorMap d_out, dx_acc, dw;  // outputs: boxes of 32 rows x 128 bytes
 };
 
+struct Share;
+
 struct Params {
     Rows r;
     int V, H, Np;
@@ -175,68 +204,164 @@ struct Params {
     int want_dx, want_dw;
     int acc_rows;                   // rows of the dX accumulators
     int first;                      // dX is written, not added to
+    const Share* shares;            // the pairs' shares of this launch (backward)
     unsigned int* status;
 };
 
 // How many slices of a piece's columns the tiles of D W are split into, each
-// with accumulators of its own: enough tiles for two per CTA pair, as far as the
-// accumulators reach and a slice has at least four K steps.
+// with accumulators of its own: as many as give every CTA pair at most one
+// tile, as far as the accumulators reach and a slice has at least four K steps.
 __device__ __forceinline__ int dx_slices(int mt, int ht, int pairs, int acc_rows, int n_mul) {
-    const int want = (2 * pairs + mt * ht - 1) / (mt * ht);
-    return max(1, min(min(want, acc_rows / (mt * TILE)), n_mul / (4 * BK)));
+    return max(1, min(min(pairs / (mt * ht), acc_rows / (mt * TILE)), n_mul / (4 * BK)));
 }
 
 struct Unit {
     int kind, m, n, k0, num_k, slice;   // tile (m, n); K steps k0 .. k0 + num_k
 };
 
-// The launch's units: D^T X and D W (the longer first), then the logits, whose
-// short tiles even out what the long ones leave.
-struct Plan {
-    int mt, ht, n_dw, n_dx, n_log, slices, k_slice, k_rows, k_mul, kh;
-    bool dx_first;
-    template <bool BWD>
-    static __device__ __forceinline__ Plan make(const Params& p, int count, int pairs) {
-        Plan q;
+// The tiles of one launch.
+struct Tiles {
+    int mt, ht, n_dw, n_dx, n_log, k_slice, k_rows, k_mul, kh;
+    static __device__ __forceinline__ Tiles of(int count, int H, int n_log, int n_mul, bool want_dx, bool want_dw, int pairs,
+                                               int acc_rows) {
+        Tiles q;
         q.mt = (count + TILE - 1) / TILE;
-        q.ht = (p.H + TILE - 1) / TILE;
-        q.kh = (p.H + BK - 1) / BK;
-        q.n_log = q.mt * ((p.n_log + TILE - 1) / TILE);
-        q.n_dw = q.n_dx = 0;
-        q.slices = 1;
-        q.k_slice = q.k_rows = q.k_mul = 0;
-        q.dx_first = false;
-        if (BWD && p.n_mul) {
-            q.k_rows = (count + BK - 1) / BK;
-            q.k_mul = (p.n_mul + BK - 1) / BK;
-            if (p.want_dw) q.n_dw = (p.n_mul + TILE - 1) / TILE * q.ht;
-            if (p.want_dx && q.mt) {
-                q.slices = dx_slices(q.mt, q.ht, pairs, p.acc_rows, p.n_mul);
-                q.k_slice = (q.k_mul + q.slices - 1) / q.slices;
-                q.n_dx = q.mt * q.ht * q.slices;
-            }
-            q.dx_first = q.k_slice > q.k_rows;
+        q.ht = (H + TILE - 1) / TILE;
+        q.kh = (H + BK - 1) / BK;
+        q.n_log = q.mt * ((n_log + TILE - 1) / TILE);
+        q.k_rows = (count + BK - 1) / BK;
+        q.k_mul = (n_mul + BK - 1) / BK;
+        q.n_dw = want_dw ? (n_mul + TILE - 1) / TILE * q.ht : 0;
+        q.n_dx = q.k_slice = 0;
+        if (want_dx && n_mul && q.mt) {
+            const int slices = dx_slices(q.mt, q.ht, pairs, acc_rows, n_mul);
+            q.k_slice = (q.k_mul + slices - 1) / slices;
+            q.n_dx = q.mt * q.ht * slices;
         }
         return q;
     }
-    __device__ __forceinline__ int units() const { return n_dw + n_dx + n_log; }
-    template <bool BWD>
-    __device__ __forceinline__ Unit unit(int u) const {
-        if constexpr (BWD) {
-            const int a = dx_first ? n_dx : n_dw;
-            if (u < n_dw + n_dx) {
-                const bool dx = (u < a) == dx_first;
-                if (u >= a) u -= a;
-                const int n = u % ht, rest = u / ht;
-                if (!dx) return Unit{DW, rest, n, 0, k_rows, 0};
-                const int s = rest / mt, k0 = s * k_slice;
-                return Unit{DX, rest % mt, n, k0, max(0, min(k_slice, k_mul - k0)), s};
-            }
-            u -= n_dw + n_dx;
-        }
-        return Unit{LOGITS, u % mt, u / mt, 0, kh, 0};
+    __device__ __forceinline__ Unit unit(int kind, int u) const {
+        if (kind == LOGITS) return Unit{LOGITS, u % mt, u / mt, 0, kh, 0};
+        const int n = u % ht, rest = u / ht;
+        if (kind == DW) return Unit{DW, rest, n, 0, k_rows, 0};
+        const int s = rest / mt, k0 = s * k_slice;
+        return Unit{DX, rest % mt, n, k0, max(0, min(k_slice, k_mul - k0)), s};
     }
 };
+
+// A CTA pair's share of a backward launch: of each kind the units [first, first + n).
+struct Share {
+    int first[3], n[3];   // by Kind
+};
+
+// The units a CTA pair takes, in the order it takes them: D W and D^T X, the
+// longer of them first, then logits.  Forward: every pairs-th tile.
+template <bool BWD>
+struct Walk {
+    int pos, end, step;
+    Share share;
+    int order[3];
+    __device__ __forceinline__ Walk(const Tiles& t, const Share* shares, int pair, int pairs) {
+        if constexpr (BWD) {
+            share = shares[pair];
+            const int units[3] = {t.n_log, t.n_dx, t.n_dw};
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                share.first[k] = min(max(share.first[k], 0), units[k]);
+                share.n[k] = min(max(share.n[k], 0), units[k] - share.first[k]);
+            }
+            const bool dx_first = t.k_slice > t.k_rows;
+            order[0] = dx_first ? DX : DW;
+            order[1] = dx_first ? DW : DX;
+            order[2] = LOGITS;
+            pos = 0, step = 1, end = share.n[0] + share.n[1] + share.n[2];
+        } else {
+            pos = pair, step = pairs, end = t.n_log;
+        }
+    }
+    __device__ __forceinline__ bool done() const { return pos >= end; }
+    __device__ __forceinline__ Unit next(const Tiles& t) {
+        int u = pos;
+        pos += step;
+        if constexpr (!BWD) return t.unit(LOGITS, u);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int k = order[i], n = k == DX ? share.n[DX] : share.n[DW];
+            if (u < n) return t.unit(k, (k == DX ? share.first[DX] : share.first[DW]) + u);
+            u -= n;
+        }
+        return t.unit(LOGITS, share.first[LOGITS] + u);
+    }
+};
+
+// Shares of every backward launch, one warp each: launch i computes the logits
+// of piece i and multiplies D of piece i - 1.  Kind by kind, the longest units
+// first, each unit goes to the pair with the least work so far -- computed for
+// all units of a kind at once: the level X is searched up to which the pairs
+// fill (a pair takes units while its work is below X), and what is left goes to
+// pairs that stand at X exactly.
+__global__ void __launch_bounds__(32) vocab_share_kernel(Rows r, int N, int V, int H, int piece, int pieces, int want_dx, int want_dw,
+                                                         int pairs, int acc_rows, Share* shares) {
+    pdl_wait();
+    pdl_trigger();
+    constexpr int PER = MAX_PAIRS / 32;   // pair j * 32 + lane
+    const int i = blockIdx.x, lane = threadIdx.x;
+    const int n_log = i < pieces ? min(piece, V - i * piece) : 0;
+    const int n_mul = i > 0 ? min(piece, V - (i - 1) * piece) : 0;
+    const Tiles t = Tiles::of(min(max(*r.count, 0), N), H, n_log, n_mul, want_dx, want_dw, pairs, acc_rows);
+    const bool dx_first = t.k_slice > t.k_rows;
+    int load[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) load[j] = j * 32 + lane < pairs ? 0 : INT32_MAX;
+    auto sum = [](int v) { return __reduce_add_sync(0xffffffffu, v); };
+#pragma unroll 1
+    for (int q = 0; q < 3; ++q) {
+        const int kind = q == 2 ? LOGITS : (q == 0) == dx_first ? DX : DW;
+        const int units = kind == LOGITS ? t.n_log : kind == DX ? t.n_dx : t.n_dw;
+        // a unit's time in K steps: its products, or its epilogue where that is longer
+        const int cost = max(kind == LOGITS ? t.kh : kind == DX ? t.k_slice : t.k_rows, EPILOGUE_K_STEPS);
+        auto taken = [&](int x, int j) { return load[j] < x ? (x - load[j] + cost - 1) / cost : 0; };
+        int top = 0;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) top = max(top, load[j] == INT32_MAX ? 0 : load[j]);
+        top = __reduce_max_sync(0xffffffffu, top);
+        // at lo the pairs take at most `units` units, at hi more
+        long long lo = 0, hi = (long long)top + (long long)(units / pairs + 1) * cost + 1;
+        while (hi - lo > 1) {
+            const int mid = (int)((lo + hi) / 2);
+            int f = 0;
+#pragma unroll
+            for (int j = 0; j < PER; ++j) f += taken(mid, j);
+            if (sum(f) <= units) lo = mid;
+            else hi = mid;
+        }
+        int k[PER], f = 0;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) f += k[j] = taken((int)lo, j);
+        int left = units - sum(f);
+        int first = 0;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const bool at = load[j] != INT32_MAX && load[j] + k[j] * cost == (int)lo;
+            const unsigned m = __ballot_sync(0xffffffffu, at);
+            if (at && __popc(m & ((1u << lane) - 1)) < left) ++k[j];
+            left -= min(left, __popc(m));
+            int inc = k[j];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += up;
+            }
+            if (j * 32 + lane < pairs) {
+                Share& s = shares[i * pairs + j * 32 + lane];
+                s.first[kind] = first + inc - k[j];
+                s.n[kind] = k[j];
+                load[j] += k[j] * cost;
+            }
+            first += __shfl_sync(0xffffffffu, inc, 31);
+        }
+    }
+}
 
 template <bool BWD>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
@@ -248,7 +373,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + N_BARS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     auto bar = [&](int i) { return smem_u32(bars + i); };
-    constexpr int FULL = 0, EMPTY = STAGES, TFULL = 2 * STAGES, TEMPTY = 2 * STAGES + 2, MMA_DONE = 2 * STAGES + 4;
+    constexpr int FULL = 0, EMPTY = STAGES, TFULL = 2 * STAGES, TEMPTY = 2 * STAGES + 2, MMA_DONE = 2 * STAGES + 4,
+                  JOIN = 2 * STAGES + 5;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t crank = cluster_ctarank();
     auto lead_bar = [&](int i) { return mapa_shared(bar(i), 0); };   // the even CTA's, which both CTAs signal
@@ -260,9 +386,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(bar(TFULL + a), 1);
-            mbar_init(bar(TEMPTY + a), 256);   // every epilogue thread of both CTAs
+            mbar_init(bar(TEMPTY + a), 2 * 32 * EPI_WARPS);   // every epilogue thread of both CTAs
         }
         mbar_init(bar(MMA_DONE), 1);
+        for (int j = 0; j < 16; ++j) mbar_init(bar(JOIN + j), 32);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -275,10 +402,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     pdl_wait();
     pdl_trigger();
 
-    const int count = __ldcg(p.r.count);
-    const int unit0 = blockIdx.x / 2, ustride = gridDim.x / 2;
-    const Plan plan = Plan::make<BWD>(p, count, ustride);
-    const int num_units = plan.units();
+    // (what comes out of the workspace is kept within its arrays, so that a
+    // workspace that another call writes to gives wrong numbers and no stray access)
+    const int count = min(max(__ldcg(p.r.count), 0), p.Np);
+    const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+    const Tiles tiles = Tiles::of(count, p.H, p.n_log, p.n_mul, p.want_dx, p.want_dw, pairs, p.acc_rows);
+    Walk<BWD> walk(tiles, p.shares, pair, pairs);
 
     if (warp == 0) {
         // ---------------- TMA producer ----------------
@@ -287,8 +416,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
             bool armed[STAGES], ok = true;
             uint32_t armed_parity[STAGES];
             for (int s = 0; s < STAGES; ++s) armed[s] = false, armed_parity[s] = 0;
-            for (int u = unit0; u < num_units && ok; u += ustride) {
-                const Unit w = plan.unit<BWD>(u);
+            while (ok && !walk.done()) {
+                const Unit w = walk.next(tiles);
                 const int a0 = w.m * TILE + (int)crank * 128, b0 = w.n * TILE + (int)crank * 128;
                 for (int kb = 0; kb < w.num_k; ++kb, ++g) {
                     const int s = g % STAGES;
@@ -331,8 +460,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
             uint32_t g = 0;
             int it = 0;
             bool ok = true;
-            for (int u = unit0; u < num_units && ok; u += ustride, ++it) {
-                const Unit w = plan.unit<BWD>(u);
+            for (; ok && !walk.done(); ++it) {
+                const Unit w = walk.next(tiles);
                 const int acc = it & 1, use = it >> 1;
                 if (!mbar_wait_cluster(bar(TEMPTY + acc), (use & 1) ^ 1, abort_flag)) {
                     ok = false;
@@ -368,128 +497,145 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         }
         __syncwarp();
     } else {
-        // ---------------- epilogue (warps 2..5): thread = row of the accumulator ----------------
-        const int quad = warp & 3;
-        uint8_t* stage = smem + OUT_OFF + (warp - 2) * 8192;   // this warp's two staging boxes
-        uint32_t n_stores = 0;
-        auto box = [&]() {   // the next box, free to be written
-            if (lane == 0 && n_stores >= 2) bulk_wait_read<1>();
+        // ---------------- epilogue: thread = row, warps 2..5 columns 0..127, warps 6..9 the others ----------------
+        const int quad = warp & 3, half = (warp - 2) >> 2;
+        uint8_t* stage = smem + OUT_OFF + (warp - 2) * 4096;   // this warp's staging box
+        auto box_free = [&]() {   // the box's last store has read it
+            if (lane == 0) bulk_wait_read<0>();
             __syncwarp();
-            return stage + (n_stores & 1) * 4096;
         };
         auto send = [&](auto&& issue) {   // lane 0 stores the box just written
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                issue(smem_u32(stage + (n_stores & 1) * 4096));
+                issue(smem_u32(stage));
                 bulk_commit();
             }
-            ++n_stores;
         };
         const float gmax = BWD ? __ldcg(p.r.gmax) : 0.f;
-        int it = 0;
-        for (int u = unit0; u < num_units; u += ustride, ++it) {
-            const Unit w = plan.unit<BWD>(u);
+        for (int it = 0; !walk.done(); ++it) {
+            const Unit w = walk.next(tiles);
             const int acc = it & 1, use = it >> 1;
             const int row0 = w.m * TILE + (int)crank * 128 + quad * 32, row = row0 + lane;
-            const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + acc * TILE;
+            const int col0 = w.n * TILE + half * 128;          // this warp's first column of the output
+            const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + acc * TILE + half * 128;
+            // what the row needs, fetched while the products run
+            float lse2 = 0.f, ratio = 0.f;
+            int target = -1;
+            if (!BWD || w.kind == LOGITS) {
+                target = p.r.target[row] - p.v_log - col0;     // within this warp's columns, if it is there
+                if (BWD) lse2 = p.r.lse2[row], ratio = p.r.ratio[row];
+            }
+            if (!mbar_wait(bar(TFULL + acc), use & 1, abort_flag)) break;
+            tc_fence_after();
+            // the accumulator is free once both loads are in registers
+            float v[2][64];
+            tmem_ld64_issue(taddr, v[0]);
+            tmem_ld64_issue(taddr + 64, v[1]);
+            tmem_wait_ld();
+            tmem_tie64(v[0]);
+            tmem_tie64(v[1]);
+            tc_fence_before();
+            mbar_arrive_cluster(lead_bar(TEMPTY + acc));
             if constexpr (!BWD) {
-                const int target = p.r.target[row] - w.n * TILE;   // within this tile's columns, if it is there
-                if (!mbar_wait(bar(TFULL + acc), use & 1, abort_flag)) break;
-                tc_fence_after();
                 float top = -INFINITY, ref = -INFINITY, sum = 0.f;
-#pragma unroll 1
-                for (int c = 0; c < TILE; c += 64) {
-                    float v[64];
-                    tmem_ld64(taddr + c, v);
-                    if (w.n * TILE + c + 64 > p.V) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    if (col0 + 64 * c + 64 > p.V) {
 #pragma unroll
                         for (int j = 0; j < 64; ++j)
-                            if (w.n * TILE + c + j >= p.V) v[j] = -INFINITY;
+                            if (col0 + 64 * c + j >= p.V) v[c][j] = -INFINITY;
                     }
-                    const int tj = target - c;
+                    const int tj = target - 64 * c;
                     if (__any_sync(0xffffffffu, tj >= 0 && tj < 64)) {
                         float tv = 0.f;
 #pragma unroll
-                        for (int j = 0; j < 64; ++j) tv = j == tj ? v[j] : tv;
+                        for (int j = 0; j < 64; ++j) tv = j == tj ? v[c][j] : tv;
                         if (tj >= 0 && tj < 64) p.target_logit[row] = tv;
                     }
-                    float mx[4] = {v[0], v[1], v[2], v[3]};
+                    float mx[4] = {v[c][0], v[c][1], v[c][2], v[c][3]};
 #pragma unroll
-                    for (int j = 4; j < 64; ++j) mx[j & 3] = fmaxf(mx[j & 3], v[j]);
+                    for (int j = 4; j < 64; j += 8)   // (the last step's upper half repeats its lower one)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) mx[q] = fmax3(mx[q], v[c][j + q], v[c][j + 4 < 64 ? j + 4 + q : j + q]);
                     top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-                    // exponentials are taken against the running maximum; one that is
-                    // infinite would give NaN where the sum is 0 or infinite
-                    const float to = isinf(top) ? 0.f : top * LOG2E;
-                    sum *= ex2_approx(ref - to);
-                    float s4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int j = 0; j < 64; ++j) s4[j & 3] += ex2_approx(fmaf(v[j], LOG2E, -to));
-                    sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
-                    ref = top == -INFINITY ? -INFINITY : to;
                 }
-                if (row < count) p.part[(size_t)w.n * p.Np + row] = make_float2(ref, sum);
-            } else if (w.kind == LOGITS) {
-                const float lse2 = p.r.lse2[row], ratio = p.r.ratio[row];
-                const int target = p.r.target[row] - p.v_log - w.n * TILE;
-                if (!mbar_wait(bar(TFULL + acc), use & 1, abort_flag)) break;
-                tc_fence_after();
-#pragma unroll 1
-                for (int c = 0; c < TILE; c += 64) {
-                    float v[64];
-                    tmem_ld64(taddr + c, v);
+                // exponentials are taken against the maximum; one that is infinite would give NaN
+                const float to = isinf(top) ? 0.f : top * LOG2E;
+                float s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int j = 0; j < 64; ++j) v[j] = ex2_approx(fmaf(v[j], LOG2E, -lse2));
-                    const int tj = target - c;
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) s4[j & 3] += ex2_approx(fmaf(v[c][j], LOG2E, -to));
+                sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+                ref = top == -INFINITY ? -INFINITY : to;
+                // the two warps of a row join through shared memory.  Four slots: a
+                // slot comes round again after its tile's fourth successor has been
+                // multiplied, which waits for this row's warps to have left the second
+                const int slot = it & 3, joined = JOIN + quad * 4 + slot;
+                float2* other = reinterpret_cast<float2*>(smem + OUT_OFF) + slot * 128 + quad * 32 + lane;
+                if (half) {
+                    *other = make_float2(ref, sum);
+                    mbar_arrive(bar(joined));
+                } else {
+                    if (!mbar_wait(bar(joined), (it >> 2) & 1, abort_flag)) break;
+                    const float2 o = *other;
+                    const float both = fmaxf(ref, o.x);
+                    if (both != -INFINITY) sum = sum * ex2_approx(ref - both) + o.y * ex2_approx(o.x - both);
+                    else sum += o.y;
+                    if (row < count) p.part[(size_t)w.n * p.Np + row] = make_float2(both, sum);
+                }
+            } else if (w.kind == LOGITS) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) v[c][j] = ex2_approx(fmaf(v[c][j], LOG2E, -lse2));
+                    const int tj = target - 64 * c;
                     if (__any_sync(0xffffffffu, tj >= 0 && tj < 64)) {
 #pragma unroll
-                        for (int j = 0; j < 64; ++j) v[j] -= j == tj ? 1.f : 0.f;
+                        for (int j = 0; j < 64; ++j) v[c][j] -= j == tj ? 1.f : 0.f;
                     }
                     // rows of padding are zero whatever the table holds
 #pragma unroll
-                    for (int j = 0; j < 64; ++j) v[j] = row < count ? v[j] * ratio : 0.f;
-                    stage_row_bf16x64(box(), lane, v);
-                    send([&](uint32_t src) { tma_store_2d(&maps.d_out, src, w.n * TILE + c, row0); });
+                    for (int j = 0; j < 64; ++j) v[c][j] = row < count ? v[c][j] * ratio : 0.f;
+                    box_free();
+                    stage_row_bf16x64(stage, lane, v[c]);
+                    send([&](uint32_t src) { tma_store_2d(&maps.d_out, src, col0 + 64 * c, row0); });
                 }
             } else if (w.kind == DX) {
-                if (!mbar_wait(bar(TFULL + acc), use & 1, abort_flag)) break;
-                tc_fence_after();
-                const int y = w.slice * plan.mt * TILE + row0;
-#pragma unroll 1
-                for (int c = 0; c < TILE; c += 32) {
-                    const int x = w.n * TILE + c;
-                    if (x >= p.H) break;
-                    float v[32];
-                    tmem_ld32(taddr + c, v);
-                    uint8_t* b = box() + lane * 128;
+                const int y = w.slice * tiles.mt * TILE + row0;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        *reinterpret_cast<float4*>(b + ((k ^ (lane & 7)) << 4)) =
-                            w.num_k ? make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
-                    // each element is added to once a launch: the order of the sums is fixed
-                    send([&](uint32_t src) {
-                        if (p.first) tma_store_2d(&maps.dx_acc, src, x, y);
-                        else tma_reduce_add_2d(&maps.dx_acc, src, x, y);
-                    });
+                for (int c = 0; c < 4; ++c) {
+                    const int x = col0 + 32 * c;
+                    if (x < p.H) {
+                        const float* a = v[c >> 1] + 32 * (c & 1);
+                        box_free();
+                        uint8_t* b = stage + lane * 128;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            *reinterpret_cast<float4*>(b + ((k ^ (lane & 7)) << 4)) =
+                                w.num_k ? make_float4(a[4 * k], a[4 * k + 1], a[4 * k + 2], a[4 * k + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        // each element is added to once a launch: the order of the sums is fixed
+                        send([&](uint32_t src) {
+                            if (p.first) tma_store_2d(&maps.dx_acc, src, x, y);
+                            else tma_reduce_add_2d(&maps.dx_acc, src, x, y);
+                        });
+                    }
                 }
             } else {
-                if (!mbar_wait(bar(TFULL + acc), use & 1, abort_flag)) break;
-                tc_fence_after();
                 const int y = p.v_mul + row0;
-#pragma unroll 1
-                for (int c = 0; c < TILE; c += 64) {
-                    const int x = w.n * TILE + c;
-                    if (x >= p.H) break;
-                    float v[64];
-                    tmem_ld64(taddr + c, v);
 #pragma unroll
-                    for (int j = 0; j < 64; ++j) v[j] = w.num_k ? v[j] * gmax : 0.f;
-                    stage_row_bf16x64(box(), lane, v);
-                    if (y < p.V) send([&](uint32_t src) { tma_store_2d(&maps.dw, src, x, y); });
+                for (int c = 0; c < 2; ++c) {
+                    const int x = col0 + 64 * c;
+                    if (x < p.H && y < p.V) {
+#pragma unroll
+                        for (int j = 0; j < 64; ++j) v[c][j] = w.num_k ? v[c][j] * gmax : 0.f;
+                        box_free();
+                        stage_row_bf16x64(stage, lane, v[c]);
+                        send([&](uint32_t src) { tma_store_2d(&maps.dw, src, x, y); });
+                    }
                 }
             }
-            tc_fence_before();
-            mbar_arrive_cluster(lead_bar(TEMPTY + acc));
         }
         if (lane == 0) bulk_wait_all();   // stores complete before the CTA exits
     }
@@ -514,13 +660,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
 // lse and loss of the counted positions from the tiles' pairs: 32 rows by 16
 // slices of the tiles per block; the last step in 64 bits.
 __global__ void __launch_bounds__(512) vocab_finish_kernel(const float2* __restrict__ part, const float* __restrict__ target_logit,
-                                                           Rows r, int tiles, int Np, float* __restrict__ loss,
-                                                           float* __restrict__ lse) {
+                                                           Rows r, int tiles, int N, int Np,
+                                                           float* __restrict__ loss, float* __restrict__ lse) {
     __shared__ float2 red[16][32];
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, sl = threadIdx.x >> 5;
-    const int row = blockIdx.x * 32 + lane, n = *r.count;
+    const int row = blockIdx.x * 32 + lane, n = min(*r.count, N);
     if (blockIdx.x * 32 >= n) return;
     float2 a = make_float2(-INFINITY, 0.f);
     auto join = [](float2 a, float2 b) {
@@ -538,6 +684,7 @@ __global__ void __launch_bounds__(512) vocab_finish_kernel(const float2* __restr
     for (int s = 1; s < 16; ++s) a = join(a, red[s][lane]);
     const double l = ((double)a.x + log2((double)a.y)) * 0.69314718055994530942;
     const int i = r.list[row];
+    if ((unsigned)i >= (unsigned)N) return;
     lse[i] = (float)l;
     loss[i] = (float)(l - (double)target_logit[row]);
 }
@@ -550,9 +697,9 @@ __global__ void __launch_bounds__(256) vocab_scatter_kernel(const float* __restr
     pdl_trigger();
     const int i = (blockIdx.x * 256 + threadIdx.x) >> 5, lane = threadIdx.x & 31;
     if (i >= N) return;
-    const int at = r.index[i];
     const float gmax = *r.gmax;
-    const int mt = (*r.count + TILE - 1) / TILE;
+    const int n = min(max(*r.count, 0), N), mt = (n + TILE - 1) / TILE;
+    const int at = min(r.index[i], n - 1);
     const int slices = at < 0 ? 0 : dx_slices(mt, (H + TILE - 1) / TILE, pairs, acc_rows, n_mul);
     for (int k = lane; k < H / 8; k += 32) {
         float v[8] = {};
@@ -591,6 +738,7 @@ struct LossWs {
     float* target_logit = nullptr;
     bf16* d[2] = {nullptr, nullptr};
     float* acc = nullptr;
+    Share* shares = nullptr;
     size_t bytes = 0;
 };
 LossWs carve_loss(int N, int V, int H, bool backward, void* base) {
@@ -612,6 +760,7 @@ LossWs carve_loss(int N, int V, int H, bool backward, void* base) {
         const int vc = piece_columns(Np, V);
         for (int b = 0; b < (vc < V ? 2 : 1); ++b) w.d[b] = ws.take<bf16>((size_t)Np * vc);
         w.acc = ws.take<float>((size_t)accumulator_rows(Np, H) * H);
+        w.shares = ws.take<Share>((size_t)((V + vc - 1) / vc + 1) * MAX_PAIRS);
     }
     w.bytes = ws.off;
     return w;
@@ -638,7 +787,7 @@ cudaError_t max_pairs(int dev, int num_sms, int* pairs) {
         int n = 0;
         e = cudaOccupancyMaxActiveClusters(&n, vocab_kernel<BWD>, &cfg);
         if (e != cudaSuccess) return e;
-        of[dev] = std::max(1, n);
+        of[dev] = std::min(std::max(1, n), MAX_PAIRS);
     }
     *pairs = of[dev];
     return cudaSuccess;
@@ -652,9 +801,10 @@ cudaError_t max_pairs(int dev, int num_sms, int* pairs) {
 
 cudaError_t prepare_rows(const void* x, const int32_t* targets, const float* lse_in, const float* gloss, float* loss,
                          float* lse, int N, int V, int H, int ignore_id, const LossWs& w, unsigned int* status, cudaStream_t s) {
-    TRY(launch_pdl(vocab_rows_kernel, dim3(1), dim3(1024), 0, s, targets, N, V, ignore_id, gloss, loss, lse, w.r, status));
-    return launch_pdl(vocab_gather_kernel, dim3(round_up(N, TILE) / 8), dim3(256), 0, s, (const bf16*)x, targets, lse_in, gloss,
-                      H, w.r);
+    // a slice for each of 148 blocks, whole block steps at least
+    const int slice = round_up(std::max(1, (N + 147) / 148), ROWS_THREADS / 2);
+    return launch_pdl(vocab_rows_kernel, dim3((N + slice - 1) / slice), dim3(ROWS_THREADS), 0, s, (const bf16*)x, targets,
+                      lse_in, gloss, N, V, H, ignore_id, slice, loss, lse, w.r, status);
 }
 
 }  // namespace
@@ -683,7 +833,7 @@ cudaError_t launch_vocab_loss_forward(const void* x, const void* wt, const int32
     const int grid = 2 * std::min(pairs, Np / TILE * tiles);
     TRY(launch_pdl(vocab_kernel<false>, dim3(grid), dim3(NUM_THREADS), SMEM_BYTES, s, maps, p));
     return launch_pdl(vocab_finish_kernel, dim3(round_up(N, 32) / 32), dim3(512), 0, s, (const float2*)w.part,
-                      (const float*)w.target_logit, w.r, tiles, Np, loss, lse);
+                      (const float*)w.target_logit, w.r, tiles, N, Np, loss, lse);
 }
 
 cudaError_t launch_vocab_loss_backward(const void* x, const void* wt, const int32_t* targets, const float* lse,
@@ -717,6 +867,8 @@ cudaError_t launch_vocab_loss_backward(const void* x, const void* wt, const int3
     p.status = status;
     TRY(prepare_rows(x, targets, lse, gloss, nullptr, nullptr, N, V, H, ignore_id, w, status, s));
     const int pieces = (V + vc - 1) / vc;
+    TRY(launch_pdl(vocab_share_kernel, dim3(pieces + 1), dim3(32), 0, s, w.r, N, V, H, vc, pieces, p.want_dx, p.want_dw, pairs,
+                   acc_rows, w.shares));
     for (int i = 0; i <= pieces; ++i) {
         // logits of piece i into one buffer, products of piece i - 1 out of the other
         p.v_log = i < pieces ? i * vc : 0;
@@ -724,6 +876,7 @@ cudaError_t launch_vocab_loss_backward(const void* x, const void* wt, const int3
         p.v_mul = i > 0 ? (i - 1) * vc : 0;
         p.n_mul = i > 0 ? std::min(vc, V - p.v_mul) : 0;
         p.first = i == 1;
+        p.shares = w.shares + (size_t)i * pairs;
         if (i < pieces) maps.d_out = d_out[i & 1];
         if (i > 0) maps.d = d_in[(i - 1) & 1], maps.d_mn = d_mn[(i - 1) & 1];
         TRY(launch_pdl(vocab_kernel<true>, dim3(2 * pairs), dim3(NUM_THREADS), SMEM_BYTES, s, maps, p));
