@@ -28,6 +28,7 @@
 
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "tc_ptx.cuh"
 
@@ -283,14 +284,17 @@ struct Walk {
     __device__ __forceinline__ Unit next(const Tiles& t) {
         int u = pos;
         pos += step;
-        if constexpr (!BWD) return t.unit(LOGITS, u);
+        if constexpr (BWD) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int k = order[i], n = k == DX ? share.n[DX] : share.n[DW];
-            if (u < n) return t.unit(k, (k == DX ? share.first[DX] : share.first[DW]) + u);
-            u -= n;
+            for (int i = 0; i < 2; ++i) {
+                const int k = order[i], n = k == DX ? share.n[DX] : share.n[DW];
+                if (u < n) return t.unit(k, (k == DX ? share.first[DX] : share.first[DW]) + u);
+                u -= n;
+            }
+            return t.unit(LOGITS, share.first[LOGITS] + u);
+        } else {
+            return t.unit(LOGITS, u);
         }
-        return t.unit(LOGITS, share.first[LOGITS] + u);
     }
 };
 
@@ -375,9 +379,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     auto bar = [&](int i) { return smem_u32(bars + i); };
     constexpr int FULL = 0, EMPTY = STAGES, TFULL = 2 * STAGES, TEMPTY = 2 * STAGES + 2, MMA_DONE = 2 * STAGES + 4,
                   JOIN = 2 * STAGES + 5;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t crank = cluster_ctarank();
-    auto lead_bar = [&](int i) { return mapa_shared(bar(i), 0); };   // the even CTA's, which both CTAs signal
+    const uint32_t full0 = mapa_shared(bar(FULL), 0), tempty0 = mapa_shared(bar(TEMPTY), 0);   // the even CTA's, which both signal
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -386,7 +390,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(bar(TFULL + a), 1);
-            mbar_init(bar(TEMPTY + a), 2 * 32 * EPI_WARPS);   // every epilogue thread of both CTAs
+            mbar_init(bar(TEMPTY + a), 2 * EPI_WARPS);   // every epilogue warp of both CTAs
         }
         mbar_init(bar(MMA_DONE), 1);
         for (int j = 0; j < 16; ++j) mbar_init(bar(JOIN + j), 32);
@@ -409,93 +413,110 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     const Tiles tiles = Tiles::of(count, p.H, p.n_log, p.n_mul, p.want_dx, p.want_dw, pairs, p.acc_rows);
     Walk<BWD> walk(tiles, p.shares, pair, pairs);
 
+    // a wait that gives up does so for the whole warp
+    auto all = [](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
+
     if (warp == 0) {
-        // ---------------- TMA producer ----------------
-        if (lane == 0) {
-            uint32_t g = 0;
-            bool armed[STAGES], ok = true;
-            uint32_t armed_parity[STAGES];
-            for (int s = 0; s < STAGES; ++s) armed[s] = false, armed_parity[s] = 0;
-            while (ok && !walk.done()) {
-                const Unit w = walk.next(tiles);
-                const int a0 = w.m * TILE + (int)crank * 128, b0 = w.n * TILE + (int)crank * 128;
-                for (int kb = 0; kb < w.num_k; ++kb, ++g) {
-                    const int s = g % STAGES;
-                    const uint32_t r = g / STAGES;
-                    if (!mbar_wait(bar(EMPTY + s), (r & 1) ^ 1, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t sa = sbase + s * STAGE_BYTES, sb = sa + HALF_BYTES;
-                    const int k = (w.k0 + kb) * BK;
-                    const uint32_t full = lead_bar(FULL + s);
-                    if (crank == 0) {   // its barrier expects both CTAs' halves
-                        mbar_expect_tx(bar(FULL + s), 2 * STAGE_BYTES);
-                        armed[s] = true;
-                        armed_parity[s] = r & 1;
-                    }
-                    if (!BWD || w.kind == LOGITS) {
+        // ---------------- TMA producer (the whole warp, one lane issuing) ----------------
+        uint32_t s = 0, phase = 0, loaded = 0;
+        bool ok = true;
+        // one K step: both CTAs' halves land on the even CTA's barrier, which expects both
+        auto step = [&](auto&& loads) {
+            if (!all(mbar_wait(bar(EMPTY) + 8 * s, phase ^ 1, abort_flag))) return false;
+            if (elect_one()) {
+                if (crank == 0) mbar_expect_tx(bar(FULL) + 8 * s, 2 * STAGE_BYTES);
+                const uint32_t sa = sbase + s * STAGE_BYTES;
+                loads(sa, sa + HALF_BYTES, full0 + 8 * s);
+            }
+            __syncwarp();
+            ++loaded;
+            if (++s == STAGES) s = 0, phase ^= 1;
+            return true;
+        };
+        while (ok && !walk.done()) {
+            const Unit w = walk.next(tiles);
+            const int a0 = w.m * TILE + (int)crank * 128, b0 = w.n * TILE + (int)crank * 128;
+            const int k_end = (w.k0 + w.num_k) * BK;
+            if (!BWD || w.kind == LOGITS) {
+                for (int k = 0; k < k_end && ok; k += BK)
+                    ok = step([&](uint32_t sa, uint32_t sb, uint32_t full) {
                         tma_load_2d_pair(sa, &maps.x, k, a0, full);
                         tma_load_2d_pair(sb, &maps.w, k, p.v_log + b0, full);
-                    } else if (w.kind == DX) {
+                    });
+            } else if (w.kind == DX) {
+                for (int k = w.k0 * BK; k < k_end && ok; k += BK)
+                    ok = step([&](uint32_t sa, uint32_t sb, uint32_t full) {
                         tma_load_2d_pair(sa, &maps.d, k, a0, full);
                         tma_load_2d_pair(sb, &maps.w_mn, b0, p.v_mul + k, full);
                         tma_load_2d_pair(sb + HALF_BYTES / 2, &maps.w_mn, b0 + 64, p.v_mul + k, full);
-                    } else {
+                    });
+            } else {
+                for (int k = 0; k < k_end && ok; k += BK)
+                    ok = step([&](uint32_t sa, uint32_t sb, uint32_t full) {
                         tma_load_2d_pair(sa, &maps.d_mn, a0, k, full);
                         tma_load_2d_pair(sa + HALF_BYTES / 2, &maps.d_mn, a0 + 64, k, full);
                         tma_load_2d_pair(sb, &maps.x_mn, b0, k, full);
                         tma_load_2d_pair(sb + HALF_BYTES / 2, &maps.x_mn, b0 + 64, k, full);
-                    }
-                }
+                    });
             }
-            // no copy may still be landing in shared memory when the CTA exits
-            for (int s = 0; s < STAGES; ++s)
-                if (armed[s]) mbar_wait_drain(bar(FULL + s), armed_parity[s]);
         }
-        __syncwarp();
+        // no copy may still be landing in shared memory when the CTA exits (the
+        // even CTA's barriers complete with both CTAs' copies)
+        if (crank == 0)
+            for (uint32_t left = loaded < STAGES ? loaded : STAGES; left > 0; --left) {
+                if (s == 0) s = STAGES, phase ^= 1;
+                --s;
+                mbar_wait_drain(bar(FULL) + 8 * s, phase);
+            }
     } else if (warp == 1) {
-        // ---------------- MMA issuer (the even CTA's, for both) ----------------
-        if (lane == 0 && crank == 0) {
-            uint32_t g = 0;
-            int it = 0;
+        // ---------------- MMA issuer (the even CTA's, for both; the whole warp, one lane issuing) ----------------
+        if (crank == 0) {
+            uint32_t s = 0, phase = 0;
             bool ok = true;
-            for (; ok && !walk.done(); ++it) {
+            // the products of one unit; a K step of 16 is 32 bytes along a K-major
+            // row, or 16 rows of 128 bytes of an MN-major group
+            auto products = [&](auto a_mn, auto b_mn, uint32_t d_tmem, int num_k) {
+                constexpr bool A_MN = decltype(a_mn)::value, B_MN = decltype(b_mn)::value;
+                constexpr uint32_t idesc =
+                    make_idesc(2 * 128, TILE) | (A_MN ? IDESC_A_MN_MAJOR : 0) | (B_MN ? IDESC_B_MN_MAJOR : 0);
+                constexpr uint32_t a_step = A_MN ? 128 : 2, b_step = B_MN ? 128 : 2;
+                const uint64_t a0 = A_MN ? sw128_desc_mn_groups(sbase, HALF_BYTES / 2) : sw128_desc(sbase);
+                const uint64_t b0 = B_MN ? sw128_desc_mn_groups(sbase + HALF_BYTES, HALF_BYTES / 2)
+                                         : sw128_desc(sbase + HALF_BYTES);
+                for (int kb = 0; kb < num_k; ++kb) {
+                    if (!all(mbar_wait_cluster(bar(FULL) + 8 * s, phase, abort_flag))) return false;
+                    tc_fence_after();
+                    const uint64_t ad = a0 + s * (STAGE_BYTES >> 4), bd = b0 + s * (STAGE_BYTES >> 4);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < BK / 16; ++k)
+                            mma_bf16_pair(d_tmem, ad + k * a_step, bd + k * b_step, idesc, (kb | k) != 0);
+                        mma_commit_pair(bar(EMPTY) + 8 * s, 0x3);   // both CTAs' stage s
+                    }
+                    __syncwarp();
+                    if (++s == STAGES) s = 0, phase ^= 1;
+                }
+                return true;
+            };
+            constexpr std::integral_constant<bool, true> mn{};
+            constexpr std::integral_constant<bool, false> kmajor{};
+            for (int it = 0; ok && !walk.done(); ++it) {
                 const Unit w = walk.next(tiles);
                 const int acc = it & 1, use = it >> 1;
-                if (!mbar_wait_cluster(bar(TEMPTY + acc), (use & 1) ^ 1, abort_flag)) {
-                    ok = false;
-                    break;
-                }
+                if (!all(mbar_wait_cluster(bar(TEMPTY + acc), (use & 1) ^ 1, abort_flag))) break;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + acc * TILE;
-                const bool a_mn = BWD && w.kind == DW, b_mn = BWD && w.kind != LOGITS;
-                const uint32_t idesc = make_idesc(2 * 128, TILE) | (a_mn ? IDESC_A_MN_MAJOR : 0) | (b_mn ? IDESC_B_MN_MAJOR : 0);
-                // a K step of 16: 32 bytes along a K-major row, 16 rows of 128 bytes of an MN-major group
-                const uint32_t a_step = a_mn ? 128 : 2, b_step = b_mn ? 128 : 2;
-                for (int kb = 0; kb < w.num_k; ++kb, ++g) {
-                    const int s = g % STAGES;
-                    if (!mbar_wait_cluster(bar(FULL + s), (g / STAGES) & 1, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t sa = sbase + s * STAGE_BYTES, sb = sa + HALF_BYTES;
-                    const uint64_t ad = a_mn ? sw128_desc_mn_groups(sa, HALF_BYTES / 2) : sw128_desc(sa);
-                    const uint64_t bd = b_mn ? sw128_desc_mn_groups(sb, HALF_BYTES / 2) : sw128_desc(sb);
-#pragma unroll
-                    for (int k = 0; k < BK / 16; ++k)
-                        mma_bf16_pair(d_tmem, ad + k * a_step, bd + k * b_step, idesc, (kb | k) != 0);
-                    mma_commit_pair(bar(EMPTY + s), 0x3);   // both CTAs' stage s
-                }
-                if (!ok) break;
-                mma_commit_pair(bar(TFULL + acc), 0x3);     // both CTAs' accumulator halves
+                if (!BWD || w.kind == LOGITS) ok = products(kmajor, kmajor, d_tmem, w.num_k);
+                else if (w.kind == DX) ok = products(kmajor, mn, d_tmem, w.num_k);
+                else ok = products(mn, mn, d_tmem, w.num_k);
+                if (ok && elect_one()) mma_commit_pair(bar(TFULL + acc), 0x3);   // both CTAs' accumulator halves
+                __syncwarp();
             }
             // every MMA issued must be finished before TMEM is freed
-            mma_commit_pair(bar(MMA_DONE), 0x1);
+            if (elect_one()) mma_commit_pair(bar(MMA_DONE), 0x1);
+            __syncwarp();
             mbar_wait_drain(bar(MMA_DONE), 0);
         }
-        __syncwarp();
     } else {
         // ---------------- epilogue: thread = row, warps 2..5 columns 0..127, warps 6..9 the others ----------------
         const int quad = warp & 3, half = (warp - 2) >> 2;
@@ -526,7 +547,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                 target = p.r.target[row] - p.v_log - col0;     // within this warp's columns, if it is there
                 if (BWD) lse2 = p.r.lse2[row], ratio = p.r.ratio[row];
             }
-            if (!mbar_wait(bar(TFULL + acc), use & 1, abort_flag)) break;
+            if (!all(mbar_wait(bar(TFULL + acc), use & 1, abort_flag))) break;
             tc_fence_after();
             // the accumulator is free once both loads are in registers
             float v[2][64];
@@ -536,7 +557,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
             tmem_tie64(v[0]);
             tmem_tie64(v[1]);
             tc_fence_before();
-            mbar_arrive_cluster(lead_bar(TEMPTY + acc));
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(tempty0 + 8 * acc);
             if constexpr (!BWD) {
                 float top = -INFINITY, ref = -INFINITY, sum = 0.f;
 #pragma unroll
@@ -578,7 +600,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                     *other = make_float2(ref, sum);
                     mbar_arrive(bar(joined));
                 } else {
-                    if (!mbar_wait(bar(joined), (it >> 2) & 1, abort_flag)) break;
+                    if (!all(mbar_wait(bar(joined), (it >> 2) & 1, abort_flag))) break;
                     const float2 o = *other;
                     const float both = fmaxf(ref, o.x);
                     if (both != -INFINITY) sum = sum * ex2_approx(ref - both) + o.y * ex2_approx(o.x - both);

@@ -153,6 +153,19 @@ __device__ __forceinline__ void store_bf16x32(bf16* dst, const float (&v)[32]) {
 
 namespace tc {
 
+// True in one lane of a converged warp.  Issuing from inside a warp-uniform loop
+// by this, rather than running the loop in one lane, leaves addresses and
+// descriptors in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred P;\n\t"
+        "elect.sync _|P, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, P;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 // Make generic-proxy writes to shared memory visible to the async proxy
 // (tensor-core operand reads) before signalling the MMA issuer.
 __device__ __forceinline__ void fence_proxy_async_smem() {
