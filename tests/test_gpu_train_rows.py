@@ -200,7 +200,7 @@ def test_ln_gradients_against_differences(enc):
 @pytest.mark.parametrize("H", [1, 3, 8, 24, 62, 96, 250, 256, 264, 768, 1000, 2500])
 def test_embed_forward(enc, H):
     for te, ty in TYPES:
-        for T, V in ((1, 1), (37, 5), (1051, 777)):
+        for T, V in ((1, 1), (37, 5), (1051, 777), (8193, 99)):
             g = _gen(H + T)
             table = _randn(g, V, H).to(te)
             ids = torch.randint(0, V, (T,), generator=g, device="cuda", dtype=torch.int32)
@@ -233,8 +233,8 @@ def _check_embed_backward(grad, dy, ids, V, scale, old=None):
     T, H = dy.shape
     want = torch.zeros(V, H, dtype=torch.float64, device="cuda").index_add_(0, ids.long(), dy.double())
     mag = torch.zeros(V, H, dtype=torch.float64, device="cuda").index_add_(0, ids.long(), dy.double().abs())
-    # 32 tokens in a warp, 8 warps, the blocks' pieces in four slices, and their sum
-    chain = 32 + 8 + T / 1024 + 6
+    # 8 tokens (T <= 16384) or 32 in a warp, 8 warps, the pieces of a run that crosses blocks in four slices, and their sum
+    chain = 8 + 8 + T / 256 + 8 if T <= 16384 else 32 + 8 + T / 1024 + 8
     s = float(np.float32(scale))
     want, bound = want * s, (chain + 1) * U * mag * abs(s)
     if old is not None:
@@ -263,7 +263,7 @@ def _ids(kind, T, V, g):
 
 @pytest.mark.parametrize("kind", ["uniform", "one", "descending", "runs", "heavy"])
 @pytest.mark.parametrize("T,V,H", [(1, 1, 8), (1, 9, 5), (31, 2, 24), (33, 40, 257), (256, 511, 40), (257, 512, 264),
-                                   (2561, 513, 96), (8193, 5000, 33), (20000, 300001, 8)])
+                                   (2561, 513, 96), (8193, 5000, 33), (20000, 300001, 8), (16385, 60000, 72)])
 def test_embed_backward(enc, kind, T, V, H):
     for n, (te, ty) in enumerate(TYPES):
         g = _gen(T + H + n)

@@ -12,8 +12,10 @@ def test_workspace_sizes(built_lib):  # noqa: F811
     assert ln(1 << 30, 768) == ln(65536, 768) == 640 * 768 * 4        # the grid is bounded
     assert ln(1 << 30, 8192) == 640 * 8192 * 4
     assert em(0, 1, 1) == 0
-    # two pair arrays, a state and two fp32 rows for each block of 256 tokens, rounded up to 256 bytes each
-    assert em(257, 1000, 768) == 2 * 2304 + 256 + 2 * (2 * 768 * 4)
+    # two pair arrays, a state and two fp32 rows for each block of 64 tokens (256 past 16384 tokens), rounded up to
+    # 256 bytes each
+    assert em(257, 1000, 768) == 2 * 2304 + 256 + 2 * (5 * 768 * 4)
+    assert em(16385, 1000, 768) == 2 * 131328 + 768 + 2 * (65 * 768 * 4)
     assert em(1 << 30, 1, 1) > 1 << 33                               # past 32 bits
 
 

@@ -4,16 +4,19 @@
 // The gradient dE[v] = scale sum_{t: id[t] = v} dy[t] is bound by HBM: dy is
 // read once and the whole table written once (most rows with zeros).  Three
 // launches, all without atomics on values:
-//   embed_sort_fill_kernel  one cluster of eight CTAs sorts (id, t) stably by id
+//   embed_sort_kernel  one cluster of sixteen CTAs sorts (id, t) stably by id
 //     (radix sort, at most nine bits a pass, counters in shared memory, column
 //     totals exchanged through distributed shared memory); meanwhile the other
-//     CTAs zero the table rows that no token has.
-//   embed_sum_kernel  each warp adds the rows of 32 consecutive sorted tokens
-//     for 256 columns; runs of one id inside a block of 256 tokens are joined in
-//     shared memory and written, the pieces of runs that cross blocks are kept.
+//     CTAs zero the first rows of the table, as many as the sort has time for.
+//     Few tokens are sorted by counting instead (embed_rank_kernel).
+//   embed_sum_kernel  each warp adds the rows of 8 or 32 consecutive sorted tokens
+//     for 256 columns; runs of one id inside a block's tokens are joined in shared
+//     memory and written, the pieces of runs that cross blocks are kept.  Blocks
+//     behind these zero the rest of the rows that no token has.
 //   embed_join_kernel  adds the pieces of each run that crosses blocks, in order.
 #include "train_internal.cuh"
 
+#include <algorithm>
 #include <mutex>
 
 #include "tc_ptx.cuh"
@@ -24,8 +27,9 @@ namespace {
 // forward
 // ---------------------------------------------------------------------------
 
-// y[t] = scale E[id[t]]; 2^lane_bits lanes per token.
-template <typename TE, typename TY, bool VEC>
+// y[t] = scale E[id[t]]; 2^lane_bits lanes per token.  (Four tokens a group, for
+// more reads in flight, measured slower: 29.5 against 25.8 us at 32768 x 768.)
+template <typename TE, typename TY, int W>
 __global__ void __launch_bounds__(256) embed_forward_kernel(const TE* __restrict__ table, const int32_t* __restrict__ ids,
                                                             TY* __restrict__ y, int T, int V, int H, float scale,
                                                             int lane_bits, unsigned int* status) {
@@ -40,14 +44,14 @@ __global__ void __launch_bounds__(256) embed_forward_kernel(const TE* __restrict
     if (!ok && lane == 0) atomicOr(status, TEE_STATUS_BAD_ID);
     const TE* src = table + (size_t)(ok ? id : 0) * H;
     TY* dst = y + (size_t)t * H;
-    if constexpr (VEC) {
-#pragma unroll 4
-        for (int c = lane; c < H / 8; c += step) {
-            float v[8];
-            load8(src + 8 * c, v);
+    if constexpr (W > 1) {
+#pragma unroll 6
+        for (int c = lane; c < H / W; c += step) {
+            float v[W];
+            load_vec(src + W * c, v);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = ok ? v[j] * scale : 0.f;
-            store8(dst + 8 * c, v);
+            for (int j = 0; j < W; ++j) v[j] = ok ? v[j] * scale : 0.f;
+            store_vec(dst + W * c, v);
         }
     } else {
 #pragma unroll 4
@@ -59,11 +63,10 @@ __global__ void __launch_bounds__(256) embed_forward_kernel(const TE* __restrict
 // backward: sort
 // ---------------------------------------------------------------------------
 
-constexpr int SORT_CTAS = 8, SORT_THREADS = 1024, SORT_WARPS = SORT_THREADS / 32;
+constexpr int SORT_CTAS = 16, SORT_THREADS = 1024, SORT_WARPS = SORT_THREADS / 32;
 constexpr int MAX_DIGIT_BITS = 9, MAX_BINS = 1 << MAX_DIGIT_BITS;
-constexpr int TOKENS_PER_WARP = 32, SUM_WARPS = 8, TOKENS_PER_BLOCK = TOKENS_PER_WARP * SUM_WARPS;
+constexpr int SUM_WARPS = 8;
 constexpr int COLS = 256;   // columns per block of embed_sum_kernel: eight per lane
-constexpr int FILL_WORDS = SORT_WARPS * MAX_BINS;   // the fill CTAs' row flags take the sort's counters
 
 struct SortSmem {
     uint32_t hist[SORT_WARPS][MAX_BINS];   // per warp: its keys per digit, then where its next such key goes
@@ -71,6 +74,8 @@ struct SortSmem {
     uint32_t scan[SORT_WARPS];
 };
 static_assert(sizeof(SortSmem) <= 80 * 1024, "shared memory");
+
+constexpr uint32_t NO_KEY = 0xffffffffu;
 
 // A sorted token: key = its id (V where the id is out of range), and its place in the batch.
 typedef uint2 Pair;
@@ -81,7 +86,9 @@ __device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
     return v;
 }
 
-// One stable pass over digit `shift` .. `shift + bits` by the cluster's 256
+constexpr int GROUP = 8;
+
+// One stable pass over digit `shift` .. `shift + bits` by the cluster's 512
 // warps, each with `slice` consecutive keys.
 template <bool FIRST>
 __device__ void sort_pass(SortSmem& sm, const int32_t* __restrict__ ids, const Pair* in, Pair* out, int T, int V,
@@ -101,11 +108,21 @@ __device__ void sort_pass(SortSmem& sm, const int32_t* __restrict__ ids, const P
     };
     for (int b = lane; b < bins; b += 32) sm.hist[warp][b] = 0;
     __syncwarp();
-#pragma unroll 4
-    for (int p = lo + lane; p < hi; p += 32) {
-        const uint32_t key = fetch(p).x;
-        if (FIRST && key == (uint32_t)V) atomicOr(status, TEE_STATUS_BAD_ID);
-        atomicAdd(&sm.hist[warp][(key >> shift) & mask], 1u);
+    // eight keys per lane in flight at a time, here and below
+    for (int p0 = lo; p0 < hi; p0 += 32 * GROUP) {
+        uint32_t key[GROUP];
+#pragma unroll
+        for (int q = 0; q < GROUP; ++q) {
+            const int p = p0 + 32 * q + lane;
+            key[q] = p < hi ? fetch(p).x : 0xffffffffu;
+        }
+#pragma unroll
+        for (int q = 0; q < GROUP; ++q) {
+            if (p0 + 32 * q + lane < hi) {
+                if (FIRST && key[q] == (uint32_t)V) atomicOr(status, TEE_STATUS_BAD_ID);
+                atomicAdd(&sm.hist[warp][(key[q] >> shift) & mask], 1u);
+            }
+        }
     }
     __syncthreads();
     // per digit: turn the warps' counts into offsets within this CTA
@@ -140,42 +157,146 @@ __device__ void sort_pass(SortSmem& sm, const int32_t* __restrict__ ids, const P
     }
     if (lane == 31) sm.scan[warp] = inc;
     __syncthreads();
-    uint32_t base = inc - all + before;
-    for (int w = 0; w < warp; ++w) base += sm.scan[w];
+    const uint32_t others = __reduce_add_sync(0xffffffffu, lane < warp ? sm.scan[lane] : 0u);
+    const uint32_t base = inc - all + before + others;
     if (threadIdx.x < bins) {
 #pragma unroll 8
         for (int w = 0; w < SORT_WARPS; ++w) sm.hist[w][threadIdx.x] += base;
     }
     __syncthreads();
-    for (int p0 = lo; p0 < hi; p0 += 32) {
-        const int p = p0 + lane;
-        const unsigned live = __ballot_sync(0xffffffffu, p < hi);
-        if (p < hi) {
-            const Pair kv = fetch(p);
-            const uint32_t d = (kv.x >> shift) & mask;
-            const unsigned peers = __match_any_sync(live, d);
-            const uint32_t at = sm.hist[warp][d];
-            __syncwarp(live);
-            if (lane == 31 - __clz(peers)) sm.hist[warp][d] = at + __popc(peers);
-            __syncwarp(live);
-            const uint32_t to = at + __popc(peers & ((1u << lane) - 1));
-            if (to < (uint32_t)T) out[to] = kv;   // always, unless another call writes to this workspace
+    for (int p0 = lo; p0 < hi; p0 += 32 * GROUP) {
+        Pair kv[GROUP];
+#pragma unroll
+        for (int q = 0; q < GROUP; ++q) {
+            const int p = p0 + 32 * q + lane;
+            kv[q] = p < hi ? fetch(p) : make_uint2(0, 0);
         }
-        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < GROUP; ++q) {
+            const int p = p0 + 32 * q + lane;
+            const unsigned live = __ballot_sync(0xffffffffu, p < hi);
+            if (p < hi) {
+                const uint32_t d = (kv[q].x >> shift) & mask;
+                const unsigned peers = __match_any_sync(live, d);
+                const uint32_t at = sm.hist[warp][d];
+                __syncwarp(live);
+                if (lane == 31 - __clz(peers)) sm.hist[warp][d] = at + __popc(peers);
+                const uint32_t to = at + __popc(peers & ((1u << lane) - 1));
+                if (to < (uint32_t)T) out[to] = kv[q];   // always, unless another call writes to this workspace
+            }
+            __syncwarp();
+        }
     }
     // the next pass reads the other CTAs' keys and rewrites the totals
     tc::cluster_sync();
 }
 
+// Zeroes n elements: pieces of ZERO_VECS vectors, dealt out to the blocks in turn.
+constexpr size_t ZERO_VECS = 4096;
+template <int BLOCKS, int THREADS, typename TG>
+__device__ __forceinline__ void zero_span(TG* to, size_t n, int me) {
+    const size_t vecs = n * sizeof(TG) / 16;
+    for (size_t i0 = (size_t)me * ZERO_VECS; i0 < vecs; i0 += (size_t)BLOCKS * ZERO_VECS)
+#pragma unroll
+        for (size_t i = i0 + threadIdx.x; i < i0 + ZERO_VECS; i += THREADS)
+            if (i < vecs) reinterpret_cast<uint4*>(to)[i] = make_uint4(0, 0, 0, 0);
+    if (me == 0)
+        for (size_t i = vecs * 16 / sizeof(TG) + threadIdx.x; i < n; i += THREADS) f32_to_elem(0.f, to[i]);
+}
+
+// First place in the sorted tokens whose key is not below `key`, by one warp:
+// 32 probes a step.
+__device__ __forceinline__ int lower_bound_warp(const Pair* __restrict__ sorted, int T, uint32_t key) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = T;
+    while (hi - lo > 32) {
+        const int stride = (hi - lo) / 33 + 1, pos = lo + (lane + 1) * stride - 1;
+        const int c = __popc(__ballot_sync(0xffffffffu, pos < hi && sorted[pos].x < key));
+        lo += c * stride;
+        hi = min(hi, lo + stride - 1);
+    }
+    return lo + __popc(__ballot_sync(0xffffffffu, lo + lane < hi && sorted[lo + lane].x < key));
+}
+
+// Zeroes those of the rows [v_lo, v_hi) that no token has (at most 32 FLAG_WORDS
+// rows): their tokens stand together in the sorted ones.
+constexpr int FLAG_WORDS = 64;
+template <int THREADS, typename TG>
+__device__ __forceinline__ void zero_absent_rows(const Pair* __restrict__ sorted, int T, TG* grad, int H, int v_lo, int v_hi,
+                                                 uint32_t* flags, int* range) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp < 2) {
+        const int p = lower_bound_warp(sorted, T, (uint32_t)(warp ? v_hi : v_lo));
+        if (lane == 0) range[warp] = p;
+    }
+    if (threadIdx.x < FLAG_WORDS) flags[threadIdx.x] = 0;
+    __syncthreads();
+    const int end = range[1];
+#pragma unroll 4
+    for (int p = range[0] + threadIdx.x; p < end; p += THREADS) {
+        const uint32_t r = sorted[p].x - (uint32_t)v_lo;
+        if (r < 32 * FLAG_WORDS) atomicOr(&flags[r >> 5], 1u << (r & 31));
+    }
+    __syncthreads();
+    const size_t row_bytes = (size_t)H * sizeof(TG);
+    for (int r = warp; r < v_hi - v_lo; r += THREADS / 32) {
+        if (flags[r >> 5] >> (r & 31) & 1u) continue;
+        TG* row = grad + (size_t)(v_lo + r) * H;
+        if (row_bytes % 16 == 0) {
+#pragma unroll 6
+            for (uint32_t j = lane; j < (uint32_t)(row_bytes / 16); j += 32) reinterpret_cast<uint4*>(row)[j] = make_uint4(0, 0, 0, 0);
+        } else {
+            for (uint32_t j = lane; j < (uint32_t)H; j += 32) f32_to_elem(0.f, row[j]);
+        }
+    }
+}
+
+// Few tokens are sorted by counting: a token's place is the number of tokens
+// with a smaller id, or the same id and an earlier place.  Each warp places
+// tokens of its own against all ids, held in shared memory.
+constexpr int RANK_THREADS = 512, RANK_MAX_TOKENS = 4096;
+__global__ void __launch_bounds__(RANK_THREADS)
+    embed_rank_kernel(const int32_t* __restrict__ ids, int T, int V, Pair* __restrict__ out, unsigned int* status) {
+    extern __shared__ __align__(16) uint32_t keys[];   // T rounded up to 4, padded with the largest key
+    pdl_wait();
+    pdl_trigger();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int T4 = (T + 3) / 4 * 4;
+#pragma unroll 4
+    for (int t = threadIdx.x; t < T4; t += RANK_THREADS) {
+        const int id = t < T ? ids[t] : -1;
+        const bool ok = id >= 0 && id < V;
+        if (!ok && t < T && blockIdx.x == 0) atomicOr(status, TEE_STATUS_BAD_ID);
+        keys[t] = ok ? (uint32_t)id : t < T ? (uint32_t)V : NO_KEY;
+    }
+    __syncthreads();
+    for (int t = blockIdx.x * (RANK_THREADS / 32) + warp; t < T; t += gridDim.x * (RANK_THREADS / 32)) {
+        const uint32_t k = keys[t];
+        uint32_t n = 0;
+        // up to t's group of four the same id counts as smaller; the group itself is looked at one by one
+        const int g = t / 4;
+#pragma unroll 4
+        for (int j = lane; j < T4 / 4; j += 32) {
+            const uint4 v = reinterpret_cast<const uint4*>(keys)[j];
+            const uint32_t below = k + (j < g ? 1u : 0u);   // V < 2^32 - 1: no wrap
+            n += (v.x < below) + (v.y < below) + (v.z < below) + (v.w < below);
+        }
+        if (lane < t - 4 * g) n += keys[4 * g + lane] == k;
+        n = __reduce_add_sync(0xffffffffu, n);
+        if (lane == 0) out[n] = make_uint2(k, (uint32_t)t);
+    }
+}
+
+constexpr int SORT_FILLERS = 512;   // fill CTAs beside the sort's: whole clusters
+
 template <typename TG>
 __global__ void __cluster_dims__(SORT_CTAS, 1, 1) __launch_bounds__(SORT_THREADS)
-    embed_sort_fill_kernel(const int32_t* __restrict__ ids, int T, int V, int H, int key_bits, Pair* buf0, Pair* buf1,
-                           TG* __restrict__ grad, unsigned int* status) {
+    embed_sort_kernel(const int32_t* __restrict__ ids, int T, int V, int H, int key_bits, Pair* buf0, Pair* buf1,
+                      TG* __restrict__ grad, int fill_rows, unsigned int* status) {
     extern __shared__ __align__(16) uint8_t raw[];
     SortSmem& sm = *reinterpret_cast<SortSmem*>(raw);
     pdl_wait();
     pdl_trigger();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (blockIdx.x < SORT_CTAS) {
         const uint32_t rank = tc::cluster_ctarank();
         const int slice = (int)(((long long)T + SORT_CTAS * SORT_WARPS * 32 - 1) / (SORT_CTAS * SORT_WARPS * 32)) * 32;
@@ -188,45 +309,19 @@ __global__ void __cluster_dims__(SORT_CTAS, 1, 1) __launch_bounds__(SORT_THREADS
         }
         return;
     }
-    // fill: this CTA's share of the rows, in windows of as many flags as fit
-    uint32_t* flags = reinterpret_cast<uint32_t*>(raw);
-    const int fillers = gridDim.x - SORT_CTAS, me = blockIdx.x - SORT_CTAS;
-    const int v_lo = (int)((long long)V * me / fillers), v_hi = (int)((long long)V * (me + 1) / fillers);
-    const bool vec = ((size_t)H * sizeof(TG)) % 16 == 0;
-    for (int w_lo = v_lo; w_lo < v_hi; w_lo += min(v_hi - w_lo, FILL_WORDS * 32)) {
-        const int rows = min(v_hi - w_lo, FILL_WORDS * 32);
-        for (int i = threadIdx.x; i < (rows + 31) / 32; i += SORT_THREADS) flags[i] = 0;
-        __syncthreads();
-#pragma unroll 4
-        for (int t = threadIdx.x; t < T; t += SORT_THREADS) {
-            const uint32_t r = (uint32_t)ids[t] - (uint32_t)w_lo;
-            if (r < (uint32_t)rows) atomicOr(&flags[r >> 5], 1u << (r & 31));
-        }
-        __syncthreads();
-        for (int r = warp; r < rows; r += SORT_WARPS) {
-            if (flags[r >> 5] >> (r & 31) & 1u) continue;
-            TG* row = grad + (size_t)(w_lo + r) * H;
-            if (vec) {
-                const int n = (int)((size_t)H * sizeof(TG) / 16);
-                for (int c = lane; c < n; c += 32) reinterpret_cast<uint4*>(row)[c] = make_uint4(0, 0, 0, 0);
-            } else {
-                for (int c = lane; c < H; c += 32) f32_to_elem(0.f, row[c]);
-            }
-        }
-        __syncthreads();
-    }
+    // all of these rows: those that have tokens are written again by the sums, which wait for this kernel
+    zero_span<SORT_FILLERS, SORT_THREADS>(grad, (size_t)fill_rows * H, (int)blockIdx.x - SORT_CTAS);
 }
 
 // ---------------------------------------------------------------------------
 // backward: sums over runs of one id
 // ---------------------------------------------------------------------------
 
-// What a block of 256 sorted tokens leaves for embed_join_kernel.
+// What a block of embed_sum_kernel leaves for embed_join_kernel.
 //   head: the piece of a run that began in an earlier block: HEAD_NONE, HEAD_ENDS
 //     (the run ends here) or HEAD_THROUGH (it fills the block and goes on).
 //   tail_key: the id of a run that begins here and goes on, or NO_KEY.
 constexpr int HEAD_NONE = 0, HEAD_ENDS = 1, HEAD_THROUGH = 2;
-constexpr uint32_t NO_KEY = 0xffffffffu;
 struct BlockState {
     int head;
     uint32_t tail_key;
@@ -239,22 +334,38 @@ __device__ __forceinline__ void put(TG* grad, size_t at, float sum, float scale,
     f32_to_elem(v, grad[at]);
 }
 
-template <typename TY, typename TG, bool VEC>
-__global__ void __launch_bounds__(SUM_WARPS * 32)
-    embed_sum_kernel(const TY* __restrict__ dy, const Pair* __restrict__ sorted, TG* __restrict__ grad, int T, int V, int H,
-                     float scale, int accumulate, BlockState* __restrict__ state, float* __restrict__ head,
-                     float* __restrict__ tail) {
+constexpr int SUM_BATCH = 4;   // rows a warp reads together
+
+// The first sum_blocks x (column groups) blocks add, the column groups of the same
+// tokens next to one another so that their rows are read together; the blocks
+// behind them zero the rows fill_from .. V that no token has, chunk_rows each (one
+// such block for every chunk: a few hundred with many chunks each took 10 us longer
+// for 315 MB).  Eight columns per lane in runs of W; each warp adds its tokens, and the warps' pieces of runs that
+// cross warps are joined in shared memory.
+template <typename TY, typename TG, int W, int TOKENS_PER_WARP>
+__global__ void __launch_bounds__(SUM_WARPS * 32, 3)   // three blocks an SM measured best (64K tokens: 106 us for the call, 111 with two)
+    embed_sum_kernel(const TY* __restrict__ dy, const Pair* __restrict__ sorted, TG* grad, int T, int V, int H, float scale,
+                     int accumulate, int sum_blocks, int fill_from, int chunk_rows, BlockState* __restrict__ state,
+                     float* __restrict__ head, float* __restrict__ tail) {
+    constexpr int TOKENS_PER_BLOCK = TOKENS_PER_WARP * SUM_WARPS;
     // a warp's piece of the run that reaches into it from the left (L), and of the one that leaves it to the right (R)
     __shared__ float piece[2][SUM_WARPS][COLS];
     __shared__ uint32_t key_l[SUM_WARPS], key_r[SUM_WARPS];   // NO_KEY: no such piece
     __shared__ int through[SUM_WARPS];                        // L leaves the warp to the right as well
     pdl_wait();
     pdl_trigger();
+    const int groups = (H + COLS - 1) / COLS, block = blockIdx.x / groups;
+    if (block >= sum_blocks) {
+        const long long lo = fill_from + (long long)((int)blockIdx.x - sum_blocks * groups) * chunk_rows;
+        zero_absent_rows<SUM_WARPS * 32>(sorted, T, grad, H, (int)lo, (int)min((long long)V, lo + chunk_rows),
+                                         reinterpret_cast<uint32_t*>(piece), through);
+        return;
+    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int col0 = blockIdx.y * COLS;
-    const long long first = (long long)blockIdx.x * TOKENS_PER_BLOCK + warp * TOKENS_PER_WARP;
+    const int group = blockIdx.x % groups, col0 = group * COLS;
+    const long long first = (long long)block * TOKENS_PER_BLOCK + warp * TOKENS_PER_WARP;
     const int n = (int)max(0LL, min((long long)TOKENS_PER_WARP, T - first));
-    auto col = [&](int j) { return VEC ? lane * 8 + j : j * 32 + lane; };   // within the block's columns
+    auto col = [&](int j) { return (j / W * 32 + lane) * W + j % W; };   // within the block's columns
     if (lane == 0) key_l[warp] = key_r[warp] = NO_KEY, through[warp] = 0;
     if (n > 0) {
         Pair kv = make_uint2(NO_KEY, 0);
@@ -273,41 +384,43 @@ __global__ void __launch_bounds__(SUM_WARPS * 32)
         auto write = [&]() {   // a run that lies within this warp
             if (cur >= (uint32_t)V) return;
             TG* row = grad + (size_t)cur * H + col0;
-            if constexpr (VEC) {
-                if (col0 + lane * 8 < H) {
-                    float v[8];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] = acc[j] * scale;
-                    if (accumulate) {
-                        float o[8];
-                        load8(row + lane * 8, o);
+            for (int j0 = 0; j0 < 8; j0 += W) {
+                if (col0 + col(j0) >= H) continue;
+                if constexpr (W == 1) {
+                    put(row, col(j0), acc[j0], scale, accumulate);
+                } else {
+                    float v[W] = {};
+                    if (accumulate) load_vec(row + col(j0), v);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) v[j] += o[j];
-                    }
-                    store8(row + lane * 8, v);
+                    for (int j = 0; j < W; ++j) v[j] = acc[j0 + j] * scale + v[j];
+                    store_vec(row + col(j0), v);
                 }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (col0 + col(j) < H) put(row, col(j), acc[j], scale, accumulate);
             }
         };
-        constexpr int BATCH = 8;
+        constexpr int BATCH = SUM_BATCH;
+#pragma unroll 1
         for (int i0 = 0; i0 < n; i0 += BATCH) {
             float v[BATCH][8];
 #pragma unroll
             for (int q = 0; q < BATCH; ++q) {
                 const uint32_t k = __shfl_sync(0xffffffffu, kv.x, i0 + q), t = __shfl_sync(0xffffffffu, kv.y, i0 + q);
+                const uint32_t last = i0 + q > 0 ? __shfl_sync(0xffffffffu, kv.x, (i0 + q - 1) & 31) : before;
                 const TY* row = dy + (size_t)t * H + col0;
                 const bool ok = k < (uint32_t)V && t < (uint32_t)T;   // false past the end as well (NO_KEY)
-                if constexpr (VEC) {
-                    if (ok && col0 + lane * 8 < H) load8(row + lane * 8, v[q]);
-                    else
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) v[q][j] = 0.f;
-                } else {
+                for (int j0 = 0; j0 < 8; j0 += W) {
+                    const bool in = ok && col0 + col(j0) < H;
+                    if constexpr (W == 1) {
+                        v[q][j0] = in ? elem_to_f32(row[col(j0)]) : 0.f;
+                    } else {
+                        float x[W] = {};
+                        if (in) load_vec(row + col(j0), x);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[q][j] = ok && col0 + col(j) < H ? elem_to_f32(row[col(j)]) : 0.f;
+                        for (int j = 0; j < W; ++j) v[q][j0 + j] = x[j];
+                    }
+                    // the row of the table that a new run will be added to, on its way while the tokens' rows are
+                    if (accumulate && in && k != last) asm volatile("prefetch.global.L2 [%0];" ::"l"(grad + (size_t)k * H + col0 + col(j0)));
                 }
             }
 #pragma unroll
@@ -357,7 +470,7 @@ __global__ void __launch_bounds__(SUM_WARPS * 32)
             if (!through[w]) {
                 if (open == 1) {
                     head_state = HEAD_ENDS;
-                    if (in) head[(size_t)blockIdx.x * H + col0 + c] = acc;
+                    if (in) head[(size_t)block * H + col0 + c] = acc;
                 } else if (in && key_l[w] < (uint32_t)V) {
                     put(grad, (size_t)key_l[w] * H + col0 + c, acc, scale, accumulate);
                 }
@@ -373,50 +486,64 @@ __global__ void __launch_bounds__(SUM_WARPS * 32)
     }
     if (open == 1) {
         head_state = HEAD_THROUGH;
-        if (in) head[(size_t)blockIdx.x * H + col0 + c] = acc;
+        if (in) head[(size_t)block * H + col0 + c] = acc;
     } else if (open == 2) {
-        if (in) tail[(size_t)blockIdx.x * H + col0 + c] = acc;
+        if (in) tail[(size_t)block * H + col0 + c] = acc;
     }
-    if (blockIdx.y == 0 && c == 0) state[blockIdx.x] = BlockState{head_state, open == 2 ? open_key : NO_KEY};
+    if (group == 0 && c == 0) state[block] = BlockState{head_state, open == 2 ? open_key : NO_KEY};
 }
 
 // Block b adds the run that begins in block b of embed_sum_kernel and crosses
-// its end: tail of b, then the heads of b + 1 .. the block where the run ends.
-// Four slices of the heads, 256 columns.
+// its end: tail of b, then the heads of b + 1 .. the block where the run ends, in
+// four slices of 64 columns.
+constexpr int JOIN_COLS = 64, JOIN_SLICES = 4;
 template <typename TG>
-__global__ void __launch_bounds__(1024)
+__global__ void __launch_bounds__(JOIN_COLS* JOIN_SLICES)
     embed_join_kernel(const BlockState* __restrict__ state, int n_blocks, const float* __restrict__ head,
                       const float* __restrict__ tail, TG* __restrict__ grad, int V, int H, float scale, int accumulate) {
-    __shared__ float red[3][COLS];
+    __shared__ float red[JOIN_SLICES][JOIN_COLS];
     __shared__ int end_s;
     pdl_wait();
     pdl_trigger();
     const int b = blockIdx.x;
     const uint32_t key = state[b].tail_key;
+    // the first block after b whose head ends the run
+    int e = b + 1 + threadIdx.x;
+    int mine = e < n_blocks ? state[e].head : HEAD_NONE;
     if (key >= (uint32_t)V) return;   // NO_KEY, or the run of out-of-range ids
     if (threadIdx.x == 0) end_s = INT32_MAX;
     __syncthreads();
-    // the first block after b whose head ends the run
-    for (int e0 = b + 1; e0 < n_blocks; e0 += 1024) {
-        const int e = e0 + threadIdx.x;
-        if (e < n_blocks && state[e].head == HEAD_ENDS) atomicMin(&end_s, e);
+    for (int e0 = b + 1; e0 < n_blocks; e0 += JOIN_COLS * JOIN_SLICES) {
+        if (e0 != b + 1) {
+            e = e0 + threadIdx.x;
+            mine = e < n_blocks ? state[e].head : HEAD_NONE;
+        }
+        if (mine == HEAD_ENDS) atomicMin(&end_s, e);
         __syncthreads();
         const bool found = end_s != INT32_MAX;
         __syncthreads();
         if (found) break;
     }
     const int end = min(end_s, n_blocks - 1);
-    const int c = threadIdx.x & (COLS - 1), sl = threadIdx.x / COLS;
-    const int h = blockIdx.y * COLS + c;
+    const int c = threadIdx.x % JOIN_COLS, sl = threadIdx.x / JOIN_COLS;
+    const int h = blockIdx.y * JOIN_COLS + c;
     float s = 0.f;
     if (h < H) {
-#pragma unroll 4
-        for (int e = b + 1 + sl; e <= end; e += 4) s += head[(size_t)e * H + h];
+#pragma unroll 8
+        for (int e = b + 1 + sl; e <= end; e += JOIN_SLICES) s += head[(size_t)e * H + h];
     }
-    if (sl) red[sl - 1][c] = s;
+    red[sl][c] = s;
     __syncthreads();
-    if (sl == 0 && h < H) put(grad, (size_t)key * H + h, (tail[(size_t)b * H + h] + s) + (red[0][c] + (red[1][c] + red[2][c])), scale, accumulate);
+    if (sl || h >= H) return;
+    float sum = tail[(size_t)b * H + h];
+#pragma unroll
+    for (int i = 0; i < JOIN_SLICES; ++i) sum += red[i][c];
+    put(grad, (size_t)key * H + h, sum, scale, accumulate);
 }
+
+// Tokens per warp of embed_sum_kernel: 32 keep the pieces few; 8 spread few
+// tokens over more blocks.
+int tokens_per_warp(int T) { return T <= 16384 ? 8 : 32; }
 
 struct EmbedWs {
     Pair *buf0, *buf1;
@@ -427,7 +554,7 @@ struct EmbedWs {
 EmbedWs carve_embed(int T, int H, void* base) {
     WsCarve ws(base);
     EmbedWs w;
-    const size_t nb = ((size_t)T + TOKENS_PER_BLOCK - 1) / TOKENS_PER_BLOCK;
+    const size_t per = (size_t)SUM_WARPS * tokens_per_warp(T), nb = (T + per - 1) / per;
     w.buf0 = ws.take<Pair>(T);
     w.buf1 = ws.take<Pair>(T);
     w.state = ws.take<BlockState>(nb);
@@ -448,7 +575,9 @@ cudaError_t backward_t(const void* dy_, const int32_t* ids, void* grad_, int T, 
         static bool ready[TEE_MAX_DEVICES] = {};
         std::lock_guard<std::mutex> lock(mu);
         if (!ready[dev]) {
-            e = cudaFuncSetAttribute(embed_sort_fill_kernel<TG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            e = cudaFuncSetAttribute(embed_sort_kernel<TG>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e != cudaSuccess) return e;
+            e = cudaFuncSetAttribute(embed_sort_kernel<TG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      (int)sizeof(SortSmem));
             if (e != cudaSuccess) return e;
             ready[dev] = true;
@@ -457,37 +586,52 @@ cudaError_t backward_t(const void* dy_, const int32_t* ids, void* grad_, int T, 
     int key_bits = 1;
     while (key_bits < 32 && (V >> key_bits)) ++key_bits;   // keys 0 .. V
     const int passes = (key_bits + MAX_DIGIT_BITS - 1) / MAX_DIGIT_BITS;
-    const int fillers = accumulate ? 0 : max(1, num_sms / SORT_CTAS - 1) * SORT_CTAS;
-    if ((e = launch_pdl(embed_sort_fill_kernel<TG>, dim3(SORT_CTAS + fillers), dim3(SORT_THREADS), sizeof(SortSmem), s,
-                        ids, T, V, H, key_bits, w.buf0, w.buf1, grad, status)))
-        return e;
-    const Pair* sorted = passes & 1 ? w.buf0 : w.buf1;
-    const int nb = (T - 1) / TOKENS_PER_BLOCK + 1;
-    const dim3 grid(nb, (H + COLS - 1) / COLS);
-    if (H % 8 == 0)
-        e = launch_pdl(embed_sum_kernel<TY, TG, true>, grid, dim3(SUM_WARPS * 32), 0, s, dy, sorted, grad, T, V, H, scale,
-                       (int)accumulate, w.state, w.head, w.tail);
-    else
-        e = launch_pdl(embed_sum_kernel<TY, TG, false>, grid, dim3(SUM_WARPS * 32), 0, s, dy, sorted, grad, T, V, H, scale,
-                       (int)accumulate, w.state, w.head, w.tail);
+    // sorting by counting takes 4 us at 2048 tokens and 25 at 8192, by digits 13 and 14
+    const Pair* sorted = w.buf0;
+    int fill_rows = 0;   // rows zeroed beside the sort
+    if (T <= RANK_MAX_TOKENS) {
+        const int blocks = std::min((T - 1) / (RANK_THREADS / 32) + 1, num_sms);
+        e = launch_pdl(embed_rank_kernel, dim3(blocks), dim3(RANK_THREADS), (size_t)(T + 3) / 4 * 16, s, ids, T, V, w.buf0, status);
+    } else {
+        // as many as its time allows
+        const double sort_us = 8.0 + (double)T * passes / 16384;
+        fill_rows = accumulate ? 0 : (int)std::min((double)V, sort_us * 5e6 / ((double)H * sizeof(TG)));
+        e = launch_pdl(embed_sort_kernel<TG>, dim3(SORT_CTAS + (accumulate ? 0 : SORT_FILLERS)), dim3(SORT_THREADS),
+                       sizeof(SortSmem), s, ids, T, V, H, key_bits, w.buf0, w.buf1, grad, fill_rows, status);
+        if (!(passes & 1)) sorted = w.buf1;
+    }
+    if (e != cudaSuccess) return e;
+    const int per_warp = tokens_per_warp(T), nb = (T - 1) / (SUM_WARPS * per_warp) + 1;
+    // chunks of 32 rows, more where they are shorter than 64 KB
+    const int chunk_rows = 32 * (int)std::max<size_t>(1, std::min<size_t>(FLAG_WORDS, 2048 / ((size_t)H * sizeof(TG))));
+    const int chunks = accumulate ? 0 : (int)(((long long)V - fill_rows + chunk_rows - 1) / chunk_rows);
+    const dim3 grid((unsigned)((H + COLS - 1) / COLS * nb + chunks));
+    auto sum = [&](auto kernel) {
+        return launch_pdl(kernel, grid, dim3(SUM_WARPS * 32), 0, s, dy, sorted, grad, T, V, H, scale, (int)accumulate, nb,
+                          fill_rows, chunk_rows, w.state, w.head, w.tail);
+    };
+    constexpr int W = sizeof(TY) == 4 || sizeof(TG) == 4 ? 4 : 8;
+    if (H % W == 0) e = per_warp == 8 ? sum(embed_sum_kernel<TY, TG, W, 8>) : sum(embed_sum_kernel<TY, TG, W, 32>);
+    else e = per_warp == 8 ? sum(embed_sum_kernel<TY, TG, 1, 8>) : sum(embed_sum_kernel<TY, TG, 1, 32>);
     if (e != cudaSuccess || nb == 1) return e;   // one block: no run crosses blocks
-    return launch_pdl(embed_join_kernel<TG>, grid, dim3(1024), 0, s, (const BlockState*)w.state, nb, (const float*)w.head,
-                      (const float*)w.tail, grad, V, H, scale, (int)accumulate);
+    return launch_pdl(embed_join_kernel<TG>, dim3(nb, (H + JOIN_COLS - 1) / JOIN_COLS), dim3(JOIN_COLS * JOIN_SLICES), 0, s,
+                      (const BlockState*)w.state, nb, (const float*)w.head, (const float*)w.tail, grad, V, H, scale,
+                      (int)accumulate);
 }
 
 template <typename TE, typename TY>
 cudaError_t forward_t(const void* table, const int32_t* ids, void* y, int T, int V, int H, float scale,
                       unsigned int* status, cudaStream_t s) {
-    const bool vec = H % 8 == 0;
-    const int work = vec ? H / 8 : H;
+    constexpr int W = sizeof(TE) == 4 || sizeof(TY) == 4 ? 4 : 8;
+    const bool vec = H % W == 0;
+    const int work = vec ? H / W : H;
     int lane_bits = 0;
     while (lane_bits < 5 && (1 << lane_bits) < work) ++lane_bits;
     const dim3 grid((unsigned)((((long long)T << lane_bits) + 255) / 256));
-    if (vec)
-        return launch_pdl(embed_forward_kernel<TE, TY, true>, grid, dim3(256), 0, s, (const TE*)table, ids, (TY*)y, T, V, H,
-                          scale, lane_bits, status);
-    return launch_pdl(embed_forward_kernel<TE, TY, false>, grid, dim3(256), 0, s, (const TE*)table, ids, (TY*)y, T, V, H,
-                      scale, lane_bits, status);
+    auto go = [&](auto kernel) {
+        return launch_pdl(kernel, grid, dim3(256), 0, s, (const TE*)table, ids, (TY*)y, T, V, H, scale, lane_bits, status);
+    };
+    return vec ? go(embed_forward_kernel<TE, TY, W>) : go(embed_forward_kernel<TE, TY, 1>);
 }
 
 }  // namespace

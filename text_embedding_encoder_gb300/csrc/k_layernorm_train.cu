@@ -3,8 +3,7 @@
 //
 // Both are bound by HBM: forward reads x and writes y once, backward reads x,
 // dy (and the residual gradient) and writes dx once.  A row is held in the
-// registers of WPR warps (one up to 1024 columns), eight consecutive columns
-// per lane and chunk, so the variance is taken around the mean without reading
+// registers of WPR warps (one up to 1024 columns), so the variance is taken around the mean without reading
 // the row again.
 #include "train_internal.cuh"
 
@@ -15,40 +14,64 @@ constexpr int THREADS = 256, WARPS = THREADS / 32;
 // (four per SM on 152 SMs, rounded up).
 constexpr int BWD_MAX_GRID = 640;
 
-// How a row of H elements is spread over a group of G = 32 WPR lanes, VPL
-// chunks of eight elements each.  VEC (H % 8 == 0): a chunk is eight consecutive
-// elements, moved as 16-byte vectors; otherwise element by element, lanes
-// interleaved.
-template <bool VEC, int VPL, int WPR>
+// How a row of H elements is spread over a group of G = 32 WPR lanes, N elements
+// per lane: in runs of W consecutive ones, moved as vectors (4 where one of the
+// types is fp32 and H % 4 == 0, 8 where all are bf16 and H % 8 == 0), or W = 1,
+// element by element; the lanes' runs side by side.
+template <int W, int N_, int WPR>
 struct Row {
-    static constexpr int G = 32 * WPR, N = 8 * VPL;
-    static __device__ __forceinline__ int col(int k, int lg) { return VEC ? ((k >> 3) * G + lg) * 8 + (k & 7) : k * G + lg; }
-    static __device__ __forceinline__ bool has(int k, int lg, int H) { return col(VEC ? k & ~7 : k, lg) < H; }
+    static constexpr int G = 32 * WPR, N = N_;
+    static __device__ __forceinline__ int col(int k, int lg) { return (k / W * G + lg) * W + k % W; }
+    static __device__ __forceinline__ bool has(int k, int lg, int H) { return col(k / W * W, lg) < H; }
     template <typename T>
     static __device__ __forceinline__ void load(const T* row, int H, int lg, float (&v)[N]) {
-        if constexpr (VEC) {
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                if (has(8 * i, lg, H)) load8(row + col(8 * i, lg), v + 8 * i);
-                else
+        for (int k = 0; k < N; k += W) {
+            if constexpr (W == 1) {
+                v[k] = has(k, lg, H) ? elem_to_f32(row[col(k, lg)]) : 0.f;
+            } else {
+                float r[W] = {};
+                if (has(k, lg, H)) load_part(row + col(k, lg), r);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[8 * i + j] = 0.f;
+                for (int j = 0; j < W; ++j) v[k + j] = r[j];
             }
-        } else {
-#pragma unroll
-            for (int k = 0; k < N; ++k) v[k] = has(k, lg, H) ? elem_to_f32(row[col(k, lg)]) : 0.f;
         }
     }
     template <typename T>
     static __device__ __forceinline__ void store(T* row, int H, int lg, const float (&v)[N]) {
-        if constexpr (VEC) {
 #pragma unroll
-            for (int i = 0; i < VPL; ++i)
-                if (has(8 * i, lg, H)) store8(row + col(8 * i, lg), v + 8 * i);
+        for (int k = 0; k < N; k += W) {
+            if (!has(k, lg, H)) continue;
+            if constexpr (W == 1) {
+                f32_to_elem(v[k], row[col(k, lg)]);
+            } else {
+                float r[W];
+#pragma unroll
+                for (int j = 0; j < W; ++j) r[j] = v[k + j];
+                store_part(row + col(k, lg), r);
+            }
+        }
+    }
+    // eight fp32 elements (the gain and the partial sums of an all-bf16 norm) go as two vectors
+    template <typename T, int M>
+    static __device__ __forceinline__ void load_part(const T* p, float (&r)[M]) {
+        if constexpr (M == 8 && sizeof(T) == 4) {
+            float a[4], b[4];
+            load_vec(p, a);
+            load_vec(p + 4, b);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) r[j] = a[j], r[4 + j] = b[j];
         } else {
-#pragma unroll
-            for (int k = 0; k < N; ++k)
-                if (has(k, lg, H)) f32_to_elem(v[k], row[col(k, lg)]);
+            load_vec(p, r);
+        }
+    }
+    template <typename T, int M>
+    static __device__ __forceinline__ void store_part(T* p, const float (&r)[M]) {
+        if constexpr (M == 8 && sizeof(T) == 4) {
+            store_vec(p, {r[0], r[1], r[2], r[3]});
+            store_vec(p + 4, {r[4], r[5], r[6], r[7]});
+        } else {
+            store_vec(p, r);
         }
     }
 };
@@ -75,10 +98,10 @@ __device__ __forceinline__ float2 group_sum(float a, float b, float2* red) {
     return make_float2(a, b);
 }
 
-template <typename TX, typename TY, bool VEC, int VPL, int WPR>
+template <typename TX, typename TY, int W, int N, int WPR>
 __global__ void __launch_bounds__(THREADS) ln_forward_kernel(const TX* x, const float* __restrict__ gamma, TY* y,
                                                              float2* __restrict__ stats, int T, int H, float eps) {
-    using R = Row<VEC, VPL, WPR>;
+    using R = Row<W, N, WPR>;
     pdl_wait();
     pdl_trigger();
     __shared__ float2 red[2][WARPS];
@@ -112,11 +135,11 @@ __global__ void __launch_bounds__(THREADS) ln_forward_kernel(const TX* x, const 
 // Groups take rows blockIdx-strided; each lane keeps the gain's gradient of its
 // columns over all its rows, the block adds its groups' sums and writes one row
 // of partials, which ln_dgamma_kernel adds up in a fixed order.
-template <typename TX, typename TY, bool VEC, int VPL, int WPR>
+template <typename TX, typename TY, int W, int N, int WPR>
 __global__ void __launch_bounds__(THREADS)
     ln_backward_kernel(const TY* dy, const TX* x, const float* __restrict__ gamma, const float2* __restrict__ stats,
                        const TX* dres, TX* dx, float* __restrict__ partial, int T, int H) {
-    using R = Row<VEC, VPL, WPR>;
+    using R = Row<W, N, WPR>;
     constexpr int GROUPS = THREADS / R::G;
     extern __shared__ __align__(16) float acc[];   // GROUPS > 1: [GROUPS][H]
     pdl_wait();
@@ -199,25 +222,25 @@ __global__ void __launch_bounds__(1024) ln_dgamma_kernel(const float* __restrict
     if (cx == 0 && blockIdx.x * 32 + sl < H) dgamma[blockIdx.x * 32 + sl] = v;
 }
 
-// Calls f.template operator()<VEC, VPL, WPR>() with the row layout for H: the
-// fewest chunks per lane that hold the row in one warp up to 1024 columns, then
-// the fewest warps.
-template <typename F>
+// Calls f.template operator()<W, N, WPR>() with the row layout for H: the fewest
+// elements per lane that hold the row in one warp up to 1024 columns, then the
+// fewest warps.  V: vector width for the types.
+template <int V, typename F>
 cudaError_t with_layout(int H, F&& f) {
-    if (H % 8 == 0) {
-        if (H <= 256) return f.template operator()<true, 1, 1>();
-        if (H <= 512) return f.template operator()<true, 2, 1>();
-        if (H <= 768) return f.template operator()<true, 3, 1>();
-        if (H <= 1024) return f.template operator()<true, 4, 1>();
-        if (H <= 2048) return f.template operator()<true, 4, 2>();
-        if (H <= 4096) return f.template operator()<true, 4, 4>();
-        return f.template operator()<true, 4, 8>();
+    if (H % V == 0) {
+        if (H <= 256) return f.template operator()<V, 8, 1>();
+        if (H <= 512) return f.template operator()<V, 16, 1>();
+        if (H <= 768) return f.template operator()<V, 24, 1>();
+        if (H <= 1024) return f.template operator()<V, 32, 1>();
+        if (H <= 2048) return f.template operator()<V, 32, 2>();
+        if (H <= 4096) return f.template operator()<V, 32, 4>();
+        return f.template operator()<V, 32, 8>();
     }
-    if (H <= 256) return f.template operator()<false, 1, 1>();
-    if (H <= 1024) return f.template operator()<false, 4, 1>();
-    if (H <= 2048) return f.template operator()<false, 4, 2>();
-    if (H <= 4096) return f.template operator()<false, 4, 4>();
-    return f.template operator()<false, 4, 8>();
+    if (H <= 256) return f.template operator()<1, 8, 1>();
+    if (H <= 1024) return f.template operator()<1, 32, 1>();
+    if (H <= 2048) return f.template operator()<1, 32, 2>();
+    if (H <= 4096) return f.template operator()<1, 32, 4>();
+    return f.template operator()<1, 32, 8>();
 }
 
 template <typename TX, typename TY>
@@ -229,10 +252,10 @@ struct Forward {
     int T, H;
     float eps;
     cudaStream_t s;
-    template <bool VEC, int VPL, int WPR>
+    template <int W, int N, int WPR>
     cudaError_t operator()() const {
         const int rows = WARPS / WPR;
-        return launch_pdl(ln_forward_kernel<TX, TY, VEC, VPL, WPR>, dim3((T - 1) / rows + 1), dim3(THREADS), 0, s,
+        return launch_pdl(ln_forward_kernel<TX, TY, W, N, WPR>, dim3((T - 1) / rows + 1), dim3(THREADS), 0, s,
                           (const TX*)x, gamma, (TY*)y, reinterpret_cast<float2*>(stats), T, H, eps);
     }
 };
@@ -246,13 +269,13 @@ struct Backward {
     float *dgamma, *partial;
     int T, H, num_sms;
     cudaStream_t s;
-    template <bool VEC, int VPL, int WPR>
+    template <int W, int N, int WPR>
     cudaError_t operator()() const {
         constexpr int GROUPS = WARPS / WPR;
         // two resident blocks per SM: the three row buffers and the gradient sums fill half the registers each
         const int grid = min(min((T - 1) / GROUPS + 1, 2 * num_sms), BWD_MAX_GRID);
         const size_t smem = GROUPS > 1 ? (size_t)GROUPS * H * sizeof(float) : 0;   // at most 32 KB
-        cudaError_t e = launch_pdl(ln_backward_kernel<TX, TY, VEC, VPL, WPR>, dim3(grid), dim3(THREADS), smem, s,
+        cudaError_t e = launch_pdl(ln_backward_kernel<TX, TY, W, N, WPR>, dim3(grid), dim3(THREADS), smem, s,
                                    (const TY*)dy, (const TX*)x, gamma, reinterpret_cast<const float2*>(stats),
                                    (const TX*)dres, (TX*)dx, partial, T, H);
         if (e != cudaSuccess) return e;
@@ -275,10 +298,10 @@ cudaError_t launch_layernorm_forward(const void* x, bool x_bf16, const float* ga
                                      int T, int H, float eps, cudaStream_t s) {
     if (T == 0) return cudaSuccess;
     if (x_bf16)
-        return y_bf16 ? with_layout(H, Forward<bf16, bf16>{x, gamma, y, stats, T, H, eps, s})
-                      : with_layout(H, Forward<bf16, float>{x, gamma, y, stats, T, H, eps, s});
-    return y_bf16 ? with_layout(H, Forward<float, bf16>{x, gamma, y, stats, T, H, eps, s})
-                  : with_layout(H, Forward<float, float>{x, gamma, y, stats, T, H, eps, s});
+        return y_bf16 ? with_layout<8>(H, Forward<bf16, bf16>{x, gamma, y, stats, T, H, eps, s})
+                      : with_layout<4>(H, Forward<bf16, float>{x, gamma, y, stats, T, H, eps, s});
+    return y_bf16 ? with_layout<4>(H, Forward<float, bf16>{x, gamma, y, stats, T, H, eps, s})
+                  : with_layout<4>(H, Forward<float, float>{x, gamma, y, stats, T, H, eps, s});
 }
 
 cudaError_t launch_layernorm_backward(const void* dy, bool y_bf16, const void* x, bool x_bf16, const float* gamma,
@@ -290,8 +313,8 @@ cudaError_t launch_layernorm_backward(const void* dy, bool y_bf16, const void* x
     if (e != cudaSuccess) return e;
     float* partial = (float*)ws;
     if (x_bf16)
-        return y_bf16 ? with_layout(H, Backward<bf16, bf16>{dy, x, gamma, stats, dres, dx, dgamma, partial, T, H, num_sms, s})
-                      : with_layout(H, Backward<bf16, float>{dy, x, gamma, stats, dres, dx, dgamma, partial, T, H, num_sms, s});
-    return y_bf16 ? with_layout(H, Backward<float, bf16>{dy, x, gamma, stats, dres, dx, dgamma, partial, T, H, num_sms, s})
-                  : with_layout(H, Backward<float, float>{dy, x, gamma, stats, dres, dx, dgamma, partial, T, H, num_sms, s});
+        return y_bf16 ? with_layout<8>(H, Backward<bf16, bf16>{dy, x, gamma, stats, dres, dx, dgamma, partial, T, H, num_sms, s})
+                      : with_layout<4>(H, Backward<bf16, float>{dy, x, gamma, stats, dres, dx, dgamma, partial, T, H, num_sms, s});
+    return y_bf16 ? with_layout<4>(H, Backward<float, bf16>{dy, x, gamma, stats, dres, dx, dgamma, partial, T, H, num_sms, s})
+                  : with_layout<4>(H, Backward<float, float>{dy, x, gamma, stats, dres, dx, dgamma, partial, T, H, num_sms, s});
 }

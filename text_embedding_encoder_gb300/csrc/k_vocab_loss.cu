@@ -723,17 +723,17 @@ __global__ void __launch_bounds__(256) vocab_scatter_kernel(const float* __restr
     const int n = min(max(*r.count, 0), N), mt = (n + TILE - 1) / TILE;
     const int at = min(r.index[i], n - 1);
     const int slices = at < 0 ? 0 : dx_slices(mt, (H + TILE - 1) / TILE, pairs, acc_rows, n_mul);
-    for (int k = lane; k < H / 8; k += 32) {
-        float v[8] = {};
+    for (int k = lane; k < H / 4; k += 32) {
+        float v[4] = {};
         for (int s = 0; s < slices; ++s) {
-            float a[8];
-            load8(acc + ((size_t)s * mt * TILE + at) * H + 8 * k, a);
+            float a[4];
+            load_vec(acc + ((size_t)s * mt * TILE + at) * H + 4 * k, a);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] += a[j];
+            for (int j = 0; j < 4; ++j) v[j] += a[j];
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= slices ? gmax : 0.f;
-        store8(dx + (size_t)i * H + 8 * k, v);
+        for (int j = 0; j < 4; ++j) v[j] *= slices ? gmax : 0.f;
+        store_vec(dx + (size_t)i * H + 4 * k, v);
     }
 }
 

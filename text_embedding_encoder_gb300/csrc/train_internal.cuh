@@ -24,32 +24,44 @@ __device__ __forceinline__ float elem_to_f32(bf16 v) { return __bfloat162float(v
 __device__ __forceinline__ void f32_to_elem(float v, float& o) { o = v; }
 __device__ __forceinline__ void f32_to_elem(float v, bf16& o) { o = __float2bfloat16_rn(v); }
 
-// Eight consecutive elements at a 16-byte aligned address.
-__device__ __forceinline__ void load8(const float* p, float* v) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+// W consecutive elements at an address aligned to W elements (at most 16 bytes):
+// 8 bf16, or 4 of either type.  A warp whose lanes move 16 bytes each side by side
+// covers whole sectors with every instruction; eight fp32 elements a lane (32
+// bytes apart) would touch each sector twice (measured: 58 against 40 us for the
+// lookup's gradient sums of 65536 rows of 768).
+__device__ __forceinline__ void load_vec(const float* p, float (&v)[4]) {
+    const float4 a = *reinterpret_cast<const float4*>(p);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
 }
-__device__ __forceinline__ void load8(const bf16* p, float* v) {
+__device__ __forceinline__ void unpack_bf16x2(uint32_t w, float& a, float& b) {
+    a = __uint_as_float(w << 16);
+    b = __uint_as_float(w & 0xffff0000u);
+}
+__device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void load_vec(const bf16* p, float (&v)[4]) {
+    const uint2 q = *reinterpret_cast<const uint2*>(p);
+    unpack_bf16x2(q.x, v[0], v[1]);
+    unpack_bf16x2(q.y, v[2], v[3]);
+}
+__device__ __forceinline__ void load_vec(const bf16* p, float (&v)[8]) {
     const uint4 q = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    unpack_bf16x2(q.x, v[0], v[1]);
+    unpack_bf16x2(q.y, v[2], v[3]);
+    unpack_bf16x2(q.z, v[4], v[5]);
+    unpack_bf16x2(q.w, v[6], v[7]);
 }
-__device__ __forceinline__ void store8(float* p, const float* v) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+__device__ __forceinline__ void store_vec(float* p, const float (&v)[4]) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
 }
-__device__ __forceinline__ void store8(bf16* p, const float* v) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+__device__ __forceinline__ void store_vec(bf16* p, const float (&v)[4]) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+}
+__device__ __forceinline__ void store_vec(bf16* p, const float (&v)[8]) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                              pack_bf16x2(v[6], v[7]));
 }
 
 __device__ __forceinline__ float warp_sum_f32(float v) {
