@@ -364,3 +364,22 @@ def test_refusals_launch_nothing(enc):
     torch.cuda.synchronize()
     assert float(out.min()) == 5.0 and float(out.max()) == 5.0
     assert enc.device_status() == 0
+
+
+@pytest.mark.parametrize("n", [1, 2, 60, 127, 128])
+def test_few_positions_are_as_exact_as_the_output_type(enc, n):
+    """Up to 128 counted positions D keeps its second half of bits: the gradients' error is their own rounding."""
+    x, w, t, _ = _inputs(700, 1500, 256, live="all")
+    t[n:] = IGNORE
+    t = t[torch.randperm(700, device="cuda")].contiguous()
+    g = torch.full((700,), 1.0 / 3, device="cuda")
+    _, lse = loss_forward(enc, x, w, t)
+    dx, dw = loss_backward(enc, x, w, t, lse, g)
+    _check_backward(dx, dw, x, w, t, lse, g)
+    live = t != IGNORE
+    d = torch.exp(x[live].double() @ w.double().t() - lse[live].double()[:, None])
+    d.scatter_add_(1, t[live].long()[:, None], -torch.ones(n, 1, dtype=F64, device="cuda"))
+    d = d * g[live].double()[:, None]
+    # rounding alone is 2^-8 of the value at most, 2^-8 / sqrt 3 in the norm; 1.15 times that leaves 0.3 of it for D's
+    for got, want in ((dx[live], d @ w.double()), (dw, d.t() @ x[live].double())):
+        assert float((got.double() - want).norm()) <= 1.15 * 2.0 ** -8 / math.sqrt(3) * float(want.norm())

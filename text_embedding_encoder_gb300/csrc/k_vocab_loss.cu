@@ -54,9 +54,17 @@ constexpr float LOG2E = 1.4426950408889634f;
 // A tile's epilogue, in K steps of products.
 constexpr int EPILOGUE_K_STEPS = 6;
 
+// Up to so many counted positions are listed twice in the backward pass, once in
+// each half of the only row tile, which is no more work: the first gives D
+// rounded to bf16, the second what that left over.  With many positions the
+// roundings of D average out; with few, one of them (the target's entry, up to
+// 2^-8 off) could be most of a gradient's error.
+constexpr int FEW_ROWS = 128;
+
 // What vocab_rows_kernel prepares, and the kernels after it read.
 struct Rows {
-    int* count;             // counted positions
+    int* count;             // rows of x in use: the counted positions, and 128 more where `twice` is set
+    int* twice;             // (backward) see FEW_ROWS
     float* gmax;            // largest finite magnitude of their upstream gradients, 1 if that is 0 (backward)
     int32_t* list;          // [N] their positions, ascending
     int32_t* index;         // [N] a position's place in the list, or -1 (backward)
@@ -64,6 +72,7 @@ struct Rows {
     int32_t* target;        // [Np]
     float* lse2;            // [Np] lse / ln 2 (backward)
     float* ratio;           // [Np] upstream gradient / gmax (backward)
+    float* target_dot;      // [Np] x . w[target] in fp32 (forward)
 };
 
 // ---------------------------------------------------------------------------
@@ -75,27 +84,45 @@ struct Rows {
 // itself, so that no block waits for another (the targets are a few hundred KB
 // out of L2).  The last block also writes their number and zeroes the rest of
 // the last tile.  Forward (gloss NULL) zeroes the outputs of the positions that
-// are not counted; backward divides the upstream gradients by the largest.
+// are not counted and takes the target's logit in plain fp32; backward divides the
+// upstream gradients by the largest.
 constexpr int ROWS_THREADS = 512, ROWS_WARPS = ROWS_THREADS / 32;
+
+// Sum of eight products of bf16 pairs (each product exact in fp32).
+__device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float x0, x1, y0, y1;
+        unpack_bf16x2(x[i], x0, x1);
+        unpack_bf16x2(y[i], y0, y1);
+        s = fmaf(x0, y0, s);
+        s = fmaf(x1, y1, s);
+    }
+    return s;
+}
+
 __global__ void __launch_bounds__(ROWS_THREADS)
-    vocab_rows_kernel(const bf16* __restrict__ x, const int32_t* __restrict__ targets, const float* __restrict__ lse_in,
-                      const float* __restrict__ gloss, int N, int V, int H, int ignore_id, int slice, float* loss, float* lse,
+    vocab_rows_kernel(const bf16* __restrict__ x, const bf16* __restrict__ wt, const int32_t* __restrict__ targets,
+                      const float* __restrict__ lse_in, const float* __restrict__ gloss, int N, int V, int H, int ignore_id, int slice, float* loss, float* lse,
                       Rows r, unsigned int* status) {
-    __shared__ int warp_n[ROWS_WARPS];
+    __shared__ int warp_n[ROWS_WARPS], warp_all[ROWS_WARPS];
     __shared__ float warp_g[ROWS_WARPS];
     pdl_wait();
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int lo = blockIdx.x * slice, hi = min(N, lo + slice);
     auto counted = [&](int t) { return t >= 0 && t < V && t != ignore_id; };
-    // the counted positions before the slice, and (backward) the largest gradient of all
-    int n = 0;
+    // the counted positions before the slice, and (backward) all of them and their largest gradient
+    int n = 0, all = 0;
     float g = 0.f;
     const int upto = gloss ? N : lo;
 #pragma unroll 8
     for (int i = threadIdx.x; i < upto; i += ROWS_THREADS) {
         const bool live = counted(targets[i]);
         n += live && i < lo;
+        all += live;
         if (gloss) {
             const float a = fabsf(gloss[i]);
             if (live && a < INFINITY) g = fmaxf(g, a);
@@ -104,13 +131,16 @@ __global__ void __launch_bounds__(ROWS_THREADS)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         n += __shfl_xor_sync(0xffffffffu, n, o);
+        all += __shfl_xor_sync(0xffffffffu, all, o);
         g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
     }
-    if (lane == 0) warp_n[warp] = n, warp_g[warp] = g;
+    if (lane == 0) warp_n[warp] = n, warp_all[warp] = all, warp_g[warp] = g;
     __syncthreads();
     int at = 0;
+    all = 0;
 #pragma unroll
-    for (int w = 0; w < ROWS_WARPS; ++w) at += warp_n[w], g = fmaxf(g, warp_g[w]);
+    for (int w = 0; w < ROWS_WARPS; ++w) at += warp_n[w], all += warp_all[w], g = fmaxf(g, warp_g[w]);
+    const bool twice = gloss && all > 0 && all <= FEW_ROWS;
     const float gmax = g > 0.f ? g : 1.f;
     __syncthreads();
     for (int i0 = lo; i0 < hi; i0 += ROWS_THREADS) {   // (uniform: the block's barriers are inside)
@@ -129,10 +159,12 @@ __global__ void __launch_bounds__(ROWS_THREADS)
         }
         if (live) {
             r.list[place] = i;
-            r.target[place] = t;
-            if (gloss) {
-                r.lse2[place] = lse_in[i] * LOG2E;
-                r.ratio[place] = gloss[i] / gmax;
+            for (int c = place; c <= place + (twice ? FEW_ROWS : 0); c += FEW_ROWS) {
+                r.target[c] = t;
+                if (gloss) {
+                    r.lse2[c] = lse_in[i] * LOG2E;
+                    r.ratio[c] = gloss[i] / gmax;
+                }
             }
         }
         if (i < hi) {
@@ -143,32 +175,51 @@ __global__ void __launch_bounds__(ROWS_THREADS)
         const int first = __shfl_sync(0xffffffffu, place - __popc(m & ((1u << lane) - 1)), 0);
         unsigned left = m;
         for (int c = first; left; c += 4) {
-            int from[4];
+            int from[4], to[4];
             const int rows = min(4, __popc(left));
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                from[q] = left ? i0 + warp * 32 + __ffs(left) - 1 : 0;
+                const int at_lane = left ? __ffs(left) - 1 : 0;
+                from[q] = i0 + warp * 32 + at_lane;
+                to[q] = __shfl_sync(0xffffffffu, t, at_lane);
                 left &= left - 1;
             }
+            float dot[4] = {};
             for (int k = lane; k < H / 8; k += 32) {
                 uint4 v[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
                     if (q < rows) v[q] = reinterpret_cast<const uint4*>(x + (size_t)from[q] * H)[k];
+                if (!gloss) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (q < rows) dot[q] += dot8(v[q], reinterpret_cast<const uint4*>(wt + (size_t)to[q] * H)[k]);
+                }
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
-                    if (q < rows) reinterpret_cast<uint4*>(r.x + (size_t)(c + q) * H)[k] = v[q];
+                    if (q < rows) {
+                        reinterpret_cast<uint4*>(r.x + (size_t)(c + q) * H)[k] = v[q];
+                        if (twice) reinterpret_cast<uint4*>(r.x + (size_t)(c + q + FEW_ROWS) * H)[k] = v[q];
+                    }
+            }
+            if (!gloss) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float d = warp_sum_f32(dot[q]);
+                    if (q < rows && lane == 0) r.target_dot[c + q] = d;
+                }
             }
         }
         __syncthreads();
     }
     if (blockIdx.x != gridDim.x - 1) return;
     if (threadIdx.x == 0) {
-        *r.count = at;
-        if (gloss) *r.gmax = gmax;
+        *r.count = twice ? FEW_ROWS + at : at;
+        if (gloss) *r.gmax = gmax, *r.twice = twice;
     }
     const int end = (at + TILE - 1) / TILE * TILE;
     for (int c = at + warp; c < end; c += ROWS_WARPS) {
+        if (twice && c >= FEW_ROWS && c < FEW_ROWS + at) continue;
         for (int k = lane; k < H / 8; k += 32) reinterpret_cast<uint4*>(r.x + (size_t)c * H)[k] = make_uint4(0, 0, 0, 0);
         if (lane == 0) {
             r.target[c] = -1;
@@ -304,7 +355,7 @@ struct Walk {
 // all units of a kind at once: the level X is searched up to which the pairs
 // fill (a pair takes units while its work is below X), and what is left goes to
 // pairs that stand at X exactly.
-__global__ void __launch_bounds__(32) vocab_share_kernel(Rows r, int N, int V, int H, int piece, int pieces, int want_dx, int want_dw,
+__global__ void __launch_bounds__(32) vocab_share_kernel(Rows r, int Np, int V, int H, int piece, int pieces, int want_dx, int want_dw,
                                                          int pairs, int acc_rows, Share* shares) {
     pdl_wait();
     pdl_trigger();
@@ -312,7 +363,7 @@ __global__ void __launch_bounds__(32) vocab_share_kernel(Rows r, int N, int V, i
     const int i = blockIdx.x, lane = threadIdx.x;
     const int n_log = i < pieces ? min(piece, V - i * piece) : 0;
     const int n_mul = i > 0 ? min(piece, V - (i - 1) * piece) : 0;
-    const Tiles t = Tiles::of(min(max(*r.count, 0), N), H, n_log, n_mul, want_dx, want_dw, pairs, acc_rows);
+    const Tiles t = Tiles::of(min(max(*r.count, 0), Np), H, n_log, n_mul, want_dx, want_dw, pairs, acc_rows);
     const bool dx_first = t.k_slice > t.k_rows;
     int load[PER];
 #pragma unroll
@@ -534,6 +585,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
             }
         };
         const float gmax = BWD ? __ldcg(p.r.gmax) : 0.f;
+        const bool left_over = BWD && crank == 1 && __ldcg(p.r.twice);   // this CTA's rows: what the even CTA's rounding left
         for (int it = 0; !walk.done(); ++it) {
             const Unit w = walk.next(tiles);
             const int acc = it & 1, use = it >> 1;
@@ -543,8 +595,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
             // what the row needs, fetched while the products run
             float lse2 = 0.f, ratio = 0.f;
             int target = -1;
+            bool counted = false;
             if (!BWD || w.kind == LOGITS) {
-                target = p.r.target[row] - p.v_log - col0;     // within this warp's columns, if it is there
+                target = p.r.target[row];
+                counted = target >= 0;
+                target -= p.v_log + col0;                      // within this warp's columns, if it is there
                 if (BWD) lse2 = p.r.lse2[row], ratio = p.r.ratio[row];
             }
             if (!all(mbar_wait(bar(TFULL + acc), use & 1, abort_flag))) break;
@@ -619,7 +674,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                     }
                     // rows of padding are zero whatever the table holds
 #pragma unroll
-                    for (int j = 0; j < 64; ++j) v[c][j] = row < count ? v[c][j] * ratio : 0.f;
+                    for (int j = 0; j < 64; ++j) v[c][j] = counted ? v[c][j] * ratio : 0.f;
+                    if (left_over) {
+#pragma unroll
+                        for (int j = 0; j < 64; ++j) v[c][j] -= __bfloat162float(__float2bfloat16_rn(v[c][j]));
+                    }
                     box_free();
                     stage_row_bf16x64(stage, lane, v[c]);
                     send([&](uint32_t src) { tma_store_2d(&maps.d_out, src, col0 + 64 * c, row0); });
@@ -707,21 +766,28 @@ __global__ void __launch_bounds__(512) vocab_finish_kernel(const float2* __restr
     const double l = ((double)a.x + log2((double)a.y)) * 0.69314718055994530942;
     const int i = r.list[row];
     if ((unsigned)i >= (unsigned)N) return;
-    lse[i] = (float)l;
-    loss[i] = (float)(l - (double)target_logit[row]);
+    // The tensor cores' sums of H products are off by a few 2^-24 of the logit
+    // (6.5e-7 of the losses at H = 768, where plain fp32 measured 2.7e-7 and this 0.8e-7).  The target's
+    // logit counts most, alone and, where it is likely, in lse: both take its
+    // plain fp32 sum instead, lse by exchanging the one term.
+    const double mma = target_logit[row], dot = r.target_dot[row];
+    const double shift = exp(mma - l) * expm1(dot - mma);
+    const double fixed = shift > -0.5 && shift < 1e3 ? l + log1p(shift) : l;   // (not with infinities or NaN)
+    lse[i] = (float)fixed;
+    loss[i] = (float)(fixed - dot);
 }
 
 // dX of every position: gmax times the sum of its accumulators, or zeros.
 // n_mul: the columns of the first piece, whose products wrote every slice.
-__global__ void __launch_bounds__(256) vocab_scatter_kernel(const float* __restrict__ acc, Rows r, int N, int H, int n_mul,
+__global__ void __launch_bounds__(256) vocab_scatter_kernel(const float* __restrict__ acc, Rows r, int N, int Np, int H, int n_mul,
                                                             int acc_rows, int pairs, bf16* __restrict__ dx) {
     pdl_wait();
     pdl_trigger();
     const int i = (blockIdx.x * 256 + threadIdx.x) >> 5, lane = threadIdx.x & 31;
     if (i >= N) return;
     const float gmax = *r.gmax;
-    const int n = min(max(*r.count, 0), N), mt = (n + TILE - 1) / TILE;
-    const int at = min(r.index[i], n - 1);
+    const int n = min(max(*r.count, 0), Np), mt = (n + TILE - 1) / TILE;
+    const int at = min(r.index[i], n - 1), more = *r.twice ? FEW_ROWS : 0;
     const int slices = at < 0 ? 0 : dx_slices(mt, (H + TILE - 1) / TILE, pairs, acc_rows, n_mul);
     for (int k = lane; k < H / 4; k += 32) {
         float v[4] = {};
@@ -730,6 +796,11 @@ __global__ void __launch_bounds__(256) vocab_scatter_kernel(const float* __restr
             load_vec(acc + ((size_t)s * mt * TILE + at) * H + 4 * k, a);
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[j] += a[j];
+            if (more) {
+                load_vec(acc + ((size_t)s * mt * TILE + (at + more) % TILE) * H + 4 * k, a);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] += a[j];
+            }
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] *= slices ? gmax : 0.f;
@@ -769,11 +840,13 @@ LossWs carve_loss(int N, int V, int H, bool backward, void* base) {
     const int Np = round_up(N, TILE);
     w.r.count = ws.take<int>(1);
     w.r.gmax = ws.take<float>(1);
+    w.r.twice = ws.take<int>(1);
     w.r.list = ws.take<int32_t>(N);
     w.r.x = ws.take<bf16>((size_t)Np * H);
     w.r.target = ws.take<int32_t>(Np);
     if (!backward) {
         w.target_logit = ws.take<float>(Np);
+        w.r.target_dot = ws.take<float>(Np);
         w.part = ws.take<float2>((size_t)Np * ((V + TILE - 1) / TILE));
     } else {
         w.r.index = ws.take<int32_t>(N);
@@ -821,12 +894,12 @@ cudaError_t max_pairs(int dev, int num_sms, int* pairs) {
         if (e_ != cudaSuccess) return e_;   \
     } while (0)
 
-cudaError_t prepare_rows(const void* x, const int32_t* targets, const float* lse_in, const float* gloss, float* loss,
+cudaError_t prepare_rows(const void* x, const void* wt, const int32_t* targets, const float* lse_in, const float* gloss, float* loss,
                          float* lse, int N, int V, int H, int ignore_id, const LossWs& w, unsigned int* status, cudaStream_t s) {
     // a slice for each of 148 blocks, whole block steps at least
     const int slice = round_up(std::max(1, (N + 147) / 148), ROWS_THREADS / 2);
-    return launch_pdl(vocab_rows_kernel, dim3((N + slice - 1) / slice), dim3(ROWS_THREADS), 0, s, (const bf16*)x, targets,
-                      lse_in, gloss, N, V, H, ignore_id, slice, loss, lse, w.r, status);
+    return launch_pdl(vocab_rows_kernel, dim3((N + slice - 1) / slice), dim3(ROWS_THREADS), 0, s, (const bf16*)x,
+                      (const bf16*)wt, targets, lse_in, gloss, N, V, H, ignore_id, slice, loss, lse, w.r, status);
 }
 
 }  // namespace
@@ -851,7 +924,7 @@ cudaError_t launch_vocab_loss_forward(const void* x, const void* wt, const int32
     p.part = w.part;
     p.target_logit = w.target_logit;
     p.status = status;
-    TRY(prepare_rows(x, targets, nullptr, nullptr, loss, lse, N, V, H, ignore_id, w, status, s));
+    TRY(prepare_rows(x, wt, targets, nullptr, nullptr, loss, lse, N, V, H, ignore_id, w, status, s));
     const int grid = 2 * std::min(pairs, Np / TILE * tiles);
     TRY(launch_pdl(vocab_kernel<false>, dim3(grid), dim3(NUM_THREADS), SMEM_BYTES, s, maps, p));
     return launch_pdl(vocab_finish_kernel, dim3(round_up(N, 32) / 32), dim3(512), 0, s, (const float2*)w.part,
@@ -887,9 +960,9 @@ cudaError_t launch_vocab_loss_backward(const void* x, const void* wt, const int3
     p.want_dx = dx != nullptr, p.want_dw = dw != nullptr;
     p.acc_rows = acc_rows;
     p.status = status;
-    TRY(prepare_rows(x, targets, lse, gloss, nullptr, nullptr, N, V, H, ignore_id, w, status, s));
+    TRY(prepare_rows(x, wt, targets, lse, gloss, nullptr, nullptr, N, V, H, ignore_id, w, status, s));
     const int pieces = (V + vc - 1) / vc;
-    TRY(launch_pdl(vocab_share_kernel, dim3(pieces + 1), dim3(32), 0, s, w.r, N, V, H, vc, pieces, p.want_dx, p.want_dw, pairs,
+    TRY(launch_pdl(vocab_share_kernel, dim3(pieces + 1), dim3(32), 0, s, w.r, Np, V, H, vc, pieces, p.want_dx, p.want_dw, pairs,
                    acc_rows, w.shares));
     for (int i = 0; i <= pieces; ++i) {
         // logits of piece i into one buffer, products of piece i - 1 out of the other
@@ -904,6 +977,6 @@ cudaError_t launch_vocab_loss_backward(const void* x, const void* wt, const int3
         TRY(launch_pdl(vocab_kernel<true>, dim3(2 * pairs), dim3(NUM_THREADS), SMEM_BYTES, s, maps, p));
     }
     if (!dx) return cudaSuccess;
-    return launch_pdl(vocab_scatter_kernel, dim3(round_up(N, 8) / 8), dim3(256), 0, s, (const float*)w.acc, w.r, N, H,
+    return launch_pdl(vocab_scatter_kernel, dim3(round_up(N, 8) / 8), dim3(256), 0, s, (const float*)w.acc, w.r, N, Np, H,
                       std::min(vc, V), acc_rows, pairs, (bf16*)dx);
 }
