@@ -18,7 +18,7 @@
 //     (W in D W, both in D^T X) are read as they lie, as MN-major tiles.
 //   * A backward launch holds three kinds of independent tiles: D^T X and D W of
 //     one piece and the logits of the next, shared out among the CTA pairs by
-//     their length (vocab_share_kernel); D is double-buffered.
+//     their length (make_shares); D is double-buffered.
 //   * D is rounded to bf16 for the tensor cores, as the states and the table are.
 //     The upstream gradients enter it divided by their largest magnitude (put
 //     back in fp32 at the end), so that a gradient that all positions share does
@@ -52,7 +52,7 @@ static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
 constexpr uint32_t TMEM_COLS = 512;    // two accumulators of 256 columns
 constexpr float LOG2E = 1.4426950408889634f;
 // A tile's epilogue, in K steps of products.
-constexpr int EPILOGUE_K_STEPS = 6;
+constexpr int EPILOGUE_K_STEPS = 8;
 
 // Up to so many counted positions are listed twice in the backward pass, once in
 // each half of the only row tile, which is no more work: the first gives D
@@ -74,159 +74,6 @@ struct Rows {
     float* ratio;           // [Np] upstream gradient / gmax (backward)
     float* target_dot;      // [Np] x . w[target] in fp32 (forward)
 };
-
-// ---------------------------------------------------------------------------
-// before the products
-// ---------------------------------------------------------------------------
-
-// Lists the counted positions and copies their states together.  Each block has
-// a slice of the positions; it counts what is counted before its slice by
-// itself, so that no block waits for another (the targets are a few hundred KB
-// out of L2).  The last block also writes their number and zeroes the rest of
-// the last tile.  Forward (gloss NULL) zeroes the outputs of the positions that
-// are not counted and takes the target's logit in plain fp32; backward divides the
-// upstream gradients by the largest.
-constexpr int ROWS_THREADS = 512, ROWS_WARPS = ROWS_THREADS / 32;
-
-// Sum of eight products of bf16 pairs (each product exact in fp32).
-__device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
-    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float x0, x1, y0, y1;
-        unpack_bf16x2(x[i], x0, x1);
-        unpack_bf16x2(y[i], y0, y1);
-        s = fmaf(x0, y0, s);
-        s = fmaf(x1, y1, s);
-    }
-    return s;
-}
-
-__global__ void __launch_bounds__(ROWS_THREADS)
-    vocab_rows_kernel(const bf16* __restrict__ x, const bf16* __restrict__ wt, const int32_t* __restrict__ targets,
-                      const float* __restrict__ lse_in, const float* __restrict__ gloss, int N, int V, int H, int ignore_id, int slice, float* loss, float* lse,
-                      Rows r, unsigned int* status) {
-    __shared__ int warp_n[ROWS_WARPS], warp_all[ROWS_WARPS];
-    __shared__ float warp_g[ROWS_WARPS];
-    pdl_wait();
-    pdl_trigger();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int lo = blockIdx.x * slice, hi = min(N, lo + slice);
-    auto counted = [&](int t) { return t >= 0 && t < V && t != ignore_id; };
-    // the counted positions before the slice, and (backward) all of them and their largest gradient
-    int n = 0, all = 0;
-    float g = 0.f;
-    const int upto = gloss ? N : lo;
-#pragma unroll 8
-    for (int i = threadIdx.x; i < upto; i += ROWS_THREADS) {
-        const bool live = counted(targets[i]);
-        n += live && i < lo;
-        all += live;
-        if (gloss) {
-            const float a = fabsf(gloss[i]);
-            if (live && a < INFINITY) g = fmaxf(g, a);
-        }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        n += __shfl_xor_sync(0xffffffffu, n, o);
-        all += __shfl_xor_sync(0xffffffffu, all, o);
-        g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
-    }
-    if (lane == 0) warp_n[warp] = n, warp_all[warp] = all, warp_g[warp] = g;
-    __syncthreads();
-    int at = 0;
-    all = 0;
-#pragma unroll
-    for (int w = 0; w < ROWS_WARPS; ++w) at += warp_n[w], all += warp_all[w], g = fmaxf(g, warp_g[w]);
-    const bool twice = gloss && all > 0 && all <= FEW_ROWS;
-    const float gmax = g > 0.f ? g : 1.f;
-    __syncthreads();
-    for (int i0 = lo; i0 < hi; i0 += ROWS_THREADS) {   // (uniform: the block's barriers are inside)
-        const int i = i0 + threadIdx.x;
-        const int t = i < hi ? targets[i] : ignore_id;
-        const bool live = counted(t);
-        if (!live && t != ignore_id) atomicOr(status, TEE_STATUS_BAD_ID);
-        const unsigned m = __ballot_sync(0xffffffffu, live);
-        if (lane == 0) warp_n[warp] = __popc(m);
-        __syncthreads();
-        int place = at + __popc(m & ((1u << lane) - 1));
-#pragma unroll
-        for (int w = 0; w < ROWS_WARPS; ++w) {
-            place += w < warp ? warp_n[w] : 0;
-            at += warp_n[w];
-        }
-        if (live) {
-            r.list[place] = i;
-            for (int c = place; c <= place + (twice ? FEW_ROWS : 0); c += FEW_ROWS) {
-                r.target[c] = t;
-                if (gloss) {
-                    r.lse2[c] = lse_in[i] * LOG2E;
-                    r.ratio[c] = gloss[i] / gmax;
-                }
-            }
-        }
-        if (i < hi) {
-            if (gloss) r.index[i] = live ? place : -1;
-            else if (!live) loss[i] = lse[i] = 0.f;
-        }
-        // each warp copies the states of its own 32 positions, four at a time
-        const int first = __shfl_sync(0xffffffffu, place - __popc(m & ((1u << lane) - 1)), 0);
-        unsigned left = m;
-        for (int c = first; left; c += 4) {
-            int from[4], to[4];
-            const int rows = min(4, __popc(left));
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int at_lane = left ? __ffs(left) - 1 : 0;
-                from[q] = i0 + warp * 32 + at_lane;
-                to[q] = __shfl_sync(0xffffffffu, t, at_lane);
-                left &= left - 1;
-            }
-            float dot[4] = {};
-            for (int k = lane; k < H / 8; k += 32) {
-                uint4 v[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (q < rows) v[q] = reinterpret_cast<const uint4*>(x + (size_t)from[q] * H)[k];
-                if (!gloss) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        if (q < rows) dot[q] += dot8(v[q], reinterpret_cast<const uint4*>(wt + (size_t)to[q] * H)[k]);
-                }
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (q < rows) {
-                        reinterpret_cast<uint4*>(r.x + (size_t)(c + q) * H)[k] = v[q];
-                        if (twice) reinterpret_cast<uint4*>(r.x + (size_t)(c + q + FEW_ROWS) * H)[k] = v[q];
-                    }
-            }
-            if (!gloss) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float d = warp_sum_f32(dot[q]);
-                    if (q < rows && lane == 0) r.target_dot[c + q] = d;
-                }
-            }
-        }
-        __syncthreads();
-    }
-    if (blockIdx.x != gridDim.x - 1) return;
-    if (threadIdx.x == 0) {
-        *r.count = twice ? FEW_ROWS + at : at;
-        if (gloss) *r.gmax = gmax, *r.twice = twice;
-    }
-    const int end = (at + TILE - 1) / TILE * TILE;
-    for (int c = at + warp; c < end; c += ROWS_WARPS) {
-        if (twice && c >= FEW_ROWS && c < FEW_ROWS + at) continue;
-        for (int k = lane; k < H / 8; k += 32) reinterpret_cast<uint4*>(r.x + (size_t)c * H)[k] = make_uint4(0, 0, 0, 0);
-        if (lane == 0) {
-            r.target[c] = -1;
-            if (gloss) r.lse2[c] = r.ratio[c] = 0.f;
-        }
-    }
-}
 
 // ---------------------------------------------------------------------------
 // the products
@@ -349,21 +196,22 @@ struct Walk {
     }
 };
 
-// Shares of every backward launch, one warp each: launch i computes the logits
+// The pairs' shares of backward launch i, by one warp: launch i computes the logits
 // of piece i and multiplies D of piece i - 1.  Kind by kind, the longest units
 // first, each unit goes to the pair with the least work so far -- computed for
 // all units of a kind at once: the level X is searched up to which the pairs
 // fill (a pair takes units while its work is below X), and what is left goes to
 // pairs that stand at X exactly.
-__global__ void __launch_bounds__(32) vocab_share_kernel(Rows r, int Np, int V, int H, int piece, int pieces, int want_dx, int want_dw,
-                                                         int pairs, int acc_rows, Share* shares) {
-    pdl_wait();
-    pdl_trigger();
+struct ShareArgs {
+    int piece, pieces, want_dx, want_dw, pairs, acc_rows;
+    Share* shares;   // [pieces + 1][pairs]
+};
+__device__ void make_shares(const ShareArgs& a, int count, int V, int H, int i) {
     constexpr int PER = MAX_PAIRS / 32;   // pair j * 32 + lane
-    const int i = blockIdx.x, lane = threadIdx.x;
-    const int n_log = i < pieces ? min(piece, V - i * piece) : 0;
-    const int n_mul = i > 0 ? min(piece, V - (i - 1) * piece) : 0;
-    const Tiles t = Tiles::of(min(max(*r.count, 0), Np), H, n_log, n_mul, want_dx, want_dw, pairs, acc_rows);
+    const int lane = threadIdx.x & 31, pairs = a.pairs;
+    const int n_log = i < a.pieces ? min(a.piece, V - i * a.piece) : 0;
+    const int n_mul = i > 0 ? min(a.piece, V - (i - 1) * a.piece) : 0;
+    const Tiles t = Tiles::of(count, H, n_log, n_mul, a.want_dx, a.want_dw, pairs, a.acc_rows);
     const bool dx_first = t.k_slice > t.k_rows;
     int load[PER];
 #pragma unroll
@@ -380,14 +228,24 @@ __global__ void __launch_bounds__(32) vocab_share_kernel(Rows r, int Np, int V, 
 #pragma unroll
         for (int j = 0; j < PER; ++j) top = max(top, load[j] == INT32_MAX ? 0 : load[j]);
         top = __reduce_max_sync(0xffffffffu, top);
-        // at lo the pairs take at most `units` units, at hi more
-        long long lo = 0, hi = (long long)top + (long long)(units / pairs + 1) * cost + 1;
-        while (hi - lo > 1) {
-            const int mid = (int)((lo + hi) / 2);
+        // at lo the pairs take at most `units` units, at hi more; first the range in
+        // which X lies where no pair's work is above it
+        auto taken_by_all = [&](int x) {
             int f = 0;
 #pragma unroll
-            for (int j = 0; j < PER; ++j) f += taken(mid, j);
-            if (sum(f) <= units) lo = mid;
+            for (int j = 0; j < PER; ++j) f += taken(x, j);
+            return sum(f);
+        };
+        int before = 0;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) before += load[j] == INT32_MAX ? 0 : load[j];
+        const int even = (int)((sum(before) + (long long)units * cost) / pairs);
+        long long lo = max(0, even - cost - 1), hi = (long long)even + 1;
+        if (taken_by_all((int)lo) > units) lo = 0;
+        if (taken_by_all((int)hi) <= units) hi = (long long)top + (long long)(units / pairs + 1) * cost + 1;
+        while (hi - lo > 1) {
+            const int mid = (int)((lo + hi) / 2);
+            if (taken_by_all(mid) <= units) lo = mid;
             else hi = mid;
         }
         int k[PER], f = 0;
@@ -408,7 +266,7 @@ __global__ void __launch_bounds__(32) vocab_share_kernel(Rows r, int Np, int V, 
                 if (lane >= o) inc += up;
             }
             if (j * 32 + lane < pairs) {
-                Share& s = shares[i * pairs + j * 32 + lane];
+                Share& s = a.shares[i * pairs + j * 32 + lane];
                 s.first[kind] = first + inc - k[j];
                 s.n[kind] = k[j];
                 load[j] += k[j] * cost;
@@ -417,6 +275,167 @@ __global__ void __launch_bounds__(32) vocab_share_kernel(Rows r, int Np, int V, 
         }
     }
 }
+
+// ---------------------------------------------------------------------------
+// before the products
+// ---------------------------------------------------------------------------
+
+// Lists the counted positions and copies their states together.  Each block has
+// a slice of the positions; it counts what is counted before its slice by
+// itself, so that no block waits for another (the targets are a few hundred KB
+// out of L2).  The last slice's block also writes their number and zeroes the rest
+// of the last tile; backward has a block more for each product launch's shares.  Forward (gloss NULL) zeroes the outputs of the positions that
+// are not counted and takes the target's logit in plain fp32; backward divides the
+// upstream gradients by the largest.
+constexpr int ROWS_THREADS = 512, ROWS_WARPS = ROWS_THREADS / 32;
+
+// Sum of eight products of bf16 pairs (each product exact in fp32).
+__device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float x0, x1, y0, y1;
+        unpack_bf16x2(x[i], x0, x1);
+        unpack_bf16x2(y[i], y0, y1);
+        s = fmaf(x0, y0, s);
+        s = fmaf(x1, y1, s);
+    }
+    return s;
+}
+
+__global__ void __launch_bounds__(ROWS_THREADS)
+    vocab_rows_kernel(const bf16* __restrict__ x, const bf16* __restrict__ wt, const int32_t* __restrict__ targets,
+                      const float* __restrict__ lse_in, const float* __restrict__ gloss, int N, int V, int H, int ignore_id, int slice, float* loss, float* lse,
+                      Rows r, ShareArgs shares, unsigned int* status) {
+    __shared__ int warp_n[ROWS_WARPS], warp_all[ROWS_WARPS], from_s[ROWS_THREADS], to_s[ROWS_THREADS];
+    __shared__ float warp_g[ROWS_WARPS];
+    pdl_wait();
+    pdl_trigger();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int lo = blockIdx.x * slice, hi = min(N, lo + slice);
+    auto counted = [&](int t) { return t >= 0 && t < V && t != ignore_id; };
+    // the counted positions before the slice, and (backward) all of them and their largest gradient
+    int n = 0, all = 0;
+    float g = 0.f;
+    const int upto = gloss ? N : lo;
+#pragma unroll 8
+    for (int i = threadIdx.x; i < upto; i += ROWS_THREADS) {
+        const bool live = counted(targets[i]);
+        n += live && i < lo;
+        all += live;
+        if (gloss) {
+            const float a = fabsf(gloss[i]);
+            if (live && a < INFINITY) g = fmaxf(g, a);
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        n += __shfl_xor_sync(0xffffffffu, n, o);
+        all += __shfl_xor_sync(0xffffffffu, all, o);
+        g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+    }
+    if (lane == 0) warp_n[warp] = n, warp_all[warp] = all, warp_g[warp] = g;
+    __syncthreads();
+    int at = 0;
+    all = 0;
+#pragma unroll
+    for (int w = 0; w < ROWS_WARPS; ++w) at += warp_n[w], all += warp_all[w], g = fmaxf(g, warp_g[w]);
+    const bool twice = gloss && all > 0 && all <= FEW_ROWS;
+    if (lo >= N) {   // the blocks behind the slices: a launch's shares each
+        if (warp == 0) make_shares(shares, twice ? FEW_ROWS + all : all, V, H, (int)blockIdx.x - (N - 1) / slice - 1);
+        return;
+    }
+    const float gmax = g > 0.f ? g : 1.f;
+    __syncthreads();
+    for (int i0 = lo; i0 < hi; i0 += ROWS_THREADS) {   // (uniform: the block's barriers are inside)
+        const int i = i0 + threadIdx.x;
+        const int t = i < hi ? targets[i] : ignore_id;
+        const bool live = counted(t);
+        if (!live && t != ignore_id) atomicOr(status, TEE_STATUS_BAD_ID);
+        const unsigned m = __ballot_sync(0xffffffffu, live);
+        if (lane == 0) warp_n[warp] = __popc(m);
+        __syncthreads();
+        const int chunk0 = at;
+        int place = at + __popc(m & ((1u << lane) - 1));
+#pragma unroll
+        for (int w = 0; w < ROWS_WARPS; ++w) {
+            place += w < warp ? warp_n[w] : 0;
+            at += warp_n[w];
+        }
+        if (live) {
+            r.list[place] = i;
+            for (int c = place; c <= place + (twice ? FEW_ROWS : 0); c += FEW_ROWS) {
+                r.target[c] = t;
+                if (gloss) {
+                    r.lse2[c] = lse_in[i] * LOG2E;
+                    r.ratio[c] = gloss[i] / gmax;
+                }
+            }
+        }
+        if (i < hi) {
+            if (gloss) r.index[i] = live ? place : -1;
+            else if (!live) loss[i] = lse[i] = 0.f;
+        }
+        if (live) {
+            const int j = place - chunk0;
+            from_s[j] = i;
+            if (!gloss) to_s[j] = t;
+        }
+        __syncthreads();
+        // the block's warps copy the states, two rows at a time
+        const int rows = at - chunk0;
+        for (int j = 2 * warp; j < rows; j += 2 * ROWS_WARPS) {
+            const bool two = j + 1 < rows;
+            const uint4* src[2] = {reinterpret_cast<const uint4*>(x + (size_t)from_s[j] * H),
+                                   reinterpret_cast<const uint4*>(x + (size_t)from_s[two ? j + 1 : j] * H)};
+            uint4* dst = reinterpret_cast<uint4*>(r.x + (size_t)(chunk0 + j) * H);
+            const int row = H / 8, half = row * FEW_ROWS;   // (in vectors)
+            float dot[2] = {};
+#pragma unroll 4
+            for (int k = lane; k < row; k += 32) {
+                const uint4 v[2] = {src[0][k], src[1][k]};
+                if (!gloss) {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        dot[q] += dot8(v[q], reinterpret_cast<const uint4*>(wt + (size_t)to_s[q && two ? j + 1 : j] * H)[k]);
+                }
+                dst[k] = v[0];
+                if (two) dst[row + k] = v[1];
+                if (twice) {
+                    dst[half + k] = v[0];
+                    if (two) dst[half + row + k] = v[1];
+                }
+            }
+            if (!gloss) {
+                const float d0 = warp_sum_f32(dot[0]), d1 = warp_sum_f32(dot[1]);
+                if (lane == 0) {
+                    r.target_dot[chunk0 + j] = d0;
+                    if (two) r.target_dot[chunk0 + j + 1] = d1;
+                }
+            }
+        }
+        __syncthreads();
+    }
+    if (hi != N) return;
+    if (threadIdx.x == 0) {
+        *r.count = twice ? FEW_ROWS + at : at;
+        if (gloss) *r.gmax = gmax, *r.twice = twice;
+    }
+    const int end = (at + TILE - 1) / TILE * TILE;
+    for (int c = at + warp; c < end; c += ROWS_WARPS) {
+        if (twice && c >= FEW_ROWS && c < FEW_ROWS + at) continue;
+        for (int k = lane; k < H / 8; k += 32) reinterpret_cast<uint4*>(r.x + (size_t)c * H)[k] = make_uint4(0, 0, 0, 0);
+        if (lane == 0) {
+            r.target[c] = -1;
+            if (gloss) r.lse2[c] = r.ratio[c] = 0.f;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// the product kernel
+// ---------------------------------------------------------------------------
 
 template <bool BWD>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
@@ -679,6 +698,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
                         for (int j = 0; j < 64; ++j) v[c][j] -= __bfloat162float(__float2bfloat16_rn(v[c][j]));
                     }
+                    if (row0 >= tiles.k_rows * BK) continue;   // rows that D^T X does not reach; in D W they only reach themselves
                     box_free();
                     stage_row_bf16x64(stage, lane, v[c]);
                     send([&](uint32_t src) { tma_store_2d(&maps.d_out, src, col0 + 64 * c, row0); });
@@ -777,35 +797,43 @@ __global__ void __launch_bounds__(512) vocab_finish_kernel(const float2* __restr
     loss[i] = (float)(fixed - dot);
 }
 
-// dX of every position: gmax times the sum of its accumulators, or zeros.
-// n_mul: the columns of the first piece, whose products wrote every slice.
+// dX of every position: gmax times the sum of its accumulators, or zeros; four
+// columns per thread.  n_mul: the columns of the first piece, whose products wrote
+// every slice.
 __global__ void __launch_bounds__(256) vocab_scatter_kernel(const float* __restrict__ acc, Rows r, int N, int Np, int H, int n_mul,
                                                             int acc_rows, int pairs, bf16* __restrict__ dx) {
     pdl_wait();
     pdl_trigger();
-    const int i = (blockIdx.x * 256 + threadIdx.x) >> 5, lane = threadIdx.x & 31;
-    if (i >= N) return;
+    const size_t at4 = (size_t)blockIdx.x * 256 + threadIdx.x;
+    const int quads = H / 4, i = (int)(at4 / quads), k = (int)(at4 - (size_t)i * quads);
+    if (at4 >= (size_t)N * quads) return;
     const float gmax = *r.gmax;
     const int n = min(max(*r.count, 0), Np), mt = (n + TILE - 1) / TILE;
     const int at = min(r.index[i], n - 1), more = *r.twice ? FEW_ROWS : 0;
-    const int slices = at < 0 ? 0 : dx_slices(mt, (H + TILE - 1) / TILE, pairs, acc_rows, n_mul);
-    for (int k = lane; k < H / 4; k += 32) {
-        float v[4] = {};
+    float v[4] = {};
+    if (at >= 0) {
+        const int slices = dx_slices(mt, (H + TILE - 1) / TILE, pairs, acc_rows, n_mul);
+        const float* from = acc + (size_t)at * H + 4 * k;
+#pragma unroll 4
         for (int s = 0; s < slices; ++s) {
             float a[4];
-            load_vec(acc + ((size_t)s * mt * TILE + at) * H + 4 * k, a);
+            load_vec(from + (size_t)s * mt * TILE * H, a);
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[j] += a[j];
-            if (more) {
-                load_vec(acc + ((size_t)s * mt * TILE + (at + more) % TILE) * H + 4 * k, a);
+        }
+        if (more) {
+            from = acc + (size_t)((at + more) % TILE) * H + 4 * k;
+            for (int s = 0; s < slices; ++s) {
+                float a[4];
+                load_vec(from + (size_t)s * mt * TILE * H, a);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) v[j] += a[j];
             }
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] *= slices ? gmax : 0.f;
-        store_vec(dx + (size_t)i * H + 4 * k, v);
+        for (int j = 0; j < 4; ++j) v[j] *= gmax;
     }
+    store_vec(dx + (size_t)i * H + 4 * k, v);
 }
 
 // ---------------------------------------------------------------------------
@@ -895,11 +923,12 @@ cudaError_t max_pairs(int dev, int num_sms, int* pairs) {
     } while (0)
 
 cudaError_t prepare_rows(const void* x, const void* wt, const int32_t* targets, const float* lse_in, const float* gloss, float* loss,
-                         float* lse, int N, int V, int H, int ignore_id, const LossWs& w, unsigned int* status, cudaStream_t s) {
-    // a slice for each of 148 blocks, whole block steps at least
-    const int slice = round_up(std::max(1, (N + 147) / 148), ROWS_THREADS / 2);
-    return launch_pdl(vocab_rows_kernel, dim3((N + slice - 1) / slice), dim3(ROWS_THREADS), 0, s, (const bf16*)x,
-                      (const bf16*)wt, targets, lse_in, gloss, N, V, H, ignore_id, slice, loss, lse, w.r, status);
+                         float* lse, int N, int V, int H, int ignore_id, const LossWs& w, const ShareArgs& shares,
+                         unsigned int* status, cudaStream_t s) {
+    // a slice for each of 148 blocks, of 32 positions at least
+    const int slice = round_up(std::max(1, (N + 147) / 148), 32);
+    return launch_pdl(vocab_rows_kernel, dim3((N + slice - 1) / slice + (shares.pairs ? shares.pieces + 1 : 0)), dim3(ROWS_THREADS), 0, s, (const bf16*)x,
+                      (const bf16*)wt, targets, lse_in, gloss, N, V, H, ignore_id, slice, loss, lse, w.r, shares, status);
 }
 
 }  // namespace
@@ -924,7 +953,7 @@ cudaError_t launch_vocab_loss_forward(const void* x, const void* wt, const int32
     p.part = w.part;
     p.target_logit = w.target_logit;
     p.status = status;
-    TRY(prepare_rows(x, wt, targets, nullptr, nullptr, loss, lse, N, V, H, ignore_id, w, status, s));
+    TRY(prepare_rows(x, wt, targets, nullptr, nullptr, loss, lse, N, V, H, ignore_id, w, ShareArgs{}, status, s));
     const int grid = 2 * std::min(pairs, Np / TILE * tiles);
     TRY(launch_pdl(vocab_kernel<false>, dim3(grid), dim3(NUM_THREADS), SMEM_BYTES, s, maps, p));
     return launch_pdl(vocab_finish_kernel, dim3(round_up(N, 32) / 32), dim3(512), 0, s, (const float2*)w.part,
@@ -960,10 +989,9 @@ cudaError_t launch_vocab_loss_backward(const void* x, const void* wt, const int3
     p.want_dx = dx != nullptr, p.want_dw = dw != nullptr;
     p.acc_rows = acc_rows;
     p.status = status;
-    TRY(prepare_rows(x, wt, targets, lse, gloss, nullptr, nullptr, N, V, H, ignore_id, w, status, s));
     const int pieces = (V + vc - 1) / vc;
-    TRY(launch_pdl(vocab_share_kernel, dim3(pieces + 1), dim3(32), 0, s, w.r, Np, V, H, vc, pieces, p.want_dx, p.want_dw, pairs,
-                   acc_rows, w.shares));
+    const ShareArgs shares{vc, pieces, p.want_dx, p.want_dw, pairs, acc_rows, w.shares};
+    TRY(prepare_rows(x, wt, targets, lse, gloss, nullptr, nullptr, N, V, H, ignore_id, w, shares, status, s));
     for (int i = 0; i <= pieces; ++i) {
         // logits of piece i into one buffer, products of piece i - 1 out of the other
         p.v_log = i < pieces ? i * vc : 0;
@@ -977,6 +1005,6 @@ cudaError_t launch_vocab_loss_backward(const void* x, const void* wt, const int3
         TRY(launch_pdl(vocab_kernel<true>, dim3(2 * pairs), dim3(NUM_THREADS), SMEM_BYTES, s, maps, p));
     }
     if (!dx) return cudaSuccess;
-    return launch_pdl(vocab_scatter_kernel, dim3(round_up(N, 8) / 8), dim3(256), 0, s, (const float*)w.acc, w.r, N, Np, H,
+    return launch_pdl(vocab_scatter_kernel, dim3((unsigned)(((size_t)N * (H / 4) + 255) / 256)), dim3(256), 0, s, (const float*)w.acc, w.r, N, Np, H,
                       std::min(vc, V), acc_rows, pairs, (bf16*)dx);
 }
