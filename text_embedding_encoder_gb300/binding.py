@@ -143,14 +143,18 @@ def load(path: str | None = None) -> ctypes.CDLL:
     return lib
 
 
+# argument types that ctypes takes as they are
+_PLAIN = frozenset((int, float, bool, type(None)))
+
+
 def _ptr(a) -> int:
     """Device or host pointer of a torch tensor / numpy array / int."""
-    if a is None:
-        return None
-    if isinstance(a, int):
-        return a
     if hasattr(a, "data_ptr"):
         return a.data_ptr()
+    if a is None:
+        return None
+    if isinstance(a, (int, float)):
+        return a
     if isinstance(a, np.ndarray):
         if not a.flags.c_contiguous:
             raise ValueError("array must be C-contiguous")
@@ -267,8 +271,8 @@ class Encoder:
 
     # -- per-step entry points (tee_ops.h) ------------------------------
     def op(self, name, *args):
-        return self.check(getattr(self.lib, name)(self.ctx, *[_ptr(a) if not isinstance(a, (int, float)) else a
-                                                              for a in args]))
+        rc = getattr(self.lib, name)(self.ctx, *[a if a.__class__ in _PLAIN else _ptr(a) for a in args])
+        return rc if rc == TEE_OK else self.check(rc)
 
 
 def workspace_bytes(name: str, *sizes: int) -> int:

@@ -494,14 +494,14 @@ __global__ void __launch_bounds__(SUM_WARPS * 32, 3)   // three blocks an SM mea
 }
 
 // Block b adds the run that begins in block b of embed_sum_kernel and crosses
-// its end: tail of b, then the heads of b + 1 .. the block where the run ends, in
-// four slices of 64 columns.
-constexpr int JOIN_COLS = 64, JOIN_SLICES = 4;
-template <typename TG>
-__global__ void __launch_bounds__(JOIN_COLS* JOIN_SLICES)
+// its end: tail of b, then the heads of b + 1 .. the block where the run ends.
+// 64 threads side by side, W columns each, in four slices of the heads.
+constexpr int JOIN_LANES = 64, JOIN_SLICES = 4;
+template <typename TG, int W>
+__global__ void __launch_bounds__(JOIN_LANES* JOIN_SLICES)
     embed_join_kernel(const BlockState* __restrict__ state, int n_blocks, const float* __restrict__ head,
                       const float* __restrict__ tail, TG* __restrict__ grad, int V, int H, float scale, int accumulate) {
-    __shared__ float red[JOIN_SLICES][JOIN_COLS];
+    __shared__ float red[JOIN_SLICES - 1][JOIN_LANES][W];
     __shared__ int end_s;
     pdl_wait();
     pdl_trigger();
@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(JOIN_COLS* JOIN_SLICES)
     if (key >= (uint32_t)V) return;   // NO_KEY, or the run of out-of-range ids
     if (threadIdx.x == 0) end_s = INT32_MAX;
     __syncthreads();
-    for (int e0 = b + 1; e0 < n_blocks; e0 += JOIN_COLS * JOIN_SLICES) {
+    for (int e0 = b + 1; e0 < n_blocks; e0 += JOIN_LANES * JOIN_SLICES) {
         if (e0 != b + 1) {
             e = e0 + threadIdx.x;
             mine = e < n_blocks ? state[e].head : HEAD_NONE;
@@ -525,20 +525,42 @@ __global__ void __launch_bounds__(JOIN_COLS* JOIN_SLICES)
         if (found) break;
     }
     const int end = min(end_s, n_blocks - 1);
-    const int c = threadIdx.x % JOIN_COLS, sl = threadIdx.x / JOIN_COLS;
-    const int h = blockIdx.y * JOIN_COLS + c;
-    float s = 0.f;
+    const int c = threadIdx.x % JOIN_LANES, sl = threadIdx.x / JOIN_LANES;
+    const int h = (blockIdx.y * JOIN_LANES + c) * W;
+    auto load = [&](const float* p, float (&v)[W]) {
+        if constexpr (W == 1) v[0] = *p;
+        else load_vec(p, v);
+    };
+    float s[W] = {}, v[W];
     if (h < H) {
-#pragma unroll 8
-        for (int e = b + 1 + sl; e <= end; e += JOIN_SLICES) s += head[(size_t)e * H + h];
+        if (sl == 0) load(tail + (size_t)b * H + h, s);
+#pragma unroll 4
+        for (int k = b + 1 + sl; k <= end; k += JOIN_SLICES) {
+            load(head + (size_t)k * H + h, v);
+#pragma unroll
+            for (int j = 0; j < W; ++j) s[j] += v[j];
+        }
     }
-    red[sl][c] = s;
+    if (sl) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) red[sl - 1][c][j] = s[j];
+    }
     __syncthreads();
     if (sl || h >= H) return;
-    float sum = tail[(size_t)b * H + h];
 #pragma unroll
-    for (int i = 0; i < JOIN_SLICES; ++i) sum += red[i][c];
-    put(grad, (size_t)key * H + h, sum, scale, accumulate);
+    for (int i = 0; i < JOIN_SLICES - 1; ++i)
+#pragma unroll
+        for (int j = 0; j < W; ++j) s[j] += red[i][c][j];
+    TG* row = grad + (size_t)key * H + h;
+    if constexpr (W == 1) {
+        put(row, 0, s[0], scale, accumulate);
+    } else {
+        float o[W] = {};
+        if (accumulate) load_vec(row, o);
+#pragma unroll
+        for (int j = 0; j < W; ++j) o[j] = s[j] * scale + o[j];
+        store_vec(row, o);
+    }
 }
 
 // Tokens per warp of embed_sum_kernel: 32 keep the pieces few; 8 spread few
@@ -614,9 +636,11 @@ cudaError_t backward_t(const void* dy_, const int32_t* ids, void* grad_, int T, 
     if (H % W == 0) e = per_warp == 8 ? sum(embed_sum_kernel<TY, TG, W, 8>) : sum(embed_sum_kernel<TY, TG, W, 32>);
     else e = per_warp == 8 ? sum(embed_sum_kernel<TY, TG, 1, 8>) : sum(embed_sum_kernel<TY, TG, 1, 32>);
     if (e != cudaSuccess || nb == 1) return e;   // one block: no run crosses blocks
-    return launch_pdl(embed_join_kernel<TG>, dim3(nb, (H + JOIN_COLS - 1) / JOIN_COLS), dim3(JOIN_COLS * JOIN_SLICES), 0, s,
-                      (const BlockState*)w.state, nb, (const float*)w.head, (const float*)w.tail, grad, V, H, scale,
-                      (int)accumulate);
+    auto join = [&](auto kernel, int cols) {
+        return launch_pdl(kernel, dim3(nb, (H + cols - 1) / cols), dim3(JOIN_LANES * JOIN_SLICES), 0, s, (const BlockState*)w.state,
+                          nb, (const float*)w.head, (const float*)w.tail, grad, V, H, scale, (int)accumulate);
+    };
+    return H % 4 == 0 ? join(embed_join_kernel<TG, 4>, 4 * JOIN_LANES) : join(embed_join_kernel<TG, 1>, JOIN_LANES);
 }
 
 template <typename TE, typename TY>

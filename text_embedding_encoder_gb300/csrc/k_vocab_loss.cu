@@ -776,8 +776,15 @@ __global__ void __launch_bounds__(512) vocab_finish_kernel(const float2* __restr
         return make_float2(to, a.y * exp2f(a.x - to) + b.y * exp2f(b.x - to));
     };
     if (row < n) {
-#pragma unroll 4
-        for (int t = sl; t < tiles; t += 16) a = join(a, part[(size_t)t * Np + row]);
+        constexpr int AT_ONCE = 9;   // pairs on their way together
+        for (int t0 = sl; t0 < tiles; t0 += 16 * AT_ONCE) {
+            float2 v[AT_ONCE];
+#pragma unroll
+            for (int q = 0; q < AT_ONCE; ++q)
+                v[q] = t0 + 16 * q < tiles ? part[(size_t)(t0 + 16 * q) * Np + row] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int q = 0; q < AT_ONCE; ++q) a = join(a, v[q]);
+        }
     }
     red[sl][lane] = a;
     __syncthreads();
