@@ -143,13 +143,15 @@ def load(path: str | None = None) -> ctypes.CDLL:
     return lib
 
 
-# argument types that ctypes takes as they are
+# argument types that ctypes takes as they are, and types seen to have a data_ptr()
 _PLAIN = frozenset((int, float, bool, type(None)))
+_POINTED = set()
 
 
 def _ptr(a) -> int:
     """Device or host pointer of a torch tensor / numpy array / int."""
     if hasattr(a, "data_ptr"):
+        _POINTED.add(a.__class__)
         return a.data_ptr()
     if a is None:
         return None
@@ -271,7 +273,8 @@ class Encoder:
 
     # -- per-step entry points (tee_ops.h) ------------------------------
     def op(self, name, *args):
-        rc = getattr(self.lib, name)(self.ctx, *[a if a.__class__ in _PLAIN else _ptr(a) for a in args])
+        rc = getattr(self.lib, name)(self.ctx, *[a if a.__class__ in _PLAIN else
+                                                 a.data_ptr() if a.__class__ in _POINTED else _ptr(a) for a in args])
         return rc if rc == TEE_OK else self.check(rc)
 
 

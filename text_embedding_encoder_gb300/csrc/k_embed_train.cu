@@ -14,6 +14,11 @@
 //     memory and written, the pieces of runs that cross blocks are kept.  Blocks
 //     behind these zero the rest of the rows that no token has.
 //   embed_join_kernel  adds the pieces of each run that crosses blocks, in order.
+// Measured, 102400 x 768: 2048 tokens into a bf16 table 29.7 us (157 MB of zeros
+// alone take 24); 65536 tokens, 30 % of them one id, into an fp32 table 102 us
+// (sort 22, sums and zeros 73 at 5.6 TB/s of DRAM traffic -- a gather of the same
+// rows by themselves runs at 5.1 -- join 8).  The lookup forward, 32768 tokens of
+// which few ids are new, bf16 -> fp32: 19.5 us, the write of its output.
 #include "train_internal.cuh"
 
 #include <algorithm>
@@ -339,8 +344,8 @@ constexpr int SUM_BATCH = 4;   // rows a warp reads together
 // The first sum_blocks x (column groups) blocks add, the column groups of the same
 // tokens next to one another so that their rows are read together; the blocks
 // behind them zero the rows fill_from .. V that no token has, chunk_rows each (one
-// such block for every chunk: a few hundred with many chunks each took 10 us longer
-// for 315 MB).  Eight columns per lane in runs of W; each warp adds its tokens, and the warps' pieces of runs that
+// such block for every chunk: 256 with many chunks each took 10 us longer for 315
+// MB).  Eight columns per lane in runs of W; each warp adds its tokens, and the warps' pieces of runs that
 // cross warps are joined in shared memory.
 template <typename TY, typename TG, int W, int TOKENS_PER_WARP>
 __global__ void __launch_bounds__(SUM_WARPS * 32, 3)   // three blocks an SM measured best (64K tokens: 106 us for the call, 111 with two)

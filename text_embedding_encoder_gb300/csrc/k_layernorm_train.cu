@@ -3,8 +3,15 @@
 //
 // Both are bound by HBM: forward reads x and writes y once, backward reads x,
 // dy (and the residual gradient) and writes dx once.  A row is held in the
-// registers of WPR warps (one up to 1024 columns), so the variance is taken around the mean without reading
-// the row again.
+// registers of WPR warps (one up to 1024 columns), so the variance is taken
+// around the mean without reading the row again.
+//   forward, 65536 x 768 fp32 -> bf16: 43.9 us, 6.9 TB/s.
+//   backward, 32768 x 768 fp32, bf16 dy, residual: 60 us, 5.9 TB/s, of which 4 are
+//     the second launch.  Two blocks of eight warps an SM and the residual read
+//     late measured best (56 us a call in a stream; one block an SM 68, four 59,
+//     three with their registers cut to fit 69, the residual read with the rest 59
+//     to 68).
+// A few hundred rows are launch latency (backward: two launches).
 #include "train_internal.cuh"
 
 namespace {
@@ -203,8 +210,8 @@ __global__ void __launch_bounds__(THREADS)
 }
 
 // dgamma[h] = sum over the blocks' partials: eight columns per block, 64 slices of
-// the partials, added slice by slice.  (The launch is latency alone: 32 columns and
-// slices took 4.5 us for 304 partials of 768 columns.)
+// the partials, added slice by slice.  Latency alone: about 4 us for 304 partials of
+// 768 columns, with 24 blocks of 32 columns as with these 96.
 constexpr int DG_COLS = 8, DG_SLICES = 64;
 __global__ void __launch_bounds__(DG_COLS* DG_SLICES) ln_dgamma_kernel(const float* __restrict__ partial, int n, int H,
                                                                        float* __restrict__ dgamma) {
@@ -277,7 +284,7 @@ struct Backward {
     template <int W, int N, int WPR>
     cudaError_t operator()() const {
         constexpr int GROUPS = WARPS / WPR;
-        // two resident blocks per SM: the three row buffers and the gradient sums fill half the registers each
+        // two resident blocks per SM (see above): the row buffers and the gradient sums fill half the registers each
         const int grid = min(min((T - 1) / GROUPS + 1, 2 * num_sms), BWD_MAX_GRID);
         const size_t smem = GROUPS > 1 ? (size_t)GROUPS * H * sizeof(float) : 0;   // at most 32 KB
         cudaError_t e = launch_pdl(ln_backward_kernel<TX, TY, W, N, WPR>, dim3(grid), dim3(THREADS), smem, s,

@@ -8,7 +8,16 @@
 // again and become D = ratio (exp(logit - lse) - [target]) in bf16, from which
 // the next launch adds D W to dX (fp32) and writes that piece's D^T X to dW.
 // Work: 2 n V H flops forward, 6 n V H backward, n the counted positions.  Both
-// are bound by the tensor cores.
+// are bound by the tensor cores.  Measured at n = 9830 of 32768, V = 102400, H = 768:
+//   forward 0.81 to 0.88 ms, 1760 to 1910 TFLOP/s, the tensor pipes 95 to 97 % busy:
+//     the clock, under the power limit, sets the time.
+//   backward 3.0 to 3.1 ms, 1500 TFLOP/s; the pipes 79 % busy.  A piece's launch
+//     takes 106 us: products at 0.29 to 0.33 us a K step (0.27 is the pipes' rate at
+//     1.9 GHz), logits 4.0 us a tile instead of 3.3 -- their operands' way through
+//     shared memory, in and out again, already takes its whole bandwidth, and D's
+//     adds to it --, and 5 us from one launch's last store to the next one's first.
+// n = 315 of 1051: backward 0.18 ms.  One piece; DRAM moves 0.6 GB (the table twice,
+// D three times, dW), and the second tile of 256 rows holds 59.
 //
 //   * Positions that are not counted cost nothing: vocab_rows_kernel lists the
 //     others in order and copies their states together, and every later kernel
@@ -51,7 +60,8 @@ constexpr uint32_t SMEM_BYTES = BAR_OFF + N_BARS * 8 + 16 + 1024;   // + alignme
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
 constexpr uint32_t TMEM_COLS = 512;    // two accumulators of 256 columns
 constexpr float LOG2E = 1.4426950408889634f;
-// A tile's epilogue, in K steps of products.
+// A tile's epilogue, in K steps of products (2.4 us; 6 measured 196 us where this
+// takes 183, 10 and 12 the same).
 constexpr int EPILOGUE_K_STEPS = 8;
 
 // Up to so many counted positions are listed twice in the backward pass, once in
@@ -283,9 +293,10 @@ __device__ void make_shares(const ShareArgs& a, int count, int V, int H, int i) 
 // Lists the counted positions and copies their states together.  Each block has
 // a slice of the positions; it counts what is counted before its slice by
 // itself, so that no block waits for another (the targets are a few hundred KB
-// out of L2).  The last slice's block also writes their number and zeroes the rest
-// of the last tile; backward has a block more for each product launch's shares.  Forward (gloss NULL) zeroes the outputs of the positions that
-// are not counted and takes the target's logit in plain fp32; backward divides the
+// out of L2).  The last slice's block also writes their number and zeroes the
+// rest of the last tile; backward has a block more for each product launch's
+// shares.  Forward (gloss NULL) zeroes the outputs of the positions that are not
+// counted and takes the target's logit in plain fp32; backward divides the
 // upstream gradients by the largest.
 constexpr int ROWS_THREADS = 512, ROWS_WARPS = ROWS_THREADS / 32;
 
@@ -793,10 +804,10 @@ __global__ void __launch_bounds__(512) vocab_finish_kernel(const float2* __restr
     const double l = ((double)a.x + log2((double)a.y)) * 0.69314718055994530942;
     const int i = r.list[row];
     if ((unsigned)i >= (unsigned)N) return;
-    // The tensor cores' sums of H products are off by a few 2^-24 of the logit
-    // (6.5e-7 of the losses at H = 768, where plain fp32 measured 2.7e-7 and this 0.8e-7).  The target's
-    // logit counts most, alone and, where it is likely, in lse: both take its
-    // plain fp32 sum instead, lse by exchanging the one term.
+    // The tensor cores' sums of H products are off by a few 2^-24 of the logit.
+    // The target's logit counts most, alone and, where it is likely, in lse: both
+    // take its plain fp32 sum instead, lse by exchanging the one term (H = 768: the
+    // losses are 0.8e-7 off; 6.5e-7 without this, 2.7e-7 with fp32 products).
     const double mma = target_logit[row], dot = r.target_dot[row];
     const double shift = exp(mma - l) * expm1(dot - mma);
     const double fixed = shift > -0.5 && shift < 1e3 ? l + log1p(shift) : l;   // (not with infinities or NaN)
@@ -850,7 +861,9 @@ __global__ void __launch_bounds__(256) vocab_scatter_kernel(const float* __restr
 int round_up(int v, int a) { return (int)(((long long)v + a - 1) / a * a); }
 
 // Columns of a backward piece: D at most 256 MB for as many rows as there are
-// positions, 2048 columns at least.
+// positions, 2048 columns at least.  Smaller pieces keep D in L2 but their launches
+// cost more than that saves (128 MB: 3.2 against 3.1 ms at 32768 positions, 0.19
+// against 0.18 at 1051); 512 MB measured the same as 256.
 int piece_columns(int Np, int V) {
     const long long fit = (256LL << 20) / (2LL * Np) / TILE * TILE;
     return (int)std::min<long long>(std::max<long long>(fit, 2048), round_up(V, TILE));
