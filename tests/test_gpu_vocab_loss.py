@@ -231,6 +231,16 @@ def test_unbounded_table_row_reaches_no_other_row_of_dw(enc):
     assert bool(torch.isfinite(dw).all()) and torch.equal(dw[keep], want) and float(dw[5].abs().max()) == 0.0
 
 
+@pytest.mark.parametrize("N", [3, 300])
+@pytest.mark.parametrize("V", [65, 700, 4099])
+def test_all_logits_far_below_zero(enc, N, V):
+    """lse is near -150: behind the table's last row, where a tile's logits are 0, exp(0 - lse) would be infinite."""
+    x, w, t, g = _inputs(N, V, 64, live="all")
+    x, w = x.abs() + 0.5, -1.5 - w.abs()
+    _, lse, _, _ = _both(enc, x, w, t, g)
+    assert float(lse.max()) < -89.0
+
+
 def test_out_of_range_targets(enc):
     x, w, t, g = _inputs(60, 500, 64, live="all")
     clean = t.clone()

@@ -705,6 +705,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                     // rows of padding are zero whatever the table holds
 #pragma unroll
                     for (int j = 0; j < 64; ++j) v[c][j] = counted ? v[c][j] * ratio : 0.f;
+                    // and so are columns behind the table, where logits of 0 against an lse far below give infinities
+                    if (col0 + 64 * c + 64 > p.n_log) {
+#pragma unroll
+                        for (int j = 0; j < 64; ++j)
+                            if (col0 + 64 * c + j >= p.n_log) v[c][j] = 0.f;
+                    }
                     if (left_over) {
 #pragma unroll
                         for (int j = 0; j < 64; ++j) v[c][j] -= __bfloat162float(__float2bfloat16_rn(v[c][j]));
