@@ -400,3 +400,56 @@ def test_empty_calls_check_no_device_pointer(enc):
     f, s = KIND[F32], stream()
     enc.op("tee_op_layernorm_forward", None, f, None, None, f, None, 0, 24, 1e-5, s)
     enc.op("tee_op_embed_forward", None, f, None, None, f, 0, 12, 24, 1.0, s)
+
+
+# widths of each vector size (1, 2, 4, 8) on both sides of where the layout of a row changes
+MORE_WIDTHS = [130, 258, 260, 259, 511, 510, 513, 514, 516, 767, 770, 772, 776, 1023, 1022, 1020, 1025, 1026, 1028, 1532, 1534,
+               1538, 1540, 2049, 2050, 2052, 4095, 4094, 4092, 4097, 4098, 4100, 8190, 8191]
+
+
+@pytest.mark.parametrize("H", MORE_WIDTHS)
+def test_ln_layouts(enc, H):
+    for seed, (tx, ty) in enumerate(TYPES):
+        for T in (3, 61):
+            g = _gen(90000 + 100 * H + seed + T)
+            x = (_randn(g, T, H) * torch.exp(_randn(g, T, 1)) + 2 * _randn(g, T, 1)).to(tx)
+            gamma, dy = 1 + 0.3 * _randn(g, H), _randn(g, T, H).to(ty)
+            y, st = ln_forward(enc, x, gamma, ty)
+            _check_ln_forward(y, st, x, gamma, 1e-5)
+            res = _randn(g, T, H).to(tx) if T == 3 else None
+            dx, dgamma = ln_backward(enc, dy, x, gamma, st, res, guard=4096)
+            _check_ln_backward(dx, dgamma, dy, x, gamma, st, res)
+
+
+@pytest.mark.parametrize("T,H", [(20001, 251), (5001, 511), (3001, 770), (2501, 1001), (2001, 1537), (1500, 2050), (1301, 4095)])
+def test_ln_backward_many_rows_of_odd_widths(enc, T, H):
+    for tx, ty in TYPES:
+        g = _gen(T + H)
+        x, gamma, dy = _randn(g, T, H).to(tx), 1 + 0.3 * _randn(g, H), _randn(g, T, H).to(ty)
+        y, st = ln_forward(enc, x, gamma, ty)
+        _check_ln_forward(y, st, x, gamma, 1e-5)
+        dx, dgamma = ln_backward(enc, dy, x, gamma, st, guard=4096)
+        _check_ln_backward(dx, dgamma, dy, x, gamma, st, None)
+
+
+@pytest.mark.parametrize("H", [1, 2, 3, 5, 7, 8, 9, 17, 30, 33, 66, 130, 250, 258, 514, 999, 1001, 1030])
+def test_embed_of_any_width(enc, H):
+    """Vectors of every size, rows that begin anywhere in 16 bytes, chunks of many short rows; nothing behind the table."""
+    V = 3001
+    for seed, (ty, te) in enumerate(TYPES):
+        for T in (5, 700, 5000):
+            g = _gen(50000 + H + seed + T)
+            ids = _ids("heavy", T, V, g)
+            dy = _randn(g, T, H).to(ty)
+            buf = torch.full((V * H + 64,), 7.0, dtype=te, device="cuda")
+            grad = buf[:V * H].view(V, H)
+            ws, n = workspace("embed_backward", T, V, H)
+            enc.op("tee_op_embed_backward", dy, KIND[ty], ids, grad, KIND[te], T, V, H, 0.5, 0, ws, n, stream())
+            _check_embed_backward(grad, dy, ids, V, 0.5)
+            assert bool((buf[V * H:] == 7.0).all())
+            old = grad.clone()
+            embed_backward(enc, dy, ids, V, te, 0.5, into=grad)
+            _check_embed_backward(grad, dy, ids, V, 0.5, old=old)
+            table = _randn(g, V, H).to(te)
+            y = embed_forward(enc, table, ids, ty, 1.5)
+            assert torch.equal(y, (table[ids.long()].float() * 1.5).to(ty))

@@ -19,6 +19,15 @@ def test_workspace_sizes(built_lib):  # noqa: F811
     assert em(1 << 30, 1, 1) > 1 << 33                               # past 32 bits
 
 
+@pytest.mark.parametrize("H,rows", [(251, 8), (257, 4), (510, 8), (511, 4), (513, 2), (770, 4), (772, 4), (1001, 2), (1025, 1),
+                                    (1026, 2), (1536, 4), (1540, 2), (2050, 1), (4096, 1), (8191, 1)])
+def test_layernorm_workspace_holds_a_row_for_each_block(built_lib, H, rows):  # noqa: F811
+    """`rows` of the tensor to a block, as wide rows take several of its eight warps."""
+    for T in (1, rows, rows + 1, 100):
+        blocks = -(-T // rows)
+        assert built_lib.tee_layernorm_backward_workspace(T, H) == -(-blocks * H * 4 // 256) * 256
+
+
 @pytest.mark.parametrize("name,sizes", [
     ("layernorm_backward", (-1, 8)), ("layernorm_backward", (1, 0)), ("layernorm_backward", (1, 8193)),
     ("layernorm_backward", ((1 << 30) + 1, 8)), ("embed_backward", (-1, 5, 8)), ("embed_backward", (1, 0, 8)),

@@ -53,13 +53,15 @@ def ln_forward(enc, x, gamma, y_dtype, eps=1e-5, stats=True, y=None):
     return y, st
 
 
-def ln_backward(enc, dy, x, gamma, stats, res=None, dx=None):
+def ln_backward(enc, dy, x, gamma, stats, res=None, dx=None, guard=0):
+    """`guard`: that many bytes behind the workspace are checked to be left alone."""
     T, H = x.shape
     dx = torch.full((T, H), float("nan"), dtype=x.dtype, device="cuda") if dx is None else dx
     dgamma = torch.full((H,), float("nan"), device="cuda")
-    ws, n = workspace("layernorm_backward", T, H)
+    ws, n = workspace("layernorm_backward", T, H, slack=guard)
     enc.op("tee_op_layernorm_backward", dy, KIND[dy.dtype], x, KIND[x.dtype], gamma, stats, res, dx, dgamma, T, H,
            ws, n, stream())
+    assert not guard or bool((ws[n:] == 0xFF).all())
     return dx, dgamma
 
 

@@ -3,14 +3,14 @@
 //
 // Both are bound by HBM: forward reads x and writes y once, backward reads x,
 // dy (and the residual gradient) and writes dx once.  A row is held in the
-// registers of WPR warps (one up to 1024 columns), so the variance is taken
+// registers of WPR warps (with_width), so the variance is taken
 // around the mean without reading the row again.
 //   forward, 65536 x 768 fp32 -> bf16: 43.9 us, 6.9 TB/s.
 //   backward, 32768 x 768 fp32, bf16 dy, residual: 60 us, 5.9 TB/s, of which 4 are
-//     the second launch.  Two blocks of eight warps an SM and the residual read
-//     late measured best (56 us a call in a stream; one block an SM 68, four 59,
-//     three with their registers cut to fit 69, the residual read with the rest 59
-//     to 68).
+//     the second launch.
+// The backward pass holds a row of x, dy and the gain and the gain's sums at once, and
+// what it reaches goes with the rows in flight an SM (bwd_blocks); 210 MB of fp32
+// x, bf16 dy, dx: 82 to 87 us from 256 to 4096 columns, 6.1 to 6.4 TB/s; 111 at 1001.
 // A few hundred rows are launch latency (backward: two launches).
 #include "train_internal.cuh"
 
@@ -22,9 +22,11 @@ constexpr int THREADS = 256, WARPS = THREADS / 32;
 constexpr int BWD_MAX_GRID = 640;
 
 // How a row of H elements is spread over a group of G = 32 WPR lanes, N elements
-// per lane: in runs of W consecutive ones, moved as vectors (4 where one of the
-// types is fp32 and H % 4 == 0, 8 where all are bf16 and H % 8 == 0), or W = 1,
-// element by element; the lanes' runs side by side.
+// per lane: in runs of W consecutive ones, moved as vectors, or W = 1, element by
+// element; the lanes' runs side by side.  W is the largest of 8 (all types bf16),
+// 4, 2 and 1 that divides H.  (Odd widths by vectors that begin where the tensor's
+// alignment has them and are masked at the row's ends measured slower: forward 95
+// against 58 us, backward 157 against 111, 52376 x 1001.)
 template <int W, int N_, int WPR>
 struct Row {
     static constexpr int G = 32 * WPR, N = N_;
@@ -139,11 +141,25 @@ __global__ void __launch_bounds__(THREADS) ln_forward_kernel(const TX* x, const 
     if (stats && lg == 0) stats[t] = make_float2(mean, rstd);
 }
 
+// Backward: resident blocks an SM, which give the grid: as many as the row's N
+// elements a lane leave registers for.  Measured, us for 210 MB of fp32 x, bf16 dy and
+// dx: N = 8, four (251 columns: 101; three 118, six 134); 16, three (1024: 83; two 94);
+// 24, two (768: 87; three, with spills, 117).  With N = 32 two blocks spill and one
+// leaves the loads exposed (2048 columns: 95 and 136; four warps of 16 a lane 83).
+// Rows by single elements keep more addresses: 8 a lane (1001: 111; 16 a lane and
+// two blocks 140, 32 and one 495).
+template <int N>
+constexpr int bwd_blocks() { return N == 8 ? 4 : N == 16 ? 3 : 2; }
+// The same as a bound on the registers.  Two blocks of 24 elements a lane fit unasked
+// (asked for, two warps a row took 112 us instead of 86 at 1536 columns).
+template <int W, int N, int WPR>
+constexpr int bwd_min_blocks() { return W == 1 && N == 16 ? 2 : N == 24 && WPR == 2 ? 1 : bwd_blocks<N>(); }
+
 // Groups take rows blockIdx-strided; each lane keeps the gain's gradient of its
 // columns over all its rows, the block adds its groups' sums and writes one row
 // of partials, which ln_dgamma_kernel adds up in a fixed order.
 template <typename TX, typename TY, int W, int N, int WPR>
-__global__ void __launch_bounds__(THREADS)
+__global__ void __launch_bounds__(THREADS, bwd_min_blocks<W, N, WPR>())
     ln_backward_kernel(const TY* dy, const TX* x, const float* __restrict__ gamma, const float2* __restrict__ stats,
                        const TX* dres, TX* dx, float* __restrict__ partial, int T, int H) {
     using R = Row<W, N, WPR>;
@@ -234,29 +250,61 @@ __global__ void __launch_bounds__(DG_COLS* DG_SLICES) ln_dgamma_kernel(const flo
     if (lane == 0 && blockIdx.x * DG_COLS + w < H) dgamma[blockIdx.x * DG_COLS + w] = v;
 }
 
-// Calls f.template operator()<W, N, WPR>() with the row layout for H: the fewest
-// elements per lane that hold the row in one warp up to 1024 columns, then the
-// fewest warps.  V: vector width for the types.
-template <int V, typename F>
-cudaError_t with_layout(int H, F&& f) {
-    if (H % V == 0) {
-        if (H <= 256) return f.template operator()<V, 8, 1>();
-        if (H <= 512) return f.template operator()<V, 16, 1>();
-        if (H <= 768) return f.template operator()<V, 24, 1>();
-        if (H <= 1024) return f.template operator()<V, 32, 1>();
-        if (H <= 2048) return f.template operator()<V, 32, 2>();
-        if (H <= 4096) return f.template operator()<V, 32, 4>();
-        return f.template operator()<V, 32, 8>();
+// Warps per row in the backward pass; the layouts below are the ones that go with it.
+int backward_warps(int H) {
+    if (H % 2) return H <= 256 ? 1 : H <= 512 ? 2 : H <= 1024 ? 4 : 8;
+    if (H <= 512) return 1;
+    if (H % 4 == 0) {
+        if (H <= 768) return 1;
+        if (H <= 1536) return 2;
     }
-    if (H <= 256) return f.template operator()<1, 8, 1>();
-    if (H <= 1024) return f.template operator()<1, 32, 1>();
-    if (H <= 2048) return f.template operator()<1, 32, 2>();
-    if (H <= 4096) return f.template operator()<1, 32, 4>();
-    return f.template operator()<1, 32, 8>();
+    return H <= 1024 ? 2 : H <= 2048 ? 4 : 8;
+}
+
+// Calls f.template operator()<W, N, WPR>() with the row layout for H.  Forward holds
+// less per element and does better with few warps a row (2048 columns, fp32 to bf16:
+// 47.4 us with two, 48.0 with four); single elements want fewer a lane here too
+// (1001 columns bf16: 71 us with 16 a lane, 101 with 32, 75 with 8).
+template <int W, typename F>
+cudaError_t with_width(int H, const F& f) {
+    if (H <= 256) return f.template operator()<W, 8, 1>();
+    if constexpr (W == 1) {
+        if constexpr (F::BACKWARD) {
+            if (H <= 512) return f.template operator()<W, 8, 2>();
+            if (H <= 1024) return f.template operator()<W, 8, 4>();
+            if (H <= 2048) return f.template operator()<W, 8, 8>();
+        }
+    }
+    if constexpr (!F::BACKWARD || W > 1) {
+        if (H <= 512) return f.template operator()<W, 16, 1>();
+    }
+    if constexpr (W >= 4) {
+        if (H <= 768) return f.template operator()<W, 24, 1>();
+    }
+    constexpr bool SIXTEEN = F::BACKWARD || W == 1;
+    if constexpr (!(F::BACKWARD && W == 1)) {
+        if (H <= 1024) return f.template operator()<W, SIXTEEN ? 16 : 32, SIXTEEN ? 2 : 1>();
+        if constexpr (W >= 4) {
+            if (H <= 1536) return f.template operator()<W, 24, 2>();
+        }
+        if (H <= 2048) return f.template operator()<W, SIXTEEN ? 16 : 32, SIXTEEN ? 4 : 2>();
+    }
+    if (H <= 4096) return f.template operator()<W, SIXTEEN ? 16 : 32, SIXTEEN ? 8 : 4>();
+    return f.template operator()<W, 32, 8>();
+}
+// V: widest vector for the types.
+template <int V, typename F>
+cudaError_t with_layout(int H, const F& f) {
+    if (H % V == 0) return with_width<V>(H, f);
+    if constexpr (V == 8) {
+        if (H % 4 == 0) return with_width<4>(H, f);
+    }
+    return H % 2 == 0 ? with_width<2>(H, f) : with_width<1>(H, f);
 }
 
 template <typename TX, typename TY>
 struct Forward {
+    static constexpr bool BACKWARD = false;
     const void* x;
     const float* gamma;
     void* y;
@@ -274,6 +322,7 @@ struct Forward {
 
 template <typename TX, typename TY>
 struct Backward {
+    static constexpr bool BACKWARD = true;
     const void *dy, *x;
     const float *gamma, *stats;
     const void* dres;
@@ -284,8 +333,8 @@ struct Backward {
     template <int W, int N, int WPR>
     cudaError_t operator()() const {
         constexpr int GROUPS = WARPS / WPR;
-        // two resident blocks per SM (see above): the row buffers and the gradient sums fill half the registers each
-        const int grid = min(min((T - 1) / GROUPS + 1, 2 * num_sms), BWD_MAX_GRID);
+        if (WPR != backward_warps(H)) return cudaErrorInvalidValue;   // the workspace is sized by it
+        const int grid = min(min((T - 1) / GROUPS + 1, bwd_blocks<N>() * num_sms), BWD_MAX_GRID);
         const size_t smem = GROUPS > 1 ? (size_t)GROUPS * H * sizeof(float) : 0;   // at most 32 KB
         cudaError_t e = launch_pdl(ln_backward_kernel<TX, TY, W, N, WPR>, dim3(grid), dim3(THREADS), smem, s,
                                    (const TY*)dy, (const TX*)x, gamma, reinterpret_cast<const float2*>(stats),
@@ -299,7 +348,7 @@ struct Backward {
 }  // namespace
 
 size_t layernorm_backward_ws(int T, int H) {
-    const int groups = H <= 1024 ? 8 : H <= 2048 ? 4 : H <= 4096 ? 2 : 1;
+    const int groups = WARPS / backward_warps(H);
     const int grid = T < 1 ? 0 : min((T - 1) / groups + 1, BWD_MAX_GRID);
     WsCarve ws(nullptr);
     ws.take<float>((size_t)grid * H);

@@ -25,7 +25,7 @@ __device__ __forceinline__ void f32_to_elem(float v, float& o) { o = v; }
 __device__ __forceinline__ void f32_to_elem(float v, bf16& o) { o = __float2bfloat16_rn(v); }
 
 // W consecutive elements at an address aligned to W elements (at most 16 bytes):
-// 8 bf16, or 4 of either type.  A warp whose lanes move 16 bytes each side by side
+// 8 bf16, or 4 or 2 of either type.  A warp whose lanes move 16 bytes each side by side
 // covers whole sectors with every instruction; eight fp32 elements a lane (32
 // bytes apart) would touch each sector twice (measured: 58 against 40 us for the
 // lookup's gradient sums of 65536 rows of 768).
@@ -52,6 +52,19 @@ __device__ __forceinline__ void load_vec(const bf16* p, float (&v)[8]) {
     unpack_bf16x2(q.y, v[2], v[3]);
     unpack_bf16x2(q.z, v[4], v[5]);
     unpack_bf16x2(q.w, v[6], v[7]);
+}
+__device__ __forceinline__ void load_vec(const float* p, float (&v)[2]) {
+    const float2 a = *reinterpret_cast<const float2*>(p);
+    v[0] = a.x, v[1] = a.y;
+}
+__device__ __forceinline__ void load_vec(const bf16* p, float (&v)[2]) {
+    unpack_bf16x2(*reinterpret_cast<const uint32_t*>(p), v[0], v[1]);
+}
+__device__ __forceinline__ void store_vec(float* p, const float (&v)[2]) {
+    *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+}
+__device__ __forceinline__ void store_vec(bf16* p, const float (&v)[2]) {
+    *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(v[0], v[1]);
 }
 __device__ __forceinline__ void store_vec(float* p, const float (&v)[4]) {
     *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
