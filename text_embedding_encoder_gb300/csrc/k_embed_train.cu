@@ -23,6 +23,7 @@
 
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "tc_ptx.cuh"
 
@@ -243,16 +244,28 @@ __device__ __forceinline__ void zero_absent_rows(const Pair* __restrict__ sorted
         if (r < 32 * FLAG_WORDS) atomicOr(&flags[r >> 5], 1u << (r & 31));
     }
     __syncthreads();
+    // a row by a warp, or by the lanes it has work for: its 16-byte pieces, and what lies beside them where rows are no
+    // multiple of 16 bytes
     const size_t row_bytes = (size_t)H * sizeof(TG);
-    for (int r = warp; r < v_hi - v_lo; r += THREADS / 32) {
+    const uint32_t vecs = max(1u, (uint32_t)(row_bytes / 16));
+    const int lane_bits = vecs < 32 ? 32 - __clz(vecs - 1) : 5;   // (one: no bits)
+    const uint32_t first = threadIdx.x & ((1u << lane_bits) - 1), step = 1u << lane_bits;
+    for (int r = threadIdx.x >> lane_bits; r < v_hi - v_lo; r += THREADS >> lane_bits) {
         if (flags[r >> 5] >> (r & 31) & 1u) continue;
         TG* row = grad + (size_t)(v_lo + r) * H;
         if (row_bytes % 16 == 0) {
 #pragma unroll 6
-            for (uint32_t j = lane; j < (uint32_t)(row_bytes / 16); j += 32) reinterpret_cast<uint4*>(row)[j] = make_uint4(0, 0, 0, 0);
-        } else {
-            for (uint32_t j = lane; j < (uint32_t)H; j += 32) f32_to_elem(0.f, row[j]);
+            for (uint32_t j = first; j < vecs; j += step) reinterpret_cast<uint4*>(row)[j] = make_uint4(0, 0, 0, 0);
+            continue;
         }
+        // elements up to the first piece, pieces, elements behind the last one
+        const uint32_t before = min((uint32_t)H, (uint32_t)(-reinterpret_cast<uintptr_t>(row) & 15) / (uint32_t)sizeof(TG));
+        const uint32_t whole = (uint32_t)((row_bytes - before * sizeof(TG)) / 16);
+        TG* inner = row + before;
+#pragma unroll 6
+        for (uint32_t j = first; j < whole; j += step) reinterpret_cast<uint4*>(inner)[j] = make_uint4(0, 0, 0, 0);
+        for (uint32_t j = first; j < before; j += step) f32_to_elem(0.f, row[j]);
+        for (uint32_t j = before + whole * (16 / (uint32_t)sizeof(TG)) + first; j < (uint32_t)H; j += step) f32_to_elem(0.f, row[j]);
     }
 }
 
@@ -389,16 +402,26 @@ __global__ void __launch_bounds__(SUM_WARPS * 32, 3)   // three blocks an SM mea
         auto write = [&]() {   // a run that lies within this warp
             if (cur >= (uint32_t)V) return;
             TG* row = grad + (size_t)cur * H + col0;
+            // what is added to is read together, before anything is written
+#pragma unroll
+            for (int j0 = 0; j0 < 8; j0 += W) {
+                float v[W] = {};
+                if (accumulate && col0 + col(j0) < H) {
+                    if constexpr (W == 1) v[0] = elem_to_f32(row[col(j0)]);
+                    else load_vec(row + col(j0), v);
+                }
+#pragma unroll
+                for (int j = 0; j < W; ++j) acc[j0 + j] = acc[j0 + j] * scale + v[j];
+            }
 #pragma unroll
             for (int j0 = 0; j0 < 8; j0 += W) {
                 if (col0 + col(j0) >= H) continue;
                 if constexpr (W == 1) {
-                    put(row, col(j0), acc[j0], scale, accumulate);
+                    f32_to_elem(acc[j0], row[col(j0)]);
                 } else {
-                    float v[W] = {};
-                    if (accumulate) load_vec(row + col(j0), v);
+                    float v[W];
 #pragma unroll
-                    for (int j = 0; j < W; ++j) v[j] = acc[j0 + j] * scale + v[j];
+                    for (int j = 0; j < W; ++j) v[j] = acc[j0 + j];
                     store_vec(row + col(j0), v);
                 }
             }
@@ -568,6 +591,16 @@ __global__ void __launch_bounds__(JOIN_LANES* JOIN_SLICES)
     }
 }
 
+// f(the largest of 8 (both types bf16), 4, 2 and 1 elements that divides H).
+template <typename TA, typename TB, typename F>
+cudaError_t with_vectors(int H, F&& f) {
+    if constexpr (sizeof(TA) == 2 && sizeof(TB) == 2) {
+        if (H % 8 == 0) return f(std::integral_constant<int, 8>{});
+    }
+    if (H % 4 == 0) return f(std::integral_constant<int, 4>{});
+    return H % 2 == 0 ? f(std::integral_constant<int, 2>{}) : f(std::integral_constant<int, 1>{});
+}
+
 // Tokens per warp of embed_sum_kernel: 32 keep the pieces few; 8 spread few
 // tokens over more blocks.
 int tokens_per_warp(int T) { return T <= 16384 ? 8 : 32; }
@@ -637,9 +670,11 @@ cudaError_t backward_t(const void* dy_, const int32_t* ids, void* grad_, int T, 
         return launch_pdl(kernel, grid, dim3(SUM_WARPS * 32), 0, s, dy, sorted, grad, T, V, H, scale, (int)accumulate, nb,
                           fill_rows, chunk_rows, w.state, w.head, w.tail);
     };
-    constexpr int W = sizeof(TY) == 4 || sizeof(TG) == 4 ? 4 : 8;
-    if (H % W == 0) e = per_warp == 8 ? sum(embed_sum_kernel<TY, TG, W, 8>) : sum(embed_sum_kernel<TY, TG, W, 32>);
-    else e = per_warp == 8 ? sum(embed_sum_kernel<TY, TG, 1, 8>) : sum(embed_sum_kernel<TY, TG, 1, 32>);
+    auto sums = [&](auto width) {
+        constexpr int W = decltype(width)::value;
+        return per_warp == 8 ? sum(embed_sum_kernel<TY, TG, W, 8>) : sum(embed_sum_kernel<TY, TG, W, 32>);
+    };
+    e = with_vectors<TY, TG>(H, sums);
     if (e != cudaSuccess || nb == 1) return e;   // one block: no run crosses blocks
     auto join = [&](auto kernel, int cols) {
         return launch_pdl(kernel, dim3(nb, (H + cols - 1) / cols), dim3(JOIN_LANES * JOIN_SLICES), 0, s, (const BlockState*)w.state,
@@ -651,16 +686,14 @@ cudaError_t backward_t(const void* dy_, const int32_t* ids, void* grad_, int T, 
 template <typename TE, typename TY>
 cudaError_t forward_t(const void* table, const int32_t* ids, void* y, int T, int V, int H, float scale,
                       unsigned int* status, cudaStream_t s) {
-    constexpr int W = sizeof(TE) == 4 || sizeof(TY) == 4 ? 4 : 8;
-    const bool vec = H % W == 0;
-    const int work = vec ? H / W : H;
-    int lane_bits = 0;
-    while (lane_bits < 5 && (1 << lane_bits) < work) ++lane_bits;
-    const dim3 grid((unsigned)((((long long)T << lane_bits) + 255) / 256));
-    auto go = [&](auto kernel) {
-        return launch_pdl(kernel, grid, dim3(256), 0, s, (const TE*)table, ids, (TY*)y, T, V, H, scale, lane_bits, status);
-    };
-    return vec ? go(embed_forward_kernel<TE, TY, W>) : go(embed_forward_kernel<TE, TY, 1>);
+    return with_vectors<TE, TY>(H, [&](auto width) {
+        constexpr int W = decltype(width)::value;
+        int lane_bits = 0;
+        while (lane_bits < 5 && (1 << lane_bits) < H / W) ++lane_bits;
+        const dim3 grid((unsigned)((((long long)T << lane_bits) + 255) / 256));
+        return launch_pdl(embed_forward_kernel<TE, TY, W>, grid, dim3(256), 0, s, (const TE*)table, ids, (TY*)y, T, V, H, scale,
+                          lane_bits, status);
+    });
 }
 
 }  // namespace
