@@ -94,7 +94,8 @@ long long tee_embed_backward_workspace(int T, int V, int H);
  *   x bf16[N*H], w bf16[V*H], targets int32[N], loss and lse float[N];
  *   H a multiple of 8 in [8, TEE_VOCAB_MAX_HIDDEN]; 0 <= N <= 2^24,
  *   1 <= V <= 2^24, and ceil(N / 256) ceil(V / 256) <= 2^30.
- * A wait inside the products that does not end gives TEE_ETIMEOUT from the next
+ * Logits are fp32; those past 2^127 in magnitude count as infinite.  A wait inside
+ * the products that does not end gives TEE_ETIMEOUT from the next
  * tee_device_status, as in the tensor-core projections. */
 #define TEE_VOCAB_MAX_HIDDEN 8192
 int tee_op_vocab_loss_forward(tee_ctx* ctx, const void* d_x, const void* d_w, const int32_t* d_targets, float* d_loss,

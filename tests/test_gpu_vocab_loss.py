@@ -217,6 +217,19 @@ def test_minus_infinity_logits(enc):
     assert bool(torch.isfinite(loss).all())
 
 
+def test_infinite_logits(enc):
+    """A logit of +inf makes its row's lse and loss infinite, whatever the other logits are and wherever it stands."""
+    for v in (5, 70, 300, 699):
+        x, w, t, _ = _inputs(40, 700, 64, live="all")
+        x = x.abs() + 0.5
+        w[v] = float("inf")
+        w[(v + 64) % 700] = 30.0                            # logits past 1000 in another part of the row
+        w[(v + 128) % 700] = 40.0
+        t = torch.where(t == v, torch.full_like(t, (v + 1) % 700), t)
+        loss, lse = loss_forward(enc, x, w, t)
+        assert bool((lse == float("inf")).all()) and bool((loss == float("inf")).all())
+
+
 def test_unbounded_table_row_reaches_no_other_row_of_dw(enc):
     """With a table row of -inf the padding behind the last counted position has no defined logits; it adds nothing."""
     x, w, t, g = _inputs(40, 700, 64, live="all")

@@ -35,6 +35,8 @@
 #include "gemm_tc.cuh"
 #include "train_internal.cuh"
 
+#include <float.h>
+
 #include <algorithm>
 #include <mutex>
 #include <type_traits>
@@ -47,8 +49,16 @@ using namespace tc;
 
 constexpr int TILE = 256;              // rows and columns of a tile (a CTA holds 128 of the rows)
 constexpr int BK = 64;
-constexpr int EPI_WARPS = 8;           // two per quarter of the accumulator's rows, 128 columns each
-constexpr int NUM_THREADS = 64 + 32 * EPI_WARPS;
+// A set of epilogue warps has two per quarter of the accumulator's rows, 128 columns
+// each.  Forward has two sets, for every other tile each, so that one's loads and
+// maxima run beside the other's exponentials: below 400 columns the epilogue is the
+// longer part (9830 x 102400: H = 128 281 us with two sets, 411 with one; 384 451
+// and 480; 768 820 and 814).  Backward measured no better with two: a box for each warp
+// costs a stage of the operands (H = 768: 3.03 ms with two, 2.97 with one; 384 1.85
+// and 1.89).
+constexpr int EPI_WARPS = 8;
+constexpr int epi_sets(bool bwd) { return bwd ? 1 : 2; }
+constexpr int num_threads(bool bwd) { return 64 + 32 * EPI_WARPS * epi_sets(bwd); }
 constexpr int MAX_PAIRS = 128;         // CTA pairs of a launch
 constexpr uint32_t HALF_BYTES = 128 * BK * 2;          // this CTA's half of one operand's K step
 constexpr uint32_t STAGE_BYTES = 2 * HALF_BYTES;
@@ -449,7 +459,7 @@ __global__ void __launch_bounds__(ROWS_THREADS)
 // ---------------------------------------------------------------------------
 
 template <bool BWD>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(num_threads(BWD), 1)
     vocab_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -599,9 +609,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
             mbar_wait_drain(bar(MMA_DONE), 0);
         }
     } else {
-        // ---------------- epilogue: thread = row, warps 2..5 columns 0..127, warps 6..9 the others ----------------
-        const int quad = warp & 3, half = (warp - 2) >> 2;
-        uint8_t* stage = smem + OUT_OFF + (warp - 2) * 4096;   // this warp's staging box
+        // ---------------- epilogue: thread = row, warps 2..5 columns 0..127, warps 6..9 the others; 10..17 as well ----------------
+        const int quad = warp & 3, half = (warp - 2) >> 2 & 1, set = (warp - 2) / EPI_WARPS;
+        uint8_t* stage = smem + OUT_OFF + (warp - 2) % EPI_WARPS * 4096;   // (backward) this warp's staging box
         auto box_free = [&]() {   // the box's last store has read it
             if (lane == 0) bulk_wait_read<0>();
             __syncwarp();
@@ -619,6 +629,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         for (int it = 0; !walk.done(); ++it) {
             const Unit w = walk.next(tiles);
             const int acc = it & 1, use = it >> 1;
+            if (!BWD && acc != set) continue;
             const int row0 = w.m * TILE + (int)crank * 128 + quad * 32, row = row0 + lane;
             const int col0 = w.n * TILE + half * 128;          // this warp's first column of the output
             const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + acc * TILE + half * 128;
@@ -634,48 +645,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
             }
             if (!all(mbar_wait(bar(TFULL + acc), use & 1, abort_flag))) break;
             tc_fence_after();
-            // the accumulator is free once both loads are in registers
-            float v[2][64];
-            tmem_ld64_issue(taddr, v[0]);
-            tmem_ld64_issue(taddr + 64, v[1]);
-            tmem_wait_ld();
-            tmem_tie64(v[0]);
-            tmem_tie64(v[1]);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(tempty0 + 8 * acc);
             if constexpr (!BWD) {
-                float top = -INFINITY, ref = -INFINITY, sum = 0.f;
+                // 64 columns at a time, to a reference exponent and a sum
+                float ref = -INFINITY, sum = 0.f;
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
+                    float v[64];
+                    tmem_ld64(taddr + 64 * c, v);
+                    if (c) {   // the accumulator is free
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(tempty0 + 8 * acc);
+                    }
                     if (col0 + 64 * c + 64 > p.V) {
 #pragma unroll
                         for (int j = 0; j < 64; ++j)
-                            if (col0 + 64 * c + j >= p.V) v[c][j] = -INFINITY;
+                            if (col0 + 64 * c + j >= p.V) v[j] = -INFINITY;
                     }
                     const int tj = target - 64 * c;
                     if (__any_sync(0xffffffffu, tj >= 0 && tj < 64)) {
                         float tv = 0.f;
 #pragma unroll
-                        for (int j = 0; j < 64; ++j) tv = j == tj ? v[c][j] : tv;
+                        for (int j = 0; j < 64; ++j) tv = j == tj ? v[j] : tv;
                         if (tj >= 0 && tj < 64) p.target_logit[row] = tv;
                     }
-                    float mx[4] = {v[c][0], v[c][1], v[c][2], v[c][3]};
+                    float mx[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
                     for (int j = 4; j < 64; j += 8)   // (the last step's upper half repeats its lower one)
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) mx[q] = fmax3(mx[q], v[c][j + q], v[c][j + 4 < 64 ? j + 4 + q : j + q]);
-                    top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+                        for (int q = 0; q < 4; ++q) mx[q] = fmax3(mx[q], v[j + q], v[j + 4 < 64 ? j + 4 + q : j + q]);
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    // exponentials are taken against the maximum so far, kept finite (infinity against infinity would give NaN)
+                    const float mine = top == -INFINITY ? -INFINITY : fminf(fmaxf(top * LOG2E, -FLT_MAX), FLT_MAX);
+                    const float both = fmaxf(ref, mine), to = both == -INFINITY ? 0.f : both;
+                    float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) s4[j & 3] += ex2_approx(fmaf(v[j], LOG2E, -to));
+                    const float s1 = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+                    sum = c && both != -INFINITY ? fmaf(sum, ex2_approx(ref - both), s1) : sum + s1;
+                    ref = both;
                 }
-                // exponentials are taken against the maximum; one that is infinite would give NaN
-                const float to = isinf(top) ? 0.f : top * LOG2E;
-                float s4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int j = 0; j < 64; ++j) s4[j & 3] += ex2_approx(fmaf(v[c][j], LOG2E, -to));
-                sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
-                ref = top == -INFINITY ? -INFINITY : to;
                 // the two warps of a row join through shared memory.  Four slots: a
                 // slot comes round again after its tile's fourth successor has been
                 // multiplied, which waits for this row's warps to have left the second
@@ -692,7 +701,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                     else sum += o.y;
                     if (row < count) p.part[(size_t)w.n * p.Np + row] = make_float2(both, sum);
                 }
-            } else if (w.kind == LOGITS) {
+                continue;
+            }
+            // the accumulator is free once both loads are in registers
+            float v[2][64];
+            tmem_ld64_issue(taddr, v[0]);
+            tmem_ld64_issue(taddr + 64, v[1]);
+            tmem_wait_ld();
+            tmem_tie64(v[0]);
+            tmem_tie64(v[1]);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(tempty0 + 8 * acc);
+            if (w.kind == LOGITS) {
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
 #pragma unroll
@@ -925,7 +946,7 @@ cudaError_t max_pairs(int dev, int num_sms, int* pairs) {
         if (e != cudaSuccess) return e;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(num_sms / 2 * 2);
-        cfg.blockDim = dim3(NUM_THREADS);
+        cfg.blockDim = dim3(num_threads(BWD));
         cfg.dynamicSmemBytes = SMEM_BYTES;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -981,7 +1002,7 @@ cudaError_t launch_vocab_loss_forward(const void* x, const void* wt, const int32
     p.status = status;
     TRY(prepare_rows(x, wt, targets, nullptr, nullptr, loss, lse, N, V, H, ignore_id, w, ShareArgs{}, status, s));
     const int grid = 2 * std::min(pairs, Np / TILE * tiles);
-    TRY(launch_pdl(vocab_kernel<false>, dim3(grid), dim3(NUM_THREADS), SMEM_BYTES, s, maps, p));
+    TRY(launch_pdl(vocab_kernel<false>, dim3(grid), dim3(num_threads(false)), SMEM_BYTES, s, maps, p));
     return launch_pdl(vocab_finish_kernel, dim3(round_up(N, 32) / 32), dim3(512), 0, s, (const float2*)w.part,
                       (const float*)w.target_logit, w.r, tiles, N, Np, loss, lse);
 }
@@ -1028,7 +1049,7 @@ cudaError_t launch_vocab_loss_backward(const void* x, const void* wt, const int3
         p.shares = w.shares + (size_t)i * pairs;
         if (i < pieces) maps.d_out = d_out[i & 1];
         if (i > 0) maps.d = d_in[(i - 1) & 1], maps.d_mn = d_mn[(i - 1) & 1];
-        TRY(launch_pdl(vocab_kernel<true>, dim3(2 * pairs), dim3(NUM_THREADS), SMEM_BYTES, s, maps, p));
+        TRY(launch_pdl(vocab_kernel<true>, dim3(2 * pairs), dim3(num_threads(true)), SMEM_BYTES, s, maps, p));
     }
     if (!dx) return cudaSuccess;
     return launch_pdl(vocab_scatter_kernel, dim3((unsigned)(((size_t)N * (H / 4) + 255) / 256)), dim3(256), 0, s, (const float*)w.acc, w.r, N, Np, H,
