@@ -265,7 +265,8 @@ __device__ __forceinline__ void zero_absent_rows(const Pair* __restrict__ sorted
 #pragma unroll 6
         for (uint32_t j = first; j < whole; j += step) reinterpret_cast<uint4*>(inner)[j] = make_uint4(0, 0, 0, 0);
         for (uint32_t j = first; j < before; j += step) f32_to_elem(0.f, row[j]);
-        for (uint32_t j = before + whole * (16 / (uint32_t)sizeof(TG)) + first; j < (uint32_t)H; j += step) f32_to_elem(0.f, row[j]);
+        const uint32_t behind = before + whole * (16 / (uint32_t)sizeof(TG));
+        for (uint32_t j = behind + first; j < (uint32_t)H; j += step) f32_to_elem(0.f, row[j]);
     }
 }
 
@@ -361,7 +362,7 @@ constexpr int SUM_BATCH = 4;   // rows a warp reads together
 // MB).  Eight columns per lane in runs of W; each warp adds its tokens, and the warps' pieces of runs that
 // cross warps are joined in shared memory.
 template <typename TY, typename TG, int W, int TOKENS_PER_WARP>
-__global__ void __launch_bounds__(SUM_WARPS * 32, 3)   // three blocks an SM measured best (64K tokens: 106 us for the call, 111 with two)
+__global__ void __launch_bounds__(SUM_WARPS * 32, 3)   // (64K tokens: 106 us for the call, 111 with two blocks an SM)
     embed_sum_kernel(const TY* __restrict__ dy, const Pair* __restrict__ sorted, TG* grad, int T, int V, int H, float scale,
                      int accumulate, int sum_blocks, int fill_from, int chunk_rows, BlockState* __restrict__ state,
                      float* __restrict__ head, float* __restrict__ tail) {
@@ -448,7 +449,8 @@ __global__ void __launch_bounds__(SUM_WARPS * 32, 3)   // three blocks an SM mea
                         for (int j = 0; j < W; ++j) v[q][j0 + j] = x[j];
                     }
                     // the row of the table that a new run will be added to, on its way while the tokens' rows are
-                    if (accumulate && in && k != last) asm volatile("prefetch.global.L2 [%0];" ::"l"(grad + (size_t)k * H + col0 + col(j0)));
+                    if (accumulate && in && k != last)
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(grad + (size_t)k * H + col0 + col(j0)));
                 }
             }
 #pragma unroll

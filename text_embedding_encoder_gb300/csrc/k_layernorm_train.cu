@@ -340,8 +340,8 @@ struct Backward {
                                    (const TY*)dy, (const TX*)x, gamma, reinterpret_cast<const float2*>(stats),
                                    (const TX*)dres, (TX*)dx, partial, T, H);
         if (e != cudaSuccess) return e;
-        return launch_pdl(ln_dgamma_kernel, dim3((H + DG_COLS - 1) / DG_COLS), dim3(DG_COLS * DG_SLICES), 0, s, (const float*)partial, grid, H,
-                          dgamma);
+        return launch_pdl(ln_dgamma_kernel, dim3((H + DG_COLS - 1) / DG_COLS), dim3(DG_COLS * DG_SLICES), 0, s,
+                          (const float*)partial, grid, H, dgamma);
     }
 };
 

@@ -327,7 +327,8 @@ __device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
 
 __global__ void __launch_bounds__(ROWS_THREADS)
     vocab_rows_kernel(const bf16* __restrict__ x, const bf16* __restrict__ wt, const int32_t* __restrict__ targets,
-                      const float* __restrict__ lse_in, const float* __restrict__ gloss, int N, int V, int H, int ignore_id, int slice, float* loss, float* lse,
+                      const float* __restrict__ lse_in, const float* __restrict__ gloss, int N, int V, int H, int ignore_id,
+                      int slice, float* loss, float* lse,
                       Rows r, ShareArgs shares, unsigned int* status) {
     __shared__ int warp_n[ROWS_WARPS], warp_all[ROWS_WARPS], from_s[ROWS_THREADS], to_s[ROWS_THREADS];
     __shared__ float warp_g[ROWS_WARPS];
@@ -472,7 +473,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(num_threads(BWD), 1)
                   JOIN = 2 * STAGES + 5;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t crank = cluster_ctarank();
-    const uint32_t full0 = mapa_shared(bar(FULL), 0), tempty0 = mapa_shared(bar(TEMPTY), 0);   // the even CTA's, which both signal
+    // the even CTA's barriers, which both signal
+    const uint32_t full0 = mapa_shared(bar(FULL), 0), tempty0 = mapa_shared(bar(TEMPTY), 0);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -609,7 +611,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(num_threads(BWD), 1)
             mbar_wait_drain(bar(MMA_DONE), 0);
         }
     } else {
-        // ---------------- epilogue: thread = row, warps 2..5 columns 0..127, warps 6..9 the others; 10..17 as well ----------------
+        // ---------------- epilogue: thread = row, warps 2..5 columns 0..127, 6..9 the others (10..17 as 2..9) ----------------
         const int quad = warp & 3, half = (warp - 2) >> 2 & 1, set = (warp - 2) / EPI_WARPS;
         uint8_t* stage = smem + OUT_OFF + (warp - 2) % EPI_WARPS * 4096;   // (backward) this warp's staging box
         auto box_free = [&]() {   // the box's last store has read it
@@ -736,7 +738,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(num_threads(BWD), 1)
 #pragma unroll
                         for (int j = 0; j < 64; ++j) v[c][j] -= __bfloat162float(__float2bfloat16_rn(v[c][j]));
                     }
-                    if (row0 >= tiles.k_rows * BK) continue;   // rows that D^T X does not reach; in D W they only reach themselves
+                    // rows that D^T X does not reach; in D W they only reach themselves
+                    if (row0 >= tiles.k_rows * BK) continue;
                     box_free();
                     stage_row_bf16x64(stage, lane, v[c]);
                     send([&](uint32_t src) { tma_store_2d(&maps.d_out, src, col0 + 64 * c, row0); });
@@ -753,7 +756,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(num_threads(BWD), 1)
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
                             *reinterpret_cast<float4*>(b + ((k ^ (lane & 7)) << 4)) =
-                                w.num_k ? make_float4(a[4 * k], a[4 * k + 1], a[4 * k + 2], a[4 * k + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+                                w.num_k ? make_float4(a[4 * k], a[4 * k + 1], a[4 * k + 2], a[4 * k + 3])
+                                        : make_float4(0.f, 0.f, 0.f, 0.f);
                         // each element is added to once a launch: the order of the sums is fixed
                         send([&](uint32_t src) {
                             if (p.first) tma_store_2d(&maps.dx_acc, src, x, y);
@@ -798,9 +802,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(num_threads(BWD), 1)
 
 // lse and loss of the counted positions from the tiles' pairs: 32 rows by 16
 // slices of the tiles per block; the last step in 64 bits.
-__global__ void __launch_bounds__(512) vocab_finish_kernel(const float2* __restrict__ part, const float* __restrict__ target_logit,
-                                                           Rows r, int tiles, int N, int Np,
-                                                           float* __restrict__ loss, float* __restrict__ lse) {
+__global__ void __launch_bounds__(512)
+    vocab_finish_kernel(const float2* __restrict__ part, const float* __restrict__ target_logit, Rows r, int tiles, int N,
+                        int Np, float* __restrict__ loss, float* __restrict__ lse) {
     __shared__ float2 red[16][32];
     pdl_wait();
     pdl_trigger();
@@ -845,8 +849,9 @@ __global__ void __launch_bounds__(512) vocab_finish_kernel(const float2* __restr
 // dX of every position: gmax times the sum of its accumulators, or zeros; four
 // columns per thread.  n_mul: the columns of the first piece, whose products wrote
 // every slice.
-__global__ void __launch_bounds__(256) vocab_scatter_kernel(const float* __restrict__ acc, Rows r, int N, int Np, int H, int n_mul,
-                                                            int acc_rows, int pairs, bf16* __restrict__ dx) {
+__global__ void __launch_bounds__(256)
+    vocab_scatter_kernel(const float* __restrict__ acc, Rows r, int N, int Np, int H, int n_mul, int acc_rows, int pairs,
+                         bf16* __restrict__ dx) {
     pdl_wait();
     pdl_trigger();
     const size_t at4 = (size_t)blockIdx.x * 256 + threadIdx.x;
@@ -969,13 +974,14 @@ cudaError_t max_pairs(int dev, int num_sms, int* pairs) {
         if (e_ != cudaSuccess) return e_;   \
     } while (0)
 
-cudaError_t prepare_rows(const void* x, const void* wt, const int32_t* targets, const float* lse_in, const float* gloss, float* loss,
-                         float* lse, int N, int V, int H, int ignore_id, const LossWs& w, const ShareArgs& shares,
-                         unsigned int* status, cudaStream_t s) {
+cudaError_t prepare_rows(const void* x, const void* wt, const int32_t* targets, const float* lse_in, const float* gloss,
+                         float* loss, float* lse, int N, int V, int H, int ignore_id, const LossWs& w,
+                         const ShareArgs& shares, unsigned int* status, cudaStream_t s) {
     // a slice for each of 148 blocks, of 32 positions at least
     const int slice = round_up(std::max(1, (N + 147) / 148), 32);
-    return launch_pdl(vocab_rows_kernel, dim3((N + slice - 1) / slice + (shares.pairs ? shares.pieces + 1 : 0)), dim3(ROWS_THREADS), 0, s, (const bf16*)x,
-                      (const bf16*)wt, targets, lse_in, gloss, N, V, H, ignore_id, slice, loss, lse, w.r, shares, status);
+    const int blocks = (N + slice - 1) / slice + (shares.pairs ? shares.pieces + 1 : 0);
+    return launch_pdl(vocab_rows_kernel, dim3(blocks), dim3(ROWS_THREADS), 0, s, (const bf16*)x, (const bf16*)wt, targets,
+                      lse_in, gloss, N, V, H, ignore_id, slice, loss, lse, w.r, shares, status);
 }
 
 }  // namespace
@@ -1052,6 +1058,7 @@ cudaError_t launch_vocab_loss_backward(const void* x, const void* wt, const int3
         TRY(launch_pdl(vocab_kernel<true>, dim3(2 * pairs), dim3(num_threads(true)), SMEM_BYTES, s, maps, p));
     }
     if (!dx) return cudaSuccess;
-    return launch_pdl(vocab_scatter_kernel, dim3((unsigned)(((size_t)N * (H / 4) + 255) / 256)), dim3(256), 0, s, (const float*)w.acc, w.r, N, Np, H,
+    const unsigned blocks = (unsigned)(((size_t)N * (H / 4) + 255) / 256);
+    return launch_pdl(vocab_scatter_kernel, dim3(blocks), dim3(256), 0, s, (const float*)w.acc, w.r, N, Np, H,
                       std::min(vc, V), acc_rows, pairs, (bf16*)dx);
 }
