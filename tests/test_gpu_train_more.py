@@ -177,3 +177,78 @@ def test_layernorm_past_two_to_the_31(lib):
     assert torch.equal(dx[rows], small) and int(torch.count_nonzero(dx.view(-1).view(torch.int16))) == int(torch.count_nonzero(small))
     assert float((dgamma - small_g).abs().max()) <= 1e-5 * float(small_g.abs().max())
     enc.close()
+
+
+def test_workspaces_at_any_sixteen_bytes(lib):
+    """A workspace needs 16-byte alignment only; 16 bytes off a 256-byte boundary it gives the same bits, and nothing
+    is written before or behind it."""
+    enc = make_context()
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+
+    def sizes():
+        for N, V, H, T in ((300, 3001, 136, 700), (40, 9000, 64, 5000), (2000, 700, 264, 20000)):
+            x, w = torch.randn(N, H, generator=g, device="cuda").bfloat16(), torch.randn(V, H, generator=g, device="cuda").bfloat16()
+            t = torch.randint(0, V, (N,), generator=g, device="cuda", dtype=torch.int32)
+            ids = torch.randint(0, V, (T,), generator=g, device="cuda", dtype=torch.int32)
+            ids[: T // 3] = 3
+            yield N, V, H, T, x, w, t, ids, torch.randn(T, H, generator=g, device="cuda"), torch.rand(N, generator=g, device="cuda")
+
+    for N, V, H, T, x, w, t, ids, dy, gl in sizes():
+        gamma = torch.ones(H, device="cuda")
+        st = ln_forward(enc, dy, gamma, BF16)[1]
+        results = []
+        for shift in (0, 16):
+            kept = []
+
+            def ws(name, *s):
+                buf, n = workspace(name, *s, slack=512)
+                kept.append((buf, n))
+                return buf.data_ptr() + shift, n
+            loss, lse = torch.empty(N, device="cuda"), torch.empty(N, device="cuda")
+            dx, dw, dt = torch.empty_like(x), torch.empty_like(w), torch.empty(V, H, device="cuda")
+            dn, dg = torch.empty_like(dy), torch.empty(H, device="cuda")
+            s = stream()
+            enc.op("tee_op_vocab_loss_forward", x, w, t, loss, lse, N, V, H, -100, *ws("vocab_loss_forward", N, V, H), s)
+            enc.op("tee_op_vocab_loss_backward", x, w, t, lse, gl, dx, dw, N, V, H, -100, *ws("vocab_loss_backward", N, V, H), s)
+            enc.op("tee_op_embed_backward", dy, KIND[F32], ids, dt, KIND[F32], T, V, H, 1.0, 0, *ws("embed_backward", T, V, H), s)
+            enc.op("tee_op_layernorm_backward", dy, KIND[F32], dy, KIND[F32], gamma, st, None, dn, dg, T, H,
+                   *ws("layernorm_backward", T, H), s)
+            torch.cuda.synchronize()
+            for buf, n in kept:
+                assert bool((buf[:shift] == 0xFF).all()) and bool((buf[shift + n:] == 0xFF).all())
+            results.append((loss, lse, dx, dw, dt, dn, dg))
+        assert all(torch.equal(a, b) for a, b in zip(*results))
+    assert enc.device_status() == 0
+    enc.close()
+
+
+def test_calls_from_two_threads(lib):
+    """Each with its own context, stream and workspace."""
+    import threading
+    results, errors = {}, []
+
+    def run(k):
+        try:
+            enc = make_context()
+            side = torch.cuda.Stream()
+            with torch.cuda.stream(side):
+                g = torch.Generator(device="cuda")
+                g.manual_seed(7)
+                x, w = torch.randn(700, 128, generator=g, device="cuda").bfloat16(), torch.randn(900, 128, generator=g, device="cuda").bfloat16()
+                t = torch.randint(0, 900, (700,), generator=g, device="cuda", dtype=torch.int32)
+                for _ in range(20):
+                    loss, lse = loss_forward(enc, x, w, t)
+                    dx, dw = loss_backward(enc, x, w, t, lse, torch.ones(700, device="cuda"))
+                    table = embed_backward(enc, dx, t, 900, BF16, 1.0, into=dw)
+            side.synchronize()
+            assert enc.device_status() == 0
+            results[k] = (loss, table)
+            enc.close()
+        except BaseException as e:  # noqa: BLE001
+            errors.append(e)
+    threads = [threading.Thread(target=run, args=(k,)) for k in range(2)]
+    [th.start() for th in threads]
+    [th.join() for th in threads]
+    assert not errors, errors
+    assert all(torch.equal(a, b) for a, b in zip(results[0], results[1]))
