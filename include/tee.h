@@ -186,8 +186,9 @@ int tee_encode_tokens_device(tee_ctx* ctx, const int32_t* d_ids, const int32_t* 
                              int n_texts, float* d_out, void* stream);
 
 /* Message of the last failure on this context ("" if none).  NULL ctx: the
- * message of the last failed context-free call in this process (tee_create,
- * tee_pool_l2_noalloc). */
+ * message of the calling thread's last failed context-free call (tee_create,
+ * tee_pool_l2_noalloc, the *_workspace functions); it holds until that thread's
+ * next failure. */
 const char* tee_last_error(const tee_ctx* ctx);
 
 /* Release the context and all its device memory.  NULL-safe. */

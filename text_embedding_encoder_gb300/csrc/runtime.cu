@@ -22,7 +22,8 @@
 
 namespace {
 
-std::string g_create_error;
+// The calling thread's: calls without a context may run in several threads at once.
+thread_local std::string g_create_error;
 
 int fail(tee_ctx* c, int code, const char* fmt, ...) {
     char buf[512];
