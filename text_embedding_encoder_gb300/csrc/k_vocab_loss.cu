@@ -92,7 +92,8 @@ struct Rows {
     int32_t* target;        // [Np]
     float* lse2;            // [Np] lse / ln 2 (backward)
     float* ratio;           // [Np] upstream gradient / gmax (backward)
-    float* target_dot;      // [Np] x . w[target] in fp32 (forward)
+    double* target_dot;     // [Np] x . w[target], summed outside the tensor cores (forward)
+    float* target_d;        // [Np] ratio (exp(target_dot - lse) - 1), the target's entry of D (backward)
 };
 
 // ---------------------------------------------------------------------------
@@ -305,27 +306,47 @@ __device__ void make_shares(const ShareArgs& a, int count, int V, int H, int i) 
 // itself, so that no block waits for another (the targets are a few hundred KB
 // out of L2).  The last slice's block also writes their number and zeroes the
 // rest of the last tile; backward has a block more for each product launch's
-// shares.  Forward (gloss NULL) zeroes the outputs of the positions that are not
-// counted and takes the target's logit in plain fp32; backward divides the
-// upstream gradients by the largest.
+// shares.  Both take the target's logit by a sum of their own; forward (gloss
+// NULL) zeroes the outputs of the positions that are not counted, backward divides
+// the upstream gradients by the largest and makes the target's entry of D: with a
+// logit that is off by 2^-20 of itself, as the tensor cores' sums are, nothing
+// would be left of exp(logit - lse) - 1 where the target is nearly certain.
 constexpr int ROWS_THREADS = 512, ROWS_WARPS = ROWS_THREADS / 32;
 
-// Sum of eight products of bf16 pairs (each product exact in fp32).
-__device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
-    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float x0, x1, y0, y1;
-        unpack_bf16x2(x[i], x0, x1);
-        unpack_bf16x2(y[i], y0, y1);
-        s = fmaf(x0, y0, s);
-        s = fmaf(x1, y1, s);
+// A sum of products of bf16 pairs, each exact in fp32, that keeps beside the fp32
+// sum what its additions round off (Knuth's two-sum).
+struct Dot {
+    float sum = 0.f, rest = 0.f;
+    __device__ __forceinline__ void add(float p) {
+        const float t = sum + p, z = t - sum;
+        rest += (sum - (t - z)) + (p - z);
+        sum = t;
     }
-    return s;
-}
+    __device__ __forceinline__ void add8(const uint4& a, const uint4& b) {
+        const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float x0, x1, y0, y1;
+            unpack_bf16x2(x[i], x0, x1);
+            unpack_bf16x2(y[i], y0, y1);
+            add(x0 * y0);
+            add(x1 * y1);
+        }
+    }
+    // over the warp's lanes (64-bit additions here cost 9 us for 9830 rows)
+    __device__ __forceinline__ void over_warp() {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const float s = __shfl_xor_sync(0xffffffffu, sum, o), r = __shfl_xor_sync(0xffffffffu, rest, o);
+            rest += r;
+            add(s);
+        }
+    }
+    // an infinite sum leaves a rest that is not a number
+    __device__ __forceinline__ double value() const { return (double)sum + (fabsf(rest) <= FLT_MAX ? (double)rest : 0.0); }
+};
 
-__global__ void __launch_bounds__(ROWS_THREADS)
+__global__ void __launch_bounds__(ROWS_THREADS, 2)
     vocab_rows_kernel(const bf16* __restrict__ x, const bf16* __restrict__ wt, const int32_t* __restrict__ targets,
                       const float* __restrict__ lse_in, const float* __restrict__ gloss, int N, int V, int H, int ignore_id,
                       int slice, float* loss, float* lse,
@@ -402,7 +423,7 @@ __global__ void __launch_bounds__(ROWS_THREADS)
         if (live) {
             const int j = place - chunk0;
             from_s[j] = i;
-            if (!gloss) to_s[j] = t;
+            to_s[j] = t;
         }
         __syncthreads();
         // the block's warps copy the states, two rows at a time
@@ -413,15 +434,14 @@ __global__ void __launch_bounds__(ROWS_THREADS)
                                    reinterpret_cast<const uint4*>(x + (size_t)from_s[two ? j + 1 : j] * H)};
             uint4* dst = reinterpret_cast<uint4*>(r.x + (size_t)(chunk0 + j) * H);
             const int row = H / 8, half = row * FEW_ROWS;   // (in vectors)
-            float dot[2] = {};
-#pragma unroll 4
+            const uint4* to[2] = {reinterpret_cast<const uint4*>(wt + (size_t)to_s[j] * H),
+                                  reinterpret_cast<const uint4*>(wt + (size_t)to_s[two ? j + 1 : j] * H)};
+            Dot dot[2];
+#pragma unroll 3
             for (int k = lane; k < row; k += 32) {
                 const uint4 v[2] = {src[0][k], src[1][k]};
-                if (!gloss) {
 #pragma unroll
-                    for (int q = 0; q < 2; ++q)
-                        dot[q] += dot8(v[q], reinterpret_cast<const uint4*>(wt + (size_t)to_s[q && two ? j + 1 : j] * H)[k]);
-                }
+                for (int q = 0; q < 2; ++q) dot[q].add8(v[q], to[q][k]);
                 dst[k] = v[0];
                 if (two) dst[row + k] = v[1];
                 if (twice) {
@@ -429,11 +449,17 @@ __global__ void __launch_bounds__(ROWS_THREADS)
                     if (two) dst[half + row + k] = v[1];
                 }
             }
-            if (!gloss) {
-                const float d0 = warp_sum_f32(dot[0]), d1 = warp_sum_f32(dot[1]);
-                if (lane == 0) {
-                    r.target_dot[chunk0 + j] = d0;
-                    if (two) r.target_dot[chunk0 + j + 1] = d1;
+            dot[0].over_warp();
+            dot[1].over_warp();
+            if (lane < (two ? 2 : 1)) {   // a row by a lane
+                const int c = chunk0 + j + lane, i = from_s[j + lane];
+                const double logit = (lane ? dot[1] : dot[0]).value();
+                if (gloss) {
+                    const float e = gloss[i] / gmax * expm1f((float)(logit - (double)lse_in[i]));
+                    r.target_d[c] = e;
+                    if (twice) r.target_d[c + FEW_ROWS] = e;
+                } else {
+                    r.target_dot[c] = logit;
                 }
             }
         }
@@ -450,7 +476,7 @@ __global__ void __launch_bounds__(ROWS_THREADS)
         for (int k = lane; k < H / 8; k += 32) reinterpret_cast<uint4*>(r.x + (size_t)c * H)[k] = make_uint4(0, 0, 0, 0);
         if (lane == 0) {
             r.target[c] = -1;
-            if (gloss) r.lse2[c] = r.ratio[c] = 0.f;
+            if (gloss) r.lse2[c] = r.ratio[c] = r.target_d[c] = 0.f;
         }
     }
 }
@@ -636,14 +662,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(num_threads(BWD), 1)
             const int col0 = w.n * TILE + half * 128;          // this warp's first column of the output
             const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + acc * TILE + half * 128;
             // what the row needs, fetched while the products run
-            float lse2 = 0.f, ratio = 0.f;
+            float lse2 = 0.f, ratio = 0.f, target_d = 0.f;
             int target = -1;
             bool counted = false;
             if (!BWD || w.kind == LOGITS) {
                 target = p.r.target[row];
                 counted = target >= 0;
                 target -= p.v_log + col0;                      // within this warp's columns, if it is there
-                if (BWD) lse2 = p.r.lse2[row], ratio = p.r.ratio[row];
+                if (BWD) lse2 = p.r.lse2[row], ratio = p.r.ratio[row], target_d = p.r.target_d[row];
             }
             if (!all(mbar_wait(bar(TFULL + acc), use & 1, abort_flag))) break;
             tc_fence_after();
@@ -720,11 +746,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(num_threads(BWD), 1)
                 for (int c = 0; c < 2; ++c) {
 #pragma unroll
                     for (int j = 0; j < 64; ++j) v[c][j] = ex2_approx(fmaf(v[c][j], LOG2E, -lse2));
-                    const int tj = target - 64 * c;
-                    if (__any_sync(0xffffffffu, tj >= 0 && tj < 64)) {
-#pragma unroll
-                        for (int j = 0; j < 64; ++j) v[c][j] -= j == tj ? 1.f : 0.f;
-                    }
                     // rows of padding are zero whatever the table holds
 #pragma unroll
                     for (int j = 0; j < 64; ++j) v[c][j] = counted ? v[c][j] * ratio : 0.f;
@@ -733,6 +754,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(num_threads(BWD), 1)
 #pragma unroll
                         for (int j = 0; j < 64; ++j)
                             if (col0 + 64 * c + j >= p.n_log) v[c][j] = 0.f;
+                    }
+                    const int tj = target - 64 * c;
+                    if (__any_sync(0xffffffffu, tj >= 0 && tj < 64)) {
+#pragma unroll
+                        for (int j = 0; j < 64; ++j) v[c][j] = j == tj ? target_d : v[c][j];
                     }
                     if (left_over) {
 #pragma unroll
@@ -837,7 +863,7 @@ __global__ void __launch_bounds__(512)
     if ((unsigned)i >= (unsigned)N) return;
     // The tensor cores' sums of H products are off by a few 2^-24 of the logit.
     // The target's logit counts most, alone and, where it is likely, in lse: both
-    // take its plain fp32 sum instead, lse by exchanging the one term (H = 768: the
+    // take the sum of its own instead, lse by exchanging the one term (H = 768: the
     // losses are 0.8e-7 off; 6.5e-7 without this, 2.7e-7 with fp32 products).
     const double mma = target_logit[row], dot = r.target_dot[row];
     const double shift = exp(mma - l) * expm1(dot - mma);
@@ -926,12 +952,13 @@ LossWs carve_loss(int N, int V, int H, bool backward, void* base) {
     w.r.target = ws.take<int32_t>(Np);
     if (!backward) {
         w.target_logit = ws.take<float>(Np);
-        w.r.target_dot = ws.take<float>(Np);
+        w.r.target_dot = ws.take<double>(Np);
         w.part = ws.take<float2>((size_t)Np * ((V + TILE - 1) / TILE));
     } else {
         w.r.index = ws.take<int32_t>(N);
         w.r.lse2 = ws.take<float>(Np);
         w.r.ratio = ws.take<float>(Np);
+        w.r.target_d = ws.take<float>(Np);
         const int vc = piece_columns(Np, V);
         for (int b = 0; b < (vc < V ? 2 : 1); ++b) w.d[b] = ws.take<bf16>((size_t)Np * vc);
         w.acc = ws.take<float>((size_t)accumulator_rows(Np, H) * H);
