@@ -874,20 +874,26 @@ __global__ void __launch_bounds__(512)
 
 // dX of every position: gmax times the sum of its accumulators, or zeros; four
 // columns per thread.  n_mul: the columns of the first piece, whose products wrote
-// every slice.
+// every slice.  What the rounding of D left of the target's entry, mostly the
+// largest by far, is added here in fp32, where D holds one half only: dx is then
+// as exact as its type (H = 768: 1.66e-3 of the norm; 1.97e-3 without).
 __global__ void __launch_bounds__(256)
-    vocab_scatter_kernel(const float* __restrict__ acc, Rows r, int N, int Np, int H, int n_mul, int acc_rows, int pairs,
-                         bf16* __restrict__ dx) {
+    vocab_scatter_kernel(const float* __restrict__ acc, const bf16* __restrict__ wt, const int32_t* __restrict__ targets,
+                         Rows r, int N, int Np, int V, int H, int n_mul, int acc_rows, int pairs, bf16* __restrict__ dx) {
     pdl_wait();
     pdl_trigger();
     const size_t at4 = (size_t)blockIdx.x * 256 + threadIdx.x;
     const int quads = H / 4, i = (int)(at4 / quads), k = (int)(at4 - (size_t)i * quads);
     if (at4 >= (size_t)N * quads) return;
+    const int target = targets[i];
     const float gmax = *r.gmax;
     const int n = min(max(*r.count, 0), Np), mt = (n + TILE - 1) / TILE;
     const int at = min(r.index[i], n - 1), more = *r.twice ? FEW_ROWS : 0;
     float v[4] = {};
     if (at >= 0) {
+        float w[4];
+        load_vec(wt + (size_t)min(max(target, 0), V - 1) * H + 4 * k, w);
+        const float d = r.target_d[at];
         const int slices = dx_slices(mt, (H + TILE - 1) / TILE, pairs, acc_rows, n_mul);
         const float* from = acc + (size_t)at * H + 4 * k;
 #pragma unroll 4
@@ -897,7 +903,13 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[j] += a[j];
         }
-        if (more) {
+        if (!more) {
+            const float rest = d - __bfloat162float(__float2bfloat16_rn(d));
+            if (fabsf(rest) <= FLT_MAX) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = fmaf(rest, w[j], v[j]);
+            }
+        } else {
             from = acc + (size_t)((at + more) % TILE) * H + 4 * k;
             for (int s = 0; s < slices; ++s) {
                 float a[4];
@@ -1086,6 +1098,6 @@ cudaError_t launch_vocab_loss_backward(const void* x, const void* wt, const int3
     }
     if (!dx) return cudaSuccess;
     const unsigned blocks = (unsigned)(((size_t)N * (H / 4) + 255) / 256);
-    return launch_pdl(vocab_scatter_kernel, dim3(blocks), dim3(256), 0, s, (const float*)w.acc, w.r, N, Np, H,
-                      std::min(vc, V), acc_rows, pairs, (bf16*)dx);
+    return launch_pdl(vocab_scatter_kernel, dim3(blocks), dim3(256), 0, s, (const float*)w.acc, (const bf16*)wt,
+                      targets, w.r, N, Np, V, H, std::min(vc, V), acc_rows, pairs, (bf16*)dx);
 }
