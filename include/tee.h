@@ -204,7 +204,8 @@ void tee_destroy(tee_ctx* ctx);
 #define TEE_K_ELEMENTWISE 4  /* stand-alone RoPE / GeGLU (when not fused)        */
 #define TEE_K_POOL       5   /* mean-pool + L2 normalisation                     */
 #define TEE_K_QUANT      6   /* per-row 7-bit activation quantiser (W8A8)        */
-#define TEE_K_COUNT      7
+#define TEE_K_LOSS       7   /* softmax cross entropy over the vocabulary (tee_train.h) */
+#define TEE_K_COUNT      8
 
 typedef struct tee_kernel_stat {
     int64_t launches;        /* launches of this class since the last reset       */
@@ -218,7 +219,11 @@ typedef struct tee_kernel_stat {
  * kernel launch of an encode is bracketed by two events on the launching
  * stream; the durations are accumulated per kernel class by
  * tee_profile_read, which synchronises the pending events first.
- * Turning it on resets the counters.
+ * Turning it on resets the counters.  A call of a training operator (tee_train.h)
+ * is bracketed as a whole and counts as one launch; the vocabulary loss, whose
+ * work goes with the number of counted positions, which only the device knows,
+ * gives no flops, and as bytes those that do not depend on it (the table, the
+ * per-position arrays and the gradients).
  */
 int tee_profile_enable(tee_ctx* ctx, int on);
 int tee_profile_read(tee_ctx* ctx, tee_kernel_stat* stats /* [TEE_K_COUNT] */);

@@ -28,7 +28,7 @@ DTYPES = {"fp32": TEE_F32, "bf16": TEE_BF16, "w8a8": TEE_W8A8, "w4a8": TEE_W4A8,
 TEE_LN_ATTN, TEE_LN_MLP = 0, 1
 TEE_W_QKV, TEE_W_OUT, TEE_W_FFN_IN, TEE_W_FFN_OUT = 0, 1, 2, 3
 
-KERNEL_CLASSES = ["embed", "layernorm", "gemm", "attention", "elementwise", "pool", "quant"]
+KERNEL_CLASSES = ["embed", "layernorm", "gemm", "attention", "elementwise", "pool", "quant", "loss"]
 
 
 class TeeConfig(ctypes.Structure):

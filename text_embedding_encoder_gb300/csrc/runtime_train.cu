@@ -188,7 +188,8 @@ int tee_op_vocab_loss_forward(tee_ctx* ctx, const void* d_x, const void* d_w, co
     int rc = check_bufs(ctx, op, {{"d_x", d_x, 16}, {"d_w", d_w, 16}, {"d_targets", d_targets, 4}, {"d_loss", d_loss, 4},
                                   {"d_lse", d_lse, 4}});
     if (rc || (rc = check_ws(ctx, op, d_ws, ws_bytes, vocab_loss_ws(N, V, H, false)))) return rc;
-    return launch(ctx, op, TEE_K_GEMM, 2.0 * N * V * H, 2.0 * ((double)N + V) * H, stream, [&](cudaStream_t s) {
+    // (products and states go with the number of counted positions, which the host does not know)
+    return launch(ctx, op, TEE_K_LOSS, 0, 2.0 * V * H + 12.0 * N, stream, [&](cudaStream_t s) {
         return launch_vocab_loss_forward(d_x, d_w, d_targets, d_loss, d_lse, N, V, H, ignore_id, d_ws, ctx->d_status, s);
     });
 }
@@ -214,7 +215,8 @@ int tee_op_vocab_loss_backward(tee_ctx* ctx, const void* d_x, const void* d_w, c
         if (d_dx && (rc = check_bufs(ctx, op, {{"d_dx", d_dx, 16}}))) return rc;
         if ((rc = check_ws(ctx, op, d_ws, ws_bytes, vocab_loss_ws(N, V, H, true)))) return rc;
     }
-    return launch(ctx, op, TEE_K_GEMM, 6.0 * N * V * H, 4.0 * ((double)N + V) * H, stream, [&](cudaStream_t s) {
+    const double bytes = (N ? 2.0 * V * H + 12.0 * N : 0.0) + (d_dx ? 2.0 * N * H : 0.0) + (d_dw ? 2.0 * V * H : 0.0);
+    return launch(ctx, op, TEE_K_LOSS, 0, bytes, stream, [&](cudaStream_t s) {
         return launch_vocab_loss_backward(d_x, d_w, d_targets, d_lse, d_gloss, d_dx, d_dw, N, V, H, ignore_id, d_ws,
                                           ctx->d_status, s);
     });
