@@ -147,13 +147,13 @@ __global__ void __launch_bounds__(THREADS) ln_forward_kernel(const TX* x, const 
 // 24, two (768: 87; three, with spills, 117).  With N = 32 two blocks spill and one
 // leaves the loads exposed (2048 columns: 95 and 136; four warps of 16 a lane 83).
 // Rows by single elements keep more addresses: 8 a lane (1001: 111; 16 a lane and
-// two blocks 140, 32 and one 495).
-template <int N>
-constexpr int bwd_blocks() { return N == 8 ? 4 : N == 16 ? 3 : 2; }
+// two blocks 140, 32 and one 495), and two blocks of 16, for which three leave no registers.
+template <int W, int N>
+constexpr int bwd_blocks() { return N == 8 ? 4 : N == 16 && W > 1 ? 3 : 2; }
 // The same as a bound on the registers.  Two blocks of 24 elements a lane fit unasked
 // (asked for, two warps a row took 112 us instead of 86 at 1536 columns).
 template <int W, int N, int WPR>
-constexpr int bwd_min_blocks() { return W == 1 && N == 16 ? 2 : N == 24 && WPR == 2 ? 1 : bwd_blocks<N>(); }
+constexpr int bwd_min_blocks() { return N == 24 && WPR == 2 ? 1 : bwd_blocks<W, N>(); }
 
 // Groups take rows blockIdx-strided; each lane keeps the gain's gradient of its
 // columns over all its rows, the block adds its groups' sums and writes one row
@@ -334,7 +334,7 @@ struct Backward {
     cudaError_t operator()() const {
         constexpr int GROUPS = WARPS / WPR;
         if (WPR != backward_warps(H)) return cudaErrorInvalidValue;   // the workspace is sized by it
-        const int grid = min(min((T - 1) / GROUPS + 1, bwd_blocks<N>() * num_sms), BWD_MAX_GRID);
+        const int grid = min(min((T - 1) / GROUPS + 1, bwd_blocks<W, N>() * num_sms), BWD_MAX_GRID);
         const size_t smem = GROUPS > 1 ? (size_t)GROUPS * H * sizeof(float) : 0;   // at most 32 KB
         cudaError_t e = launch_pdl(ln_backward_kernel<TX, TY, W, N, WPR>, dim3(grid), dim3(THREADS), smem, s,
                                    (const TY*)dy, (const TX*)x, gamma, reinterpret_cast<const float2*>(stats),
