@@ -309,8 +309,9 @@ __device__ void make_shares(const ShareArgs& a, int count, int V, int H, int i) 
 // shares.  Both take the target's logit by a sum of their own; forward (gloss
 // NULL) zeroes the outputs of the positions that are not counted, backward divides
 // the upstream gradients by the largest and makes the target's entry of D: with a
-// logit that is off by 2^-20 of itself, as the tensor cores' sums are, nothing
-// would be left of exp(logit - lse) - 1 where the target is nearly certain.
+// logit that is low by 2^-20 of itself (768 columns; 2^-18 at 2048), as the tensor
+// cores' sums are, nothing would be left of exp(logit - lse) - 1 where the target
+// is nearly certain.
 constexpr int ROWS_THREADS = 512, ROWS_WARPS = ROWS_THREADS / 32;
 
 // A sum of products of bf16 pairs, each exact in fp32, that keeps beside the fp32
