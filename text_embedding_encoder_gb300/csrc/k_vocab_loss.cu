@@ -106,7 +106,7 @@ struct Maps {
     CUtensorMap x, w;               // K-major operands of the logits: boxes of 64 columns x 128 rows
     CUtensorMap d;                  // D of the piece being multiplied, K-major (D W)
     CUtensorMap w_mn, d_mn, x_mn;   // MN-major operands: boxes of 64 columns x 64 rows
-    CUtensorMap d_out, dx_acc, dw;  // outputs: boxes of 32 rows x 128 bytes
+    CUtensorMap d_out, dx_acc, dw;  // outputs: boxes of 32 rows x 128 bytes (dw: of the table's gradient or its fp32 sums)
 };
 
 struct Share;
@@ -124,6 +124,7 @@ struct Params {
     int want_dx, want_dw;
     int acc_rows;                   // rows of the dX accumulators
     int first;                      // dX is written, not added to
+    int dw_sum;                     // 0: dW is written rounded; else its fp32 sums, 1: written, 2: added to
     const Share* shares;            // the pairs' shares of this launch (backward)
     unsigned int* status;
 };
@@ -771,24 +772,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(num_threads(BWD), 1)
                     stage_row_bf16x64(stage, lane, v[c]);
                     send([&](uint32_t src) { tma_store_2d(&maps.d_out, src, col0 + 64 * c, row0); });
                 }
-            } else if (w.kind == DX) {
-                const int y = w.slice * tiles.mt * TILE + row0;
+            } else if (w.kind == DX || p.dw_sum) {
+                // fp32 sums.  Each element is added to once a launch: the order of the sums is fixed
+                const bool is_dx = w.kind == DX, write = is_dx ? p.first != 0 : p.dw_sum == 1;
+                const CUtensorMap* map = is_dx ? &maps.dx_acc : &maps.dw;
+                const int y = is_dx ? w.slice * tiles.mt * TILE + row0 : p.v_mul + row0;
+                const float scale = is_dx ? 1.f : gmax;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const int x = col0 + 32 * c;
-                    if (x < p.H) {
+                    if (x < p.H && (is_dx || y < p.V)) {
                         const float* a = v[c >> 1] + 32 * (c & 1);
                         box_free();
                         uint8_t* b = stage + lane * 128;
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
                             *reinterpret_cast<float4*>(b + ((k ^ (lane & 7)) << 4)) =
-                                w.num_k ? make_float4(a[4 * k], a[4 * k + 1], a[4 * k + 2], a[4 * k + 3])
+                                w.num_k ? make_float4(a[4 * k] * scale, a[4 * k + 1] * scale, a[4 * k + 2] * scale,
+                                                      a[4 * k + 3] * scale)
                                         : make_float4(0.f, 0.f, 0.f, 0.f);
-                        // each element is added to once a launch: the order of the sums is fixed
                         send([&](uint32_t src) {
-                            if (p.first) tma_store_2d(&maps.dx_acc, src, x, y);
-                            else tma_reduce_add_2d(&maps.dx_acc, src, x, y);
+                            if (write) tma_store_2d(map, src, x, y);
+                            else tma_reduce_add_2d(map, src, x, y);
                         });
                     }
                 }
@@ -925,11 +930,35 @@ __global__ void __launch_bounds__(256)
     store_vec(dx + (size_t)i * H + 4 * k, v);
 }
 
+// dW from its fp32 sums, eight elements a thread.
+__global__ void __launch_bounds__(256) vocab_round_kernel(const float* __restrict__ sums, size_t n8, bf16* __restrict__ dw) {
+    pdl_wait();
+    pdl_trigger();
+    const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n8) return;
+    float a[4], b[4];
+    load_vec(sums + 8 * i, a);
+    load_vec(sums + 8 * i + 4, b);
+    store_vec(dw + 8 * i, {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]});
+}
+
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
 
+// Backward takes the positions in parts of at most so many, the parts' dW added in
+// fp32 in order.  The tensor cores drop part of the last bit of a sum at every step
+// of 16 terms: a dW of 65536 positions whose terms all have one sign is 2e-4 low,
+// which its rounding to bf16 covers; of 2^20 in one sum 0.7 %, of 2^24 10 %.
+constexpr int PART_ROWS = 65536;
+
 int round_up(int v, int a) { return (int)(((long long)v + a - 1) / a * a); }
+
+// Positions of each of the parts but the last: equal ones, whole tiles.
+int part_rows(int N) {
+    const int parts = (N + PART_ROWS - 1) / PART_ROWS;
+    return round_up((N + parts - 1) / parts, TILE);
+}
 
 // Columns of a backward piece: D at most 256 MB for as many rows as there are
 // positions, 2048 columns at least.  Smaller pieces keep D in L2 but their launches
@@ -951,11 +980,17 @@ struct LossWs {
     bf16* d[2] = {nullptr, nullptr};
     float* acc = nullptr;
     Share* shares = nullptr;
+    float* dw_sum = nullptr;
     size_t bytes = 0;
 };
+// (backward: of a part)
 LossWs carve_loss(int N, int V, int H, bool backward, void* base) {
     WsCarve ws(base);
     LossWs w;
+    if (backward && N > PART_ROWS) {
+        w.dw_sum = ws.take<float>((size_t)V * H);
+        N = part_rows(N);
+    }
     const int Np = round_up(N, TILE);
     w.r.count = ws.take<int>(1);
     w.r.gmax = ws.take<float>(1);
@@ -1060,7 +1095,8 @@ cudaError_t launch_vocab_loss_backward(const void* x, const void* wt, const int3
     int dev = 0, num_sms = 0, pairs = 0;
     TRY(tee_current_device(&dev, &num_sms));
     TRY(max_pairs<true>(dev, num_sms, &pairs));
-    const int Np = round_up(N, TILE), vc = piece_columns(Np, V);
+    const bool parts = N > PART_ROWS;
+    const int part = parts ? part_rows(N) : N, Np = round_up(part, TILE), vc = piece_columns(Np, V);
     const LossWs w = carve_loss(N, V, H, true, ws);
     Maps maps{};
     TRY(make_tensor_map_2d(&maps.x, false, w.r.x, Np, H, H, 128, 64));
@@ -1069,7 +1105,8 @@ cudaError_t launch_vocab_loss_backward(const void* x, const void* wt, const int3
     TRY(make_tensor_map_2d(&maps.x_mn, false, w.r.x, Np, H, H, 64, 64));
     const int acc_rows = accumulator_rows(Np, H);
     TRY(make_tensor_map_2d(&maps.dx_acc, true, w.acc, acc_rows, H, H, 32, 32));
-    if (dw) TRY(make_tensor_map_2d(&maps.dw, false, dw, V, H, H, 32, 64));
+    if (dw && parts) TRY(make_tensor_map_2d(&maps.dw, true, w.dw_sum, V, H, H, 32, 32));
+    else if (dw) TRY(make_tensor_map_2d(&maps.dw, false, dw, V, H, H, 32, 64));
     CUtensorMap d_in[2], d_mn[2], d_out[2];
     for (int b = 0; b < (vc < V ? 2 : 1); ++b) {
         TRY(make_tensor_map_2d(&d_in[b], false, w.d[b], Np, vc, vc, 128, 64));
@@ -1084,21 +1121,29 @@ cudaError_t launch_vocab_loss_backward(const void* x, const void* wt, const int3
     p.status = status;
     const int pieces = (V + vc - 1) / vc;
     const ShareArgs shares{vc, pieces, p.want_dx, p.want_dw, pairs, acc_rows, w.shares};
-    TRY(prepare_rows(x, wt, targets, lse, gloss, nullptr, nullptr, N, V, H, ignore_id, w, shares, status, s));
-    for (int i = 0; i <= pieces; ++i) {
-        // logits of piece i into one buffer, products of piece i - 1 out of the other
-        p.v_log = i < pieces ? i * vc : 0;
-        p.n_log = i < pieces ? std::min(vc, V - p.v_log) : 0;
-        p.v_mul = i > 0 ? (i - 1) * vc : 0;
-        p.n_mul = i > 0 ? std::min(vc, V - p.v_mul) : 0;
-        p.first = i == 1;
-        p.shares = w.shares + (size_t)i * pairs;
-        if (i < pieces) maps.d_out = d_out[i & 1];
-        if (i > 0) maps.d = d_in[(i - 1) & 1], maps.d_mn = d_mn[(i - 1) & 1];
-        TRY(launch_pdl(vocab_kernel<true>, dim3(2 * pairs), dim3(num_threads(true)), SMEM_BYTES, s, maps, p));
+    for (int at = 0; at < N; at += part) {
+        const int n = std::min(part, N - at);
+        TRY(prepare_rows((const bf16*)x + (size_t)at * H, wt, targets + at, lse + at, gloss + at, nullptr, nullptr, n, V, H,
+                         ignore_id, w, shares, status, s));
+        p.dw_sum = !parts ? 0 : at == 0 ? 1 : 2;
+        for (int i = 0; i <= pieces; ++i) {
+            // logits of piece i into one buffer, products of piece i - 1 out of the other
+            p.v_log = i < pieces ? i * vc : 0;
+            p.n_log = i < pieces ? std::min(vc, V - p.v_log) : 0;
+            p.v_mul = i > 0 ? (i - 1) * vc : 0;
+            p.n_mul = i > 0 ? std::min(vc, V - p.v_mul) : 0;
+            p.first = i == 1;
+            p.shares = w.shares + (size_t)i * pairs;
+            if (i < pieces) maps.d_out = d_out[i & 1];
+            if (i > 0) maps.d = d_in[(i - 1) & 1], maps.d_mn = d_mn[(i - 1) & 1];
+            TRY(launch_pdl(vocab_kernel<true>, dim3(2 * pairs), dim3(num_threads(true)), SMEM_BYTES, s, maps, p));
+        }
+        if (!dx) continue;
+        const unsigned blocks = (unsigned)(((size_t)n * (H / 4) + 255) / 256);
+        TRY(launch_pdl(vocab_scatter_kernel, dim3(blocks), dim3(256), 0, s, (const float*)w.acc, (const bf16*)wt,
+                       targets + at, w.r, n, Np, V, H, std::min(vc, V), acc_rows, pairs, (bf16*)dx + (size_t)at * H));
     }
-    if (!dx) return cudaSuccess;
-    const unsigned blocks = (unsigned)(((size_t)N * (H / 4) + 255) / 256);
-    return launch_pdl(vocab_scatter_kernel, dim3(blocks), dim3(256), 0, s, (const float*)w.acc, (const bf16*)wt,
-                      targets, w.r, N, Np, V, H, std::min(vc, V), acc_rows, pairs, (bf16*)dx);
+    if (!parts || !dw) return cudaSuccess;
+    const size_t n8 = (size_t)V * H / 8;
+    return launch_pdl(vocab_round_kernel, dim3((unsigned)((n8 + 255) / 256)), dim3(256), 0, s, (const float*)w.dw_sum, n8, (bf16*)dw);
 }
