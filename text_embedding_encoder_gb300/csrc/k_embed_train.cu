@@ -16,8 +16,9 @@
 //   embed_join_kernel  adds the pieces of each run that crosses blocks, in order.
 // Measured, 102400 x 768: 2048 tokens into a bf16 table 29.7 us (157 MB of zeros
 // alone take 24); 65536 tokens, 30 % of them one id, into an fp32 table 98.5 us
-// (sort 22, sums and zeros 73 at 5.6 TB/s of DRAM traffic -- a gather of the same
-// rows by themselves runs at 5.1 -- join 8).  The lookup forward, 32768 tokens of
+// (the launches one by one, caches flushed before each: sort 22, sums and zeros 70 at
+// 5.8 TB/s of DRAM traffic -- a gather of the same rows by themselves runs at 5.1 --
+// join 9).  The lookup forward, 32768 tokens of
 // which few ids are new, bf16 -> fp32: 19.5 us, the write of its output.
 #include "train_internal.cuh"
 

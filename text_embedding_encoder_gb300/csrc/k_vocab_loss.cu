@@ -9,15 +9,19 @@
 // the next launch adds D W to dX (fp32) and writes that piece's D^T X to dW.
 // Work: 2 n V H flops forward, 6 n V H backward, n the counted positions.  Both
 // are bound by the tensor cores.  Measured at n = 9830 of 32768, V = 102400, H = 768:
-//   forward 0.81 to 0.88 ms, 1760 to 1910 TFLOP/s, the tensor pipes 95 to 97 % busy:
+//   forward 0.80 to 0.92 ms, 1680 to 1930 TFLOP/s, the tensor pipes 95 to 97 % busy:
 //     the clock, under the power limit, sets the time.
-//   backward 3.0 to 3.1 ms, 1500 TFLOP/s; the pipes 79 % busy.  A piece's launch
-//     takes 106 us: products at 0.29 to 0.33 us a K step (0.27 is the pipes' rate at
+//   backward 3.0 to 3.25 ms, 1430 to 1550 TFLOP/s; the pipes 79 % busy.  A piece's
+//     launch takes 107 to 111 us: products at 0.29 to 0.33 us a K step (0.27 is the pipes' rate at
 //     1.9 GHz), logits 4.0 us a tile instead of 3.3 -- their operands' way through
 //     shared memory, in and out again, already takes its whole bandwidth, and D's
 //     adds to it --, and 5 us from one launch's last store to the next one's first.
-// n = 315 of 1051: backward 0.18 ms.  One piece; DRAM moves 0.6 GB (the table twice,
-// D three times, dW), and the second tile of 256 rows holds 59.
+// n = 315 of 1051: backward 0.18 to 0.19 ms.  One piece; DRAM moves 0.6 GB (the table
+// twice, D three times, dW), and the second tile of 256 rows holds 59.
+// Far from their floors, of whole row tiles and launches one after the other: one
+// position 151 us backward and 54 forward (the table's bytes: 47 and 24); and of a
+// small table, whose few tiles of D^T X leave CTA pairs idle: 16384 positions against
+// 1000 rows 152 us (products: 38).
 //
 //   * Positions that are not counted cost nothing: vocab_rows_kernel lists the
 //     others in order and copies their states together, and every later kernel
@@ -75,10 +79,12 @@ constexpr float LOG2E = 1.4426950408889634f;
 constexpr int EPILOGUE_K_STEPS = 8;
 
 // Up to so many counted positions are listed twice in the backward pass, once in
-// each half of the only row tile, which is no more work: the first gives D
-// rounded to bf16, the second what that left over.  With many positions the
-// roundings of D average out; with few, one of them (the target's entry, up to
-// 2^-8 off) could be most of a gradient's error.
+// each half of the only row tile: the first gives D rounded to bf16, the second what
+// that left over.  The products of the logits and of D W stay the same; D^T X walks up
+// to four K steps instead of two, and D is written and read twice (102400 x 768: 128
+// positions 171 us, 129, which are listed once, 147).  With many positions the roundings of D
+// average out; with few, one of them (the target's entry, up to 2^-8 off) could be
+// most of the error of a row of dW.
 constexpr int FEW_ROWS = 128;
 
 // What vocab_rows_kernel prepares, and the kernels after it read.
