@@ -1,6 +1,6 @@
-"""The loss takes the target's logit by a sum of its own and not out of the tensor cores, whose sums are low
-by 2^-20 of a logit at 768 columns and 2^-18 at 2048.  Here the target's logit is far from zero and the others are near zero, so that the loss is almost its
-magnitude and any error of it shows, while the others' errors cannot."""
+"""The loss takes the target's logit by a sum of its own and not out of the tensor cores, whose sums are low by 2^-20 of
+a logit at 768 columns and 2^-18 at 2048.  Here the target's logit is far from zero and the others are near zero, so
+that an error of it shows in the loss (far below zero) or in lse (far above), and the others' errors cannot."""
 import math
 
 import pytest
@@ -44,8 +44,9 @@ def test_loss_of_targets_far_from_the_others(enc, N, V, H, sign):
     # 17 times the last bit, 2^-23, of the largest of them, which is at most max_partial.
     steps = x.double().view(N, 1, H // 16, 16) * w.double().view(1, V, H // 16, 16) if N * V * H < 2 ** 28 else None
     if steps is None:
-        largest = torch.stack([(x[i].double() * w.double()).view(V, H // 16, 16).sum(2).cumsum(1).abs().amax(1) for i in range(N)])
-        product = torch.stack([(x[i].double() * w.double()).abs().amax(1) for i in range(N)])
+        products = [(x[i].double() * w.double()).view(V, H // 16, 16) for i in range(N)]
+        largest = torch.stack([p.sum(2).cumsum(1).abs().amax(1) for p in products])
+        product = torch.stack([p.abs().amax((1, 2)) for p in products])
     else:
         largest, product = steps.sum(3).cumsum(2).abs().amax(2), steps.abs().amax((2, 3))
     e = H / 16 * 17 * 2.0 ** -23 * torch.maximum(largest, product)
@@ -54,6 +55,7 @@ def test_loss_of_targets_far_from_the_others(enc, N, V, H, sign):
     # exponentials 2^-22, their arguments and the sums of up to 64 parts in fp32: relative to the sum, as log takes it
     off = off + 2.0 ** -22 + 80 * U
     # with the target nearly certain only what the others add counts
-    off = torch.minimum(off, (1 - p.gather(1, at).squeeze(1)) * 0.5 + 2.0 ** -22 + 2 * U * want_lse.abs()) if sign > 0 else off
+    if sign > 0:
+        off = torch.minimum(off, (1 - p.gather(1, at).squeeze(1)) * 0.5 + 2.0 ** -22 + 2 * U * want_lse.abs())
     assert_within(loss, want_lse - target, off + U * (want_lse - target).abs())
     assert_within(lse, want_lse, off + U * want_lse.abs())

@@ -1152,5 +1152,6 @@ cudaError_t launch_vocab_loss_backward(const void* x, const void* wt, const int3
     }
     if (!parts || !dw) return cudaSuccess;
     const size_t n8 = (size_t)V * H / 8;
-    return launch_pdl(vocab_round_kernel, dim3((unsigned)((n8 + 255) / 256)), dim3(256), 0, s, (const float*)w.dw_sum, n8, (bf16*)dw);
+    return launch_pdl(vocab_round_kernel, dim3((unsigned)((n8 + 255) / 256)), dim3(256), 0, s, (const float*)w.dw_sum, n8,
+                      (bf16*)dw);
 }
