@@ -1,7 +1,9 @@
 /*
  * tee_train.h -- the operators a training step of the encoder adds to the
- * forward pass (same library as tee.h): the LayerNorm, the scaled token lookup
- * and the softmax cross entropy over the vocabulary, each forward and backward.
+ * forward pass (same library as tee.h): the LayerNorm, the scaled token lookup,
+ * the softmax cross entropy over the vocabulary, rotary positions, attention and
+ * the gated half of the feed-forward block, each forward and backward, and the
+ * clipping of all gradients by their common norm.
  *
  * As in tee_ops.h every call runs on caller-provided DEVICE buffers,
  * asynchronously on `stream` (a cudaStream_t, NULL = legacy default stream), on
@@ -123,6 +125,91 @@ int tee_op_vocab_loss_backward(tee_ctx* ctx, const void* d_x, const void* d_w, c
                                const float* d_lse, const float* d_gloss, void* d_dx, void* d_dw, int N, int V, int H,
                                int ignore_id, void* d_ws, size_t ws_bytes, void* stream);
 long long tee_vocab_loss_backward_workspace(int N, int V, int H);
+
+/* ---- rotary positions --------------------------------------------------------
+ * On packed rows of n_heads queries, n_heads keys and n_heads values of 64 columns
+ * each (qkv, as tee_op_attention takes them).  For every query and key head,
+ * j < 32, with the angle a = pos[t] base^(-j / 32):
+ *   y[j] = x[j] cos a - x[j + 32] sin a,  y[j + 32] = x[j + 32] cos a + x[j] sin a
+ * and the values are copied.  The backward pass turns by the negated angle.
+ * x and y type[T * 192 n_heads]; pos int32[T], as tee_op_positions gives them; d_y
+ * may be d_x (the values then stay).  1 <= n_heads <= TEE_ATTN_MAX_HEADS, base > 0.
+ * Angles are taken in 64 bits, to within 1e-7 of a turn. */
+#define TEE_ATTN_MAX_HEADS 512
+int tee_op_rope_forward(tee_ctx* ctx, const void* d_x, int type, const int32_t* d_pos, void* d_y, int T, int n_heads,
+                        float base, void* stream);
+int tee_op_rope_backward(tee_ctx* ctx, const void* d_dy, int type, const int32_t* d_pos, void* d_dx, int T, int n_heads,
+                         float base, void* stream);
+
+/* ---- attention ------------------------------------------------------------------
+ * Bidirectional attention inside each text of a packed batch, as tee_op_attention,
+ * for a step that is going to be differentiated.  Row i sees the rows j of its text,
+ * with window >= 0 those with |i - j| <= window.  Per head of 64 columns:
+ *   s[i,j] = q[i] . k[j] / 8,  lse[i] = log sum_j exp s[i,j],
+ *   o[i] = sum_j exp(s[i,j] - lse[i]) v[j]
+ * qkv bf16[T * 192 n_heads] (rotated, where positions are); cu int32[n_texts + 1] on
+ * the DEVICE: cu[0] = 0, cu not decreasing, cu[n_texts] <= T, at most
+ * TEE_ATTN_MAX_TEXT_TOKENS tokens to a text.  Other offsets set the device status
+ * and leave the outputs as they were.  Texts may be empty.  Rows behind the last
+ * text are neither read nor written, whatever they hold, and no text's results
+ * depend on another's values, were they NaN.
+ * o bf16[T * 64 n_heads], lse float[n_heads * T], head by head.
+ * 0 <= T <= 2^24, 0 <= n_texts <= 2^20.  The host sees neither cu nor the texts'
+ * lengths, so one captured graph serves batches of other texts.
+ * The products take bf16 operands into fp32 accumulators: the probabilities are
+ * rounded to bf16 for the product with v (not for lse), and the gradients' factors
+ * likewise. */
+#define TEE_ATTN_MAX_TEXT_TOKENS 131072
+int tee_op_attention_forward(tee_ctx* ctx, const void* d_qkv, const int32_t* d_cu, void* d_o, float* d_lse, int T,
+                             int n_texts, int n_heads, int window, void* d_ws, size_t ws_bytes, void* stream);
+long long tee_attention_forward_workspace(int T, int n_texts, int n_heads);
+
+/* With p[i,j] = exp(s[i,j] - lse[i]), delta[i] = do[i] . o[i] and
+ * ds[i,j] = p[i,j] (do[i] . v[j] - delta[i]):
+ *   dq[i] = sum_j ds[i,j] k[j] / 8,  dk[j] = sum_i ds[i,j] q[i] / 8,  dv[j] = sum_i p[i,j] do[i]
+ * The probabilities are computed again.  o and lse as the forward pass wrote them,
+ * do bf16[T * 64 n_heads]; dqkv bf16[T * 192 n_heads] in the layout of qkv, of whose
+ * queries and keys tee_op_rope_backward makes the gradients before their rotation. */
+int tee_op_attention_backward(tee_ctx* ctx, const void* d_qkv, const int32_t* d_cu, const void* d_o, const float* d_lse,
+                              const void* d_do, void* d_dqkv, int T, int n_texts, int n_heads, int window, void* d_ws,
+                              size_t ws_bytes, void* stream);
+long long tee_attention_backward_workspace(int T, int n_texts, int n_heads);
+
+/* ---- the gated half of the feed-forward block ---------------------------------------
+ * As tee_op_ffn_in: both projections, the activation and the product, in one launch.
+ *   a = x wa^T, g = x wg^T,  z = GELU(a) g      (GELU(a) = a Phi(a))
+ * x bf16[T*H]; wi bf16[2I*H], the rows of wa and then those of wg; z bf16[T*I].
+ * H a multiple of 8 in [8, TEE_GEGLU_MAX_HIDDEN], I one in [8, TEE_GEGLU_MAX_WIDTH],
+ * 0 <= T <= 2^24. */
+#define TEE_GEGLU_MAX_HIDDEN 8192
+#define TEE_GEGLU_MAX_WIDTH 32768
+int tee_op_geglu_forward(tee_ctx* ctx, const void* d_x, const void* d_wi, void* d_z, int T, int H, int I, void* stream);
+
+/* Nothing but x is kept from the forward pass; a and g are computed again.
+ *   da = dz g GELU'(a), dg = dz GELU(a)   (rounded to bf16 for the products below)
+ *   dx = da wa + dg wg,   dwi = [da^T x; dg^T x]
+ * dz bf16[T*I], dx bf16[T*H], dwi bf16[2I*H]; d_dx or d_dwi may be NULL where that
+ * gradient is not wanted (not both).  With T == 0 dwi is set to zero.  More than 65536
+ * rows are taken in equal parts, whose dwi is added in fp32. */
+int tee_op_geglu_backward(tee_ctx* ctx, const void* d_x, const void* d_wi, const void* d_dz, void* d_dx, void* d_dwi, int T,
+                          int H, int I, void* d_ws, size_t ws_bytes, void* stream);
+long long tee_geglu_backward_workspace(int T, int H, int I);
+
+/* ---- clipping by the common norm ------------------------------------------------------
+ * Of n_tensors gradients, h_grads[i] with h_counts[i] elements of type h_types[i]:
+ *   norm = sqrt(sum of all squares),  factor = min(1, max_norm / norm),  out = factor g
+ * factor is 1 where the norm is zero, infinite or not a number: such gradients are
+ * passed on as they are, and norm tells.  d_norm float[2] = {norm, factor}.
+ * The four lists are HOST arrays, read before the call returns; the tensors are on the
+ * device, contiguous, aligned to their elements (16 bytes: faster).  h_outs[i] may be
+ * h_grads[i] (where factor is 1 it is then not written); no output may overlap another
+ * or another tensor's gradient otherwise.  h_outs NULL: all in place.  Counts may be 0.
+ * max_norm >= 0, infinity for the norm alone.  Squares are summed without overflow
+ * or underflow whatever the magnitudes.  0 <= n_tensors <= 65536. */
+int tee_op_clip_gradients(tee_ctx* ctx, const void* const* h_grads, const int32_t* h_types, const int64_t* h_counts,
+                          void* const* h_outs, int n_tensors, float max_norm, float* d_norm, void* d_ws,
+                          size_t ws_bytes, void* stream);
+long long tee_clip_gradients_workspace(int n_tensors);
 
 #ifdef __cplusplus
 }

@@ -110,6 +110,17 @@ SIGNATURES = {
     "tee_vocab_loss_forward_workspace": (ctypes.c_longlong, [_i, _i, _i]),
     "tee_op_vocab_loss_backward": (_i, [_ctx, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _sz, _vp]),
     "tee_vocab_loss_backward_workspace": (ctypes.c_longlong, [_i, _i, _i]),
+    "tee_op_rope_forward": (_i, [_ctx, _vp, _i, _vp, _vp, _i, _i, ctypes.c_float, _vp]),
+    "tee_op_rope_backward": (_i, [_ctx, _vp, _i, _vp, _vp, _i, _i, ctypes.c_float, _vp]),
+    "tee_op_attention_forward": (_i, [_ctx, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _sz, _vp]),
+    "tee_attention_forward_workspace": (ctypes.c_longlong, [_i, _i, _i]),
+    "tee_op_attention_backward": (_i, [_ctx, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _sz, _vp]),
+    "tee_attention_backward_workspace": (ctypes.c_longlong, [_i, _i, _i]),
+    "tee_op_geglu_forward": (_i, [_ctx, _vp, _vp, _vp, _i, _i, _i, _vp]),
+    "tee_op_geglu_backward": (_i, [_ctx, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _sz, _vp]),
+    "tee_geglu_backward_workspace": (ctypes.c_longlong, [_i, _i, _i]),
+    "tee_op_clip_gradients": (_i, [_ctx, _vp, _vp, _vp, _vp, _i, ctypes.c_float, _vp, _vp, _sz, _vp]),
+    "tee_clip_gradients_workspace": (ctypes.c_longlong, [_i]),
 }
 
 _LIB = None

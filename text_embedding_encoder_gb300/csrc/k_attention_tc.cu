@@ -45,11 +45,13 @@
 //                   unit's O / l is read and stored as bf16 after the next
 //                   unit's first P hand-off.
 // Pipeline counters run across units; every wait is bounded.
-#include "tee_internal.cuh"
+#include "train_internal.cuh"
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <math.h>
+
+#include <algorithm>
 #include <mutex>
 
 #include "tc_ptx.cuh"
@@ -88,6 +90,12 @@ struct AttnParams {
     float scale_log2;       // log2(e) / sqrt(64)
     bf16* o;                // [T, hidden]
     unsigned int* status;
+    // TRAIN: slots holds *n_items work items without a head; every CTA takes the units
+    // (item, head) that attn_unit gives it
+    const int* n_items;
+    int n_heads, T;
+    float* lse;             // [n_heads, T]
+    const bf16* qkv;
 };
 
 __device__ __forceinline__ int n_kv_tiles(const int4& it) { return (it.w - it.z + BKV - 1) / BKV; }
@@ -144,9 +152,34 @@ __device__ __forceinline__ void zero_pack(uint32_t* pk) {
     for (int c = B / 2; c < E / 2; ++c) pk[c] = 0u;
 }
 
+// The output of one row whose products met NaN or infinities of keys that it does not
+// see (their probability is 0, but 0 x NaN is NaN): the row's own keys [lo, hi) again,
+// outside the tensor cores, by a whole warp.  Returns o[half * 32 + lane].
+__device__ __noinline__ float attn_row_again(const AttnParams& p, int row, int head, int half, int lo, int hi, float lse2) {
+    const int lane = threadIdx.x & 31;
+    const size_t stride = 3 * (size_t)p.hidden;
+    const bf16* at = p.qkv + head * HD;
+    const __nv_bfloat162 q = *reinterpret_cast<const __nv_bfloat162*>(at + row * stride + 2 * lane);
+    float o = 0.f;
+    for (int j = lo; j < hi; ++j) {
+        const bf16* kv = at + j * stride;
+        const __nv_bfloat162 k = *reinterpret_cast<const __nv_bfloat162*>(kv + p.hidden + 2 * lane);
+        float s = __low2float(q) * __low2float(k) + __high2float(q) * __high2float(k);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+        o += ex2_approx(fmaf(s, p.scale_log2, -lse2)) * __bfloat162float(kv[2 * p.hidden + half * 32 + lane]);
+    }
+    return o;
+}
+
 // WINDOW: the ±window layers (per-row text bounds, 32-column block skipping);
 // otherwise the global layers, whose rows all see the same keys.
-template <bool WINDOW>
+// TRAIN: the training operator (tee_train.h): work items planned on the device, the
+// rows' log sums written beside their outputs, and rows that see no trace of what lies
+// outside their text: rows of V behind the item's keys are zeroed in shared memory
+// (they may be anything, also behind the last text), and a row that is not finite, in
+// items whose rows see different keys, is computed again from its own.
+template <bool WINDOW, bool TRAIN>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tm, AttnParams p) {
     extern __shared__ uint8_t smem_raw[];
@@ -187,6 +220,25 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     pdl_wait();
     pdl_trigger();
 
+    // this CTA's units are slot(i0) .. slot(i1 - 1)
+    int i0, i1;
+    if constexpr (TRAIN) {
+        i0 = 0;
+        i1 = attn_units_of(*p.n_items * p.n_heads, blockIdx.x, gridDim.x);
+    } else {
+        i0 = p.slot_off[blockIdx.x], i1 = p.slot_off[blockIdx.x + 1];
+    }
+    auto slot = [&](int i) -> int4 {
+        if constexpr (TRAIN) {
+            const int u = attn_unit(i, blockIdx.x, gridDim.x), item = u / p.n_heads;
+            int4 it = p.slots[item];
+            it.y |= (u - item * p.n_heads) << 16;
+            return it;
+        } else {
+            return p.slots[i];
+        }
+    };
+
     if (warp == 0) {
         // ---------------- TMA producer ----------------
         if (lane == 0) {
@@ -195,11 +247,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             uint32_t g = 0;   // KV tiles issued
             int ui = 0;
             bool ok = true;
-            const int i0 = p.slot_off[blockIdx.x], i1 = p.slot_off[blockIdx.x + 1];
-            int4 it_next = i0 < i1 ? p.slots[i0] : make_int4(0, 0, 0, 0);   // units are read one ahead
+            int4 it_next = i0 < i1 ? slot(i0) : make_int4(0, 0, 0, 0);   // units are read one ahead
             for (int i = i0; i < i1 && ok; ++i, ++ui) {
                 const int4 it = it_next;
-                if (i + 1 < i1) it_next = p.slots[i + 1];
+                if (i + 1 < i1) it_next = slot(i + 1);
                 const int head = it.y >> 16;
                 const int nk = n_kv_tiles(it);
                 const int qb = ui & 1;
@@ -265,11 +316,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             uint32_t t = 0;          // tiles whose S has been issued (global)
             bool ok = true;
             int ui = 0;
-            const int i0 = p.slot_off[blockIdx.x], i1 = p.slot_off[blockIdx.x + 1];
-            int4 it_next = i0 < i1 ? p.slots[i0] : make_int4(0, 0, 0, 0);
+            int4 it_next = i0 < i1 ? slot(i0) : make_int4(0, 0, 0, 0);
             for (int i = i0; i < i1 && ok; ++i, ++ui) {
                 const int nk = n_kv_tiles(it_next);
-                if (i + 1 < i1) it_next = p.slots[i + 1];
+                if (i + 1 < i1) it_next = slot(i + 1);
                 const int qb = ui & 1;
                 if (!mbar_wait(bar(B_QF + qb), (ui >> 1) & 1, abort_flag)) break;
                 const uint64_t qdesc = sw128_desc(sbase + OFF_Q + qb * TILE_BYTES);
@@ -354,6 +404,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         uint32_t t_p = 0;
         int ub_p = 0;
         bf16* dst_p = nullptr;
+        float m_p = 0.f;                      // TRAIN: the unit's reference maximum, row, and the keys it sees
+        int row_p = 0, head_p = 0, lo_p = 0, hi_p = 0;
         auto finalize = [&](bool exchanged) -> bool {
             if (!pv_done(t_p)) return false;
             tc_fence_after();
@@ -366,11 +418,26 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 pair_sync();
                 l_tot_p = l_p + red_l[(ub_p * 2 + (half ^ 1)) * 128 + r];
             }
-            if (dst_p) {
-                const float inv = 1.0f / l_tot_p;
+            const float inv = 1.0f / l_tot_p;
 #pragma unroll
-                for (int d = 0; d < 32; ++d) o[d] *= inv;
-                store_bf16x32(dst_p, o);
+            for (int d = 0; d < 32; ++d) o[d] *= inv;
+            if (dst_p) store_bf16x32(dst_p, o);
+            if constexpr (TRAIN) {
+                const float lse2 = m_p + log2f(l_tot_p);
+                if (dst_p && half == 0) p.lse[(size_t)head_p * p.T + row_p] = lse2 * 0.69314718055994531f;
+                float z = 0.f;                // not a number where one of the row's outputs is not finite
+#pragma unroll
+                for (int d = 0; d < 32; ++d) z = fmaf(o[d], 0.f, z);
+                unsigned again = __ballot_sync(0xffffffffu, dst_p != nullptr && lo_p < hi_p && !(z == 0.f));
+                while (again) {
+                    const int l = __ffs(again) - 1;
+                    again &= again - 1;
+                    const int row = __shfl_sync(0xffffffffu, row_p, l);
+                    const float v = attn_row_again(p, row, head_p, half, __shfl_sync(0xffffffffu, lo_p, l),
+                                                   __shfl_sync(0xffffffffu, hi_p, l), __shfl_sync(0xffffffffu, lse2, l));
+                    p.o[(size_t)row * p.hidden + head_p * HD + half * 32 + lane] = __float2bfloat16_rn(v);
+                }
+                __syncwarp();
             }
             pend = false;
             return true;
@@ -382,16 +449,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             return r < (x.y & 0xffff) ? p.row_tb[x.x + r] : make_int2(0, 0);
         };
         int ui = 0;
-        const int i0 = p.slot_off[blockIdx.x], i1 = p.slot_off[blockIdx.x + 1];
-        int4 it_next = i0 < i1 ? p.slots[i0] : make_int4(0, 0, 0, 0);
-        int4 it_next2 = i0 + 1 < i1 ? p.slots[i0 + 1] : make_int4(0, 0, 0, 0);
+        int4 it_next = i0 < i1 ? slot(i0) : make_int4(0, 0, 0, 0);
+        int4 it_next2 = i0 + 1 < i1 ? slot(i0 + 1) : make_int4(0, 0, 0, 0);
         int2 tb_next = row_bounds(it_next);
         for (int i = i0; i < i1 && ok; ++i, ++ui) {
             const int4 it = it_next;
             const int2 tb = tb_next;
             it_next = it_next2;
             if (i + 1 < i1) tb_next = row_bounds(it_next);
-            if (i + 2 < i1) it_next2 = p.slots[i + 2];
+            if (i + 2 < i1) it_next2 = slot(i + 2);
             const int head = it.y >> 16;
             const int q_start = it.x, q_len = it.y & 0xffff, k_lo = it.z, k_hi = it.w;
             const int nk = n_kv_tiles(it);
@@ -522,6 +588,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     else zero_pack<32, 64>(pk);
                 }
                 const float sum = rs.total();
+                if constexpr (TRAIN) {
+                    // rows of V behind the keys (P there is 0, and they may hold anything): whole 128-byte rows of the tile.
+                    // The copy's barrier has completed (S was made from the same stage); waiting on it makes V visible.
+                    const int keys = k_hi - (k_lo + kt * BKV);
+                    if (keys < BKV && k_hi < p.T) {
+                        const int st = t % KV_STAGES;
+                        if (!mbar_wait(bar(B_KVF + st), (t / KV_STAGES) & 1, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        uint4* v16 = reinterpret_cast<uint4*>(smem + OFF_V + st * TILE_BYTES);
+                        for (int c = keys * 8 + (int)threadIdx.x - 64; c < BKV * 8; c += SM_THREADS) v16[c] = make_uint4(0, 0, 0, 0);
+                        fence_proxy_async_smem();
+                    }
+                }
                 tmem_st32_u(tmem_base + lane_off + TM_S + sb * BKV + half * 32, pk);
                 tc_fence_before();
                 mbar_arrive(bar(B_PF + sb));
@@ -537,6 +618,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             t_p = t - 1;
             ub_p = ub;
             dst_p = r < q_len ? p.o + (size_t)qg * p.hidden + head * HD + half * 32 : nullptr;
+            if constexpr (TRAIN) {
+                m_p = m_ref;
+                row_p = qg, head_p = head;
+                // rows of one text that all see the same keys meet no others' values
+                const bool alone = !WINDOW && tb.x == k_lo && tb.y == k_hi;
+                lo_p = alone ? 0 : vis_lo, hi_p = alone ? 0 : vis_hi;
+            }
             pend = true;
         }
         if (ok && pend) ok = finalize(false);
@@ -575,42 +663,66 @@ void init_once() {
 
 }  // namespace
 
-cudaError_t launch_attention_tc(const void* qkv, int T, int H, int n_heads, const int4* d_slots,
-                                const int32_t* d_slot_off, int grid, bool is_global, int window, const int2* row_tb,
-                                void* o, unsigned int* status, cudaStream_t s) {
+namespace {
+
+// Tensor map and attributes of a launch on the current device.
+cudaError_t prepare_launch(const void* qkv, int T, int H, const void* o, CUtensorMap* tm, int* num_sms) {
     std::call_once(g_once, init_once);
     if (g_init_err != cudaSuccess) return g_init_err;
-    if (grid == 0 || T == 0) return cudaSuccess;
-    if (H != n_heads * HD || (reinterpret_cast<uintptr_t>(qkv) & 15) || (reinterpret_cast<uintptr_t>(o) & 15))
-        return cudaErrorInvalidValue;
-    if (!row_tb || !d_slots || !d_slot_off || grid < 0) return cudaErrorInvalidValue;
-    CUtensorMap tm;
+    if ((reinterpret_cast<uintptr_t>(qkv) & 15) || (reinterpret_cast<uintptr_t>(o) & 15)) return cudaErrorInvalidValue;
     cuuint64_t dims[2] = {(cuuint64_t)3 * H, (cuuint64_t)T};
     cuuint64_t strides[1] = {(cuuint64_t)3 * H * 2};
     cuuint32_t box[2] = {(cuuint32_t)HD, (cuuint32_t)BQ};
     cuuint32_t estr[2] = {1, 1};
-    CUresult r = g_encode(&tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(qkv), dims, strides, box, estr,
+    CUresult r = g_encode(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(qkv), dims, strides, box, estr,
                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
-    int dev = 0, num_sms = 0;
-    cudaError_t de = tee_current_device(&dev, &num_sms);
-    if (de != cudaSuccess) return de;
-    {
-        std::lock_guard<std::mutex> lock(g_attr_mu);
-        if (!g_attr_set[dev]) {
-            cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 (int)SMEM_TOTAL);
-            if (e == cudaSuccess)
-                e = cudaFuncSetAttribute(attn_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)SMEM_TOTAL);
+    int dev = 0;
+    cudaError_t e = tee_current_device(&dev, num_sms);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(g_attr_mu);
+    if (!g_attr_set[dev]) {
+        for (auto kernel : {attn_tc_kernel<true, false>, attn_tc_kernel<false, false>, attn_tc_kernel<true, true>,
+                            attn_tc_kernel<false, true>}) {
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_TOTAL);
             if (e != cudaSuccess) return e;
-            g_attr_set[dev] = true;
         }
+        g_attr_set[dev] = true;
     }
-    AttnParams p{d_slots, d_slot_off, row_tb, H, window, 1.4426950408889634f / 8.0f, (bf16*)o, status};
-    cudaError_t e = is_global ? launch_pdl(attn_tc_kernel<false>, dim3(grid), dim3(NUM_THREADS), SMEM_TOTAL, s, tm, p)
-                              : launch_pdl(attn_tc_kernel<true>, dim3(grid), dim3(NUM_THREADS), SMEM_TOTAL, s, tm, p);
+    return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_attention_tc(const void* qkv, int T, int H, int n_heads, const int4* d_slots,
+                                const int32_t* d_slot_off, int grid, bool is_global, int window, const int2* row_tb,
+                                void* o, unsigned int* status, cudaStream_t s) {
+    if (grid == 0 || T == 0) return cudaSuccess;
+    if (H != n_heads * HD) return cudaErrorInvalidValue;
+    if (!row_tb || !d_slots || !d_slot_off || grid < 0) return cudaErrorInvalidValue;
+    CUtensorMap tm;
+    int num_sms = 0;
+    cudaError_t e = prepare_launch(qkv, T, H, o, &tm, &num_sms);
+    if (e != cudaSuccess) return e;
+    AttnParams p{d_slots, d_slot_off, row_tb, H, window, 1.4426950408889634f / 8.0f, (bf16*)o, status, nullptr, 0, 0, nullptr,
+                 nullptr};
+    e = is_global ? launch_pdl(attn_tc_kernel<false, false>, dim3(grid), dim3(NUM_THREADS), SMEM_TOTAL, s, tm, p)
+                  : launch_pdl(attn_tc_kernel<true, false>, dim3(grid), dim3(NUM_THREADS), SMEM_TOTAL, s, tm, p);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
+}
+
+cudaError_t launch_attention_train_tc(const void* qkv, int T, int n_heads, int window, const AttnPlan& plan, int max_items,
+                                      void* o, float* lse, unsigned int* status, cudaStream_t s) {
+    const int H = n_heads * HD;
+    CUtensorMap tm;
+    int num_sms = 0;
+    cudaError_t e = prepare_launch(qkv, T, H, o, &tm, &num_sms);
+    if (e != cudaSuccess) return e;
+    const int grid = (int)std::min<long long>(num_sms, (long long)max_items * n_heads);
+    AttnParams p{plan.items, nullptr, plan.row_tb, H, window, 1.4426950408889634f / 8.0f, (bf16*)o, status,
+                 plan.n_items, n_heads, T, lse, (const bf16*)qkv};
+    return window < 0 ? launch_pdl(attn_tc_kernel<false, true>, dim3(grid), dim3(NUM_THREADS), SMEM_TOTAL, s, tm, p)
+                      : launch_pdl(attn_tc_kernel<true, true>, dim3(grid), dim3(NUM_THREADS), SMEM_TOTAL, s, tm, p);
 }

@@ -1,0 +1,739 @@
+// Attention of a training step over packed texts: the plan that both passes work by,
+// and the backward pass on the 5th-generation tensor cores (sm_103a); tee_train.h has
+// the formulas, k_attention_tc.cu the forward kernel.
+//
+// The probabilities are computed again from lse.  One kernel runs two kinds of units,
+// each a tile of 128 rows of one head against all 128-row tiles that it may see:
+//   rows are queries: S = Q K^T, dP = dO V^T, dQ += dS K;
+//   rows are keys:    S^T = K Q^T, dP^T = V dO^T, dK += dS^T Q, dV += P^T dO,
+// with P = exp2(S log2(e) / 8 - lse / ln 2) and dS = P (dP - delta).  Scores and
+// probabilities are thus made twice, seven products to a pair of tiles instead of
+// five: but no unit adds to another's sums, so nothing waits and nothing depends on
+// an order, and dS goes from the registers to the tensor cores through tensor memory
+// alone (for dQ from the key side it would cross shared memory twice, whose bandwidth
+// the operands of the other products already take).
+#include "gemm_tc.cuh"
+#include "train_internal.cuh"
+
+#include <algorithm>
+#include <mutex>
+#include <type_traits>
+
+#include "tc_ptx.cuh"
+
+namespace {
+
+using namespace tc;
+
+constexpr int HD = 64;
+constexpr int TILE = 128;
+
+// ---------------------------------------------------------------------------
+// the plan
+// ---------------------------------------------------------------------------
+
+constexpr int PLAN_THREADS = 512;
+constexpr int PLAN_ROWS = 32;                 // rows of a row block
+constexpr int PLAN_HEADS = 32;                // heads staged at once
+constexpr int PLAN_SHARED_TEXTS = 2048;       // texts whose lists fit shared memory
+constexpr int PLAN_BUCKETS = TEE_ATTN_MAX_TEXT / TILE + 1;
+
+struct PlanArgs {
+    const int32_t* cu;
+    int T, n_texts, n_heads, window, max_items;
+    AttnPlan plan;
+    const bf16* o;          // backward only
+    const bf16* d_o;
+    const float* lse;
+    unsigned int* status;
+};
+
+// The first index of cu[0 .. n] whose value is above v, n + 1 if none is.
+__device__ __forceinline__ int first_above(const int32_t* cu, int n, int v) {
+    int lo = 0, hi = n + 1;
+    while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (cu[mid] > v) hi = mid;
+        else lo = mid + 1;
+    }
+    return lo;
+}
+
+// Block 0 lists the work items, the others prepare PLAN_ROWS rows each.
+//
+// Items of whole-text layers: a text of more than 128 tokens gives one per 128 rows;
+// shorter ones share tiles, each the longest run of consecutive such texts that spans
+// at most 128 tokens.  Where a run's tiles start depends on where the one before
+// ended: with next(j) the start after one at j, the starts are what is reached from 0,
+// found by doubling the steps (log2 of the number of texts).
+// Items of window layers: 128 rows of the packed batch, whatever texts they are of.
+__global__ void __launch_bounds__(PLAN_THREADS) attn_plan_kernel(const PlanArgs a) {
+    __shared__ int lists[3 * (PLAN_SHARED_TEXTS + 1)];
+    __shared__ int bucket[PLAN_BUCKETS + 1];
+    __shared__ int bad;
+    __shared__ float stage[PLAN_HEADS][PLAN_ROWS + 1];
+    pdl_wait();
+    pdl_trigger();
+    const int n = a.n_texts, tid = threadIdx.x;
+    if (blockIdx.x > 0) {
+        const int row0 = (blockIdx.x - 1) * PLAN_ROWS;
+        if (tid < PLAN_ROWS && row0 + tid < a.T) {
+            const int t = row0 + tid, j = first_above(a.cu, n, t);
+            int2 tb = make_int2(0, 0);
+            if (j >= 1 && j <= n) tb = make_int2(max(a.cu[j - 1], 0), min(a.cu[j], a.T));
+            a.plan.row_tb[t] = tb;
+        }
+        if (!a.o) return;
+        // delta = sum_d do o: a head by eight lanes, eight columns each
+        const int warp = tid >> 5, lane = tid & 31, H = a.n_heads * HD;
+        for (int h0 = 0; h0 < a.n_heads; h0 += PLAN_HEADS) {
+            const int nh = min(PLAN_HEADS, a.n_heads - h0);
+            for (int r = warp; r < PLAN_ROWS && row0 + r < a.T; r += PLAN_THREADS / 32) {
+                for (int g = lane >> 3; g < (nh + 3) / 4 * 4; g += 4) {
+                    float s = 0.f;
+                    if (g < nh) {
+                        const size_t at = (size_t)(row0 + r) * H + (size_t)(h0 + g) * HD + (lane & 7) * 8;
+                        float x[8], y[8];
+                        load_vec(a.o + at, x);
+                        load_vec(a.d_o + at, y);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) s = fmaf(x[i], y[i], s);
+                    }
+#pragma unroll
+                    for (int d = 4; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+                    if (g < nh && (lane & 7) == 0) stage[g][r] = -s;
+                }
+            }
+            __syncthreads();
+            for (int i = tid; i < nh * PLAN_ROWS; i += PLAN_THREADS) {
+                const int g = i / PLAN_ROWS, r = i % PLAN_ROWS;
+                if (row0 + r < a.T) {
+                    const size_t at = (size_t)(h0 + g) * a.T + row0 + r;
+                    a.plan.ndelta[at] = stage[g][r];
+                    a.plan.nlse2[at] = a.lse[at] * -1.4426950408889634f;
+                }
+            }
+            __syncthreads();
+        }
+        return;
+    }
+    if (tid == 0) bad = 0;
+    for (int i = tid; i <= PLAN_BUCKETS; i += PLAN_THREADS) bucket[i] = 0;
+    __syncthreads();
+    int wrong = 0;
+    for (int j = tid; j < n; j += PLAN_THREADS) {
+        const int c0 = a.cu[j], c1 = a.cu[j + 1];
+        wrong |= c0 < 0 || c1 < c0 || c1 > a.T || c1 - c0 > TEE_ATTN_MAX_TEXT || (j == 0 && c0 != 0);
+    }
+    if (wrong) bad = 1;
+    __syncthreads();
+    if (bad) {
+        if (tid == 0) {
+            *a.plan.n_items = 0;
+            atomicOr(a.status, TEE_STATUS_BAD_ID);
+        }
+        return;
+    }
+    const int end = a.cu[n];
+    if (a.window >= 0) {
+        const int tiles = (end + TILE - 1) / TILE;
+        for (int i = tid; i < tiles; i += PLAN_THREADS) {
+            const int q0 = i * TILE, ql = min(TILE, end - q0);
+            const int j0 = first_above(a.cu, n, q0), j1 = first_above(a.cu, n, q0 + ql - 1);   // ends of the first and last row's texts
+            a.plan.items[i] = make_int4(q0, ql, max(a.cu[j0 - 1], q0 - a.window),
+                                        (int)min((long long)a.cu[j1], (long long)q0 + ql + a.window));
+        }
+        if (tid == 0) *a.plan.n_items = tiles;
+        return;
+    }
+    const bool fits = n <= PLAN_SHARED_TEXTS;
+    int* from = fits ? lists : a.plan.scratch;
+    int* to = from + n + 1;
+    int* mark = to + n + 1;
+    for (int j = tid; j <= n; j += PLAN_THREADS) {
+        int e = n;
+        if (j < n) {
+            const int c = a.cu[j];
+            e = a.cu[j + 1] - c > TILE ? j + 1 : first_above(a.cu, n, c + TILE) - 1;
+        }
+        from[j] = e;
+        mark[j] = j == 0;
+    }
+    __syncthreads();
+    for (int step = 1; step < n; step *= 2) {
+        for (int j = tid; j < n; j += PLAN_THREADS)
+            if (mark[j]) mark[from[j]] = 1;
+        __syncthreads();
+        for (int j = tid; j <= n; j += PLAN_THREADS) to[j] = from[from[j]];
+        __syncthreads();
+        int* const x = from;
+        from = to;
+        to = x;
+    }
+    // a start's items and their keys in tiles of 128
+    auto start = [&](int j, int& tiles, int& c0, int& c1) {
+        if (!mark[j]) return 0;
+        c0 = a.cu[j], c1 = a.cu[j + 1];
+        if (c1 - c0 > TILE) {
+            tiles = (c1 - c0 + TILE - 1) / TILE;
+            return tiles;
+        }
+        c1 = a.cu[first_above(a.cu, n, c0 + TILE) - 1];
+        tiles = 1;
+        return c1 > c0 ? 1 : 0;
+    };
+    for (int j = tid; j < n; j += PLAN_THREADS) {
+        int tiles, c0, c1;
+        const int items = start(j, tiles, c0, c1);
+        if (items) atomicAdd(&bucket[tiles], items);
+    }
+    __syncthreads();
+    if (tid < 32) {   // where each bucket's items begin, the most keys first
+        int base = 0;
+        for (int i0 = PLAN_BUCKETS; i0 >= 0; i0 -= 32) {
+            const int i = i0 - tid, v = i >= 0 ? bucket[i] : 0;
+            int inc = v;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, inc, d);
+                if (tid >= d) inc += up;
+            }
+            if (i >= 0) bucket[i] = base + inc - v;
+            base += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        if (tid == 0) *a.plan.n_items = min(base, a.max_items);
+    }
+    __syncthreads();
+    // (which of two equally long items comes first has no effect on results)
+    for (int j = tid; j < n; j += PLAN_THREADS) {
+        int tiles, c0, c1;
+        const int items = start(j, tiles, c0, c1);
+        if (!items) continue;
+        const int at = atomicAdd(&bucket[tiles], items);
+        for (int i = 0; i < items && at + i < a.max_items; ++i)
+            a.plan.items[at + i] = make_int4(c0 + i * TILE, min(TILE, c1 - c0 - i * TILE), c0, c1);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// the backward kernel
+// ---------------------------------------------------------------------------
+
+constexpr int STAGES = 4;
+constexpr int FIRST_WORKER = 3, WORKERS = 16;   // warps 3 .. 18
+constexpr int NUM_THREADS = 32 * (FIRST_WORKER + WORKERS);
+constexpr uint32_t TILE_BYTES = TILE * HD * 2;                       // 16 KB
+constexpr uint32_t OFF_ROWS = 0;                                     // 2 buffers of two tiles
+constexpr uint32_t OFF_COLS = OFF_ROWS + 4 * TILE_BYTES;             // STAGES of two tiles
+constexpr uint32_t OFF_STATS = OFF_COLS + STAGES * 2 * TILE_BYTES;   // STAGES of {-lse2[128], -delta[128]}
+constexpr uint32_t OFF_BAR = OFF_STATS + STAGES * 2 * TILE * 4;
+constexpr int B_RF = 0, B_RE = 2, B_CF = 4, B_CE = B_CF + STAGES, B_SF = B_CE + STAGES, B_XF = B_SF + STAGES, B_X2R = B_XF + 2, B_PF = B_X2R + 1,
+              B_OF = B_PF + 2, B_OE = B_OF + 1, B_DONE = B_OE + 1, N_BARS = B_DONE + 1;
+constexpr uint32_t SMEM_TOTAL = OFF_BAR + N_BARS * 8 + 16 + 1024;
+static_assert(SMEM_TOTAL <= 227 * 1024, "shared memory");
+// Tensor memory: X1 = S of even and odd tiles, X2 = dP of the current one, the outputs.
+// A worker writes dS and P over columns of S that it read itself, so workers need not
+// wait for one another.
+constexpr uint32_t TM_X1 = 0, TM_X2 = 256, TM_O = 384, TMEM_COLS = 512;
+constexpr float SCALE_LOG2 = 1.4426950408889634f / 8.0f;
+
+struct BwdParams {
+    AttnPlan plan;
+    int T, n_heads, hidden, window;
+    const bf16* qkv;
+    const bf16* d_o;
+    bf16* dqkv;
+    unsigned int* status;
+};
+
+// A unit as {q_start, q_len | keys << 8 | head << 16, k_lo, k_hi}; the units of an item:
+// its rows as keys, the longer kind, for every head, then its rows as queries.
+__device__ __forceinline__ int4 bwd_unit(const BwdParams& p, int i) {
+    const int u = attn_unit(i, blockIdx.x, gridDim.x), k = u / p.n_heads, head = u - k * p.n_heads;
+    int4 it = p.plan.items[k >> 1];
+    it.y |= ((k & 1) ^ 1) << 8 | head << 16;
+    return it;
+}
+__device__ __forceinline__ int unit_tiles(const int4& it) { return (it.w - it.z + TILE - 1) / TILE; }
+
+// Column `first` .. of one row's gradients again, outside the tensor cores, by a whole
+// warp: of a row whose products met NaN or infinities of rows that it does not see.
+// Lanes 2k and 2k + 1 of the result hold the row's columns as pairs.
+__device__ __noinline__ void bwd_row_again(const BwdParams& p, int row, int head, bool keys, int lo, int hi, int chunk) {
+    const int lane = threadIdx.x & 31, H = p.hidden;
+    auto two = [&](const bf16* base, size_t at) {
+        return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(base + at + head * HD + 2 * lane));
+    };
+    auto dot = [](float2 a, float2 b) {
+        float s = a.x * b.x + a.y * b.y;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+        return s;
+    };
+    const size_t stride = 3 * (size_t)H;
+    const float2 a1 = two(p.qkv, row * stride + (keys ? H : 0));
+    const float2 a2 = keys ? two(p.qkv, row * stride + 2 * H) : two(p.d_o, (size_t)row * H);
+    float2 o1 = make_float2(0.f, 0.f), o2 = o1;
+    for (int j = lo; j < hi; ++j) {
+        const float2 b1 = two(p.qkv, j * stride + (keys ? 0 : H));
+        const float2 b2 = keys ? two(p.d_o, (size_t)j * H) : two(p.qkv, j * stride + 2 * H);
+        const size_t s = (size_t)head * p.T + (keys ? j : row);
+        const float e = ex2_approx(fmaf(dot(a1, b1), SCALE_LOG2, p.plan.nlse2[s]));
+        const float d = e * (dot(a2, b2) + p.plan.ndelta[s]);
+        o1.x = fmaf(d, b1.x, o1.x), o1.y = fmaf(d, b1.y, o1.y);
+        o2.x = fmaf(e, b2.x, o2.x), o2.y = fmaf(e, b2.y, o2.y);
+    }
+    if (lane / 8 != chunk) return;
+    bf16* dst = p.dqkv + row * stride + head * HD + 2 * lane;
+    *reinterpret_cast<uint32_t*>(dst + (keys ? H : 0)) = pack_bf16x2(o1.x * 0.125f, o1.y * 0.125f);
+    if (keys) *reinterpret_cast<uint32_t*>(dst + 2 * H) = pack_bf16x2(o2.x, o2.y);
+}
+
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+    attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __grid_constant__ CUtensorMap tm_do, const BwdParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + N_BARS);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    auto bar = [&](int i) { return smem_u32(bars + i); };
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(bar(B_RF + b), 1);
+            mbar_init(bar(B_RE + b), 1);
+            mbar_init(bar(B_XF + b), 1);
+            mbar_init(bar(B_PF + b), WORKERS);
+        }
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(bar(B_CF + s), 1);
+            mbar_init(bar(B_CE + s), 1);
+            mbar_init(bar(B_SF + s), 1);
+        }
+        mbar_init(bar(B_X2R), WORKERS);
+        mbar_init(bar(B_OF), 1);
+        mbar_init(bar(B_OE), WORKERS);
+        mbar_init(bar(B_DONE), 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) tmem_alloc<1>(smem_u32(tmem_slot), TMEM_COLS);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    pdl_wait();
+    pdl_trigger();
+
+    const int n_units = attn_units_of(*p.plan.n_items * 2 * p.n_heads, blockIdx.x, gridDim.x);
+    // a wait that gives up does so for the whole warp
+    auto all = [](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
+
+    if (warp == 0) {
+        // ---------------- TMA producer ----------------
+        if (lane == 0) {
+            uint32_t t = 0;
+            int ui = 0;
+            bool ok = true;
+            for (; ui < n_units && ok; ++ui) {
+                const int4 it = bwd_unit(p, ui);
+                const int head = it.y >> 16, nk = unit_tiles(it), rb = ui & 1;
+                const bool keys = it.y >> 8 & 1;
+                const int xq = head * HD, xk = p.hidden + head * HD, xv = 2 * p.hidden + head * HD;
+                if (!mbar_wait(bar(B_RE + rb), ((ui >> 1) & 1) ^ 1, abort_flag)) break;
+                mbar_expect_tx(bar(B_RF + rb), 2 * TILE_BYTES);
+                const uint32_t a = sbase + OFF_ROWS + rb * 2 * TILE_BYTES;
+                tma_load_2d(a, &tm_qkv, keys ? xk : xq, it.x, bar(B_RF + rb));
+                tma_load_2d(a + TILE_BYTES, keys ? &tm_qkv : &tm_do, keys ? xv : xq, it.x, bar(B_RF + rb));
+                for (int kt = 0; kt < nk; ++kt, ++t) {
+                    const int s = t % STAGES, y = it.z + kt * TILE;
+                    if (!mbar_wait(bar(B_CE + s), ((t / STAGES) & 1) ^ 1, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_expect_tx(bar(B_CF + s), 2 * TILE_BYTES);
+                    const uint32_t b = sbase + OFF_COLS + s * 2 * TILE_BYTES;
+                    tma_load_2d(b, &tm_qkv, keys ? xq : xk, y, bar(B_CF + s));
+                    tma_load_2d(b + TILE_BYTES, keys ? &tm_do : &tm_qkv, keys ? xq : xv, y, bar(B_CF + s));
+                }
+            }
+            // no copy may still be landing in shared memory when the CTA exits
+            for (int b = 0; b < 2 && b < ui; ++b) {
+                const int u = (ui - 1 - b);
+                mbar_wait_drain(bar(B_RF + (u & 1)), (u >> 1) & 1);
+            }
+            for (uint32_t s = 0; s < STAGES && s < t; ++s) {
+                const uint32_t u = t - 1 - s;
+                mbar_wait_drain(bar(B_CF + u % STAGES), (u / STAGES) & 1);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 2) {
+        // ---------------- statistics of the columns, where columns are queries ----------------
+        uint32_t t = 0;
+        bool ok = true;
+        for (int ui = 0; ui < n_units && ok; ++ui) {
+            const int4 it = bwd_unit(p, ui);
+            const int head = it.y >> 16, nk = unit_tiles(it);
+            const bool keys = it.y >> 8 & 1;
+            for (int kt = 0; kt < nk; ++kt, ++t) {
+                const int s = t % STAGES;
+                float v[2][4];
+                if (keys) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int row = it.z + kt * TILE + i * 32 + lane;
+                        const size_t at = (size_t)head * p.T + row;
+                        v[0][i] = row < it.w ? p.plan.nlse2[at] : 0.f;
+                        v[1][i] = row < it.w ? p.plan.ndelta[at] : 0.f;
+                    }
+                }
+                if (!all(mbar_wait(bar(B_CE + s), ((t / STAGES) & 1) ^ 1, abort_flag))) {
+                    ok = false;
+                    break;
+                }
+                if (keys) {
+                    float* stats = reinterpret_cast<float*>(smem + OFF_STATS) + s * 2 * TILE;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        stats[i * 32 + lane] = v[0][i];
+                        stats[TILE + i * 32 + lane] = v[1][i];
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_SF + s));
+            }
+        }
+    } else if (warp == 1) {
+        // ---------------- MMA issuer ----------------
+        if (lane == 0) {
+            constexpr uint32_t idesc_x = make_idesc(TILE, TILE), idesc_o = make_idesc(TILE, HD) | IDESC_B_MN_MAJOR;
+            struct Pend {
+                uint32_t t;
+                int ui;
+                bool any, first, last, keys;
+            };
+            Pend pend{};
+            // the outputs' products of a tile whose P and dS the workers have written
+            auto outputs = [&](const Pend& q) -> bool {
+                if (!q.any) return true;
+                if (!mbar_wait(bar(B_PF + (q.t & 1)), (q.t >> 1) & 1, abort_flag)) return false;
+                // the unit's first: the workers have read the one before
+                if (q.first && !mbar_wait(bar(B_OE), (q.ui & 1) ^ 1, abort_flag)) return false;
+                tc_fence_after();
+                const int st = q.t % STAGES;
+                const uint32_t x = tmem_base + TM_X1 + (q.t & 1) * TILE, b = sbase + OFF_COLS + st * 2 * TILE_BYTES;
+#pragma unroll
+                for (int k = 0; k < TILE / 16; ++k)
+                    mma_bf16_ts(tmem_base + TM_O, x + k * 16, sw128_desc_mn(b + k * 2048), idesc_o,
+                                !(q.first && k == 0));
+                if (q.keys) {
+#pragma unroll
+                    for (int k = 0; k < TILE / 16; ++k)
+                        mma_bf16_ts(tmem_base + TM_O + HD, x + k * 16 + 8,
+                                    sw128_desc_mn(b + TILE_BYTES + k * 2048), idesc_o, !(q.first && k == 0));
+                }
+                mma_commit(bar(B_CE + st));
+                if (q.last) mma_commit(bar(B_OF));
+                return true;
+            };
+            uint32_t t = 0;
+            bool ok = true;
+            for (int ui = 0; ui < n_units && ok; ++ui) {
+                const int4 it = bwd_unit(p, ui);
+                const int nk = unit_tiles(it), rb = ui & 1;
+                if (!mbar_wait(bar(B_RF + rb), (ui >> 1) & 1, abort_flag)) break;
+                const uint32_t a = sbase + OFF_ROWS + rb * 2 * TILE_BYTES;
+                const uint64_t a1 = sw128_desc(a), a2 = sw128_desc(a + TILE_BYTES);
+                for (int kt = 0; kt < nk; ++kt, ++t) {
+                    const int st = t % STAGES;
+                    ok = mbar_wait(bar(B_CF + st), (t / STAGES) & 1, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t b = sbase + OFF_COLS + st * 2 * TILE_BYTES;
+                    const uint64_t b1 = sw128_desc(b), b2 = sw128_desc(b + TILE_BYTES);
+                    // (the products of tile t - 2, which read this half of X1, were issued before)
+#pragma unroll
+                    for (int k = 0; k < HD / 16; ++k)
+                        mma_bf16(tmem_base + TM_X1 + (t & 1) * TILE, a1 + 2 * k, b1 + 2 * k, idesc_x, k != 0);
+                    ok = t == 0 || mbar_wait(bar(B_X2R), (t - 1) & 1, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < HD / 16; ++k) mma_bf16(tmem_base + TM_X2, a2 + 2 * k, b2 + 2 * k, idesc_x, k != 0);
+                    mma_commit(bar(B_XF + (t & 1)));
+                    if (kt == nk - 1) mma_commit(bar(B_RE + rb));
+                    ok = outputs(pend);
+                    if (!ok) break;
+                    pend = Pend{t, ui, true, kt == 0, kt == nk - 1, (it.y >> 8 & 1) != 0};
+                }
+            }
+            if (ok) outputs(pend);
+            // every MMA issued must be finished before TMEM is freed
+            mma_commit(bar(B_DONE));
+            mbar_wait_drain(bar(B_DONE), 0);
+        }
+        __syncwarp();
+    } else {
+        // ---------------- workers: thread = row, 32 columns of each tile ----------------
+        const int quad = warp & 3, chunk = (warp - FIRST_WORKER) >> 2;
+        const int r = quad * 32 + lane;
+        const uint32_t lanes = tmem_base + ((uint32_t)(quad * 32) << 16);
+        const uint64_t sl2 = f2_pack(SCALE_LOG2, SCALE_LOG2);
+        uint32_t t = 0;
+        bool ok = true;
+
+        // the unit before's outputs, read once this unit's first tile is handed over
+        bool pending = false, keys_p = false;
+        int ui_p = 0, row_p = 0, head_p = 0, lo_p = 0, hi_p = 0;
+        auto finish = [&]() -> bool {
+            if (!all(mbar_wait(bar(B_OF), ui_p & 1, abort_flag))) return false;
+            tc_fence_after();
+            float o1[16], o2[16];
+            tmem_ld16_issue(lanes + TM_O + chunk * 16, o1);
+            if (keys_p) tmem_ld16_issue(lanes + TM_O + HD + chunk * 16, o2);
+            tmem_wait_ld();
+            tmem_tie16(o1);
+            if (keys_p) tmem_tie16(o2);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_OE));
+            float z = 0.f;   // not a number where one of the sums is not finite
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o1[i] *= 0.125f, z = fmaf(o1[i], 0.f, z);
+            if (keys_p) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) z = fmaf(o2[i], 0.f, z);
+            }
+            auto store = [&](bf16* dst, const float (&v)[16]) {
+                float a[8], b[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) a[i] = v[i], b[i] = v[8 + i];
+                store_vec(dst, a);
+                store_vec(dst + 8, b);
+            };
+            if (row_p >= 0) {
+                bf16* dst = p.dqkv + (size_t)row_p * 3 * p.hidden + head_p * HD + chunk * 16;
+                store(dst + (keys_p ? p.hidden : 0), o1);
+                if (keys_p) store(dst + 2 * p.hidden, o2);
+            }
+            unsigned again = __ballot_sync(0xffffffffu, row_p >= 0 && lo_p < hi_p && !(z == 0.f));
+            while (again) {
+                const int l = __ffs(again) - 1;
+                again &= again - 1;
+                bwd_row_again(p, __shfl_sync(0xffffffffu, row_p, l), head_p, keys_p, __shfl_sync(0xffffffffu, lo_p, l),
+                              __shfl_sync(0xffffffffu, hi_p, l), chunk);
+            }
+            __syncwarp();
+            pending = false;
+            return true;
+        };
+
+        for (int ui = 0; ui < n_units && ok; ++ui) {
+            const int4 it = bwd_unit(p, ui);
+            const int head = it.y >> 16, q_len = it.y & 0xff, k_lo = it.z, k_hi = it.w, nk = unit_tiles(it);
+            const bool keys = it.y >> 8 & 1;
+            const int row = it.x + r;
+            // the columns that this row sees: its own text, and in window layers the window in it
+            int vis_lo = 0, vis_hi = 0;
+            bool alone = false;
+            float nl = 0.f, nd = 0.f;
+            if (r < q_len) {
+                const int2 tb = p.plan.row_tb[row];
+                vis_lo = max(tb.x, k_lo), vis_hi = min(tb.y, k_hi);
+                if (p.window >= 0) vis_lo = max(vis_lo, row - p.window), vis_hi = min(vis_hi, row + p.window + 1);
+                alone = p.window < 0 && tb.x == k_lo && tb.y == k_hi;
+                if (!keys) nl = p.plan.nlse2[(size_t)head * p.T + row], nd = p.plan.ndelta[(size_t)head * p.T + row];
+            }
+            const uint64_t nl2 = f2_pack(nl, nl), nd2 = f2_pack(nd, nd);
+            for (int kt = 0; kt < nk; ++kt, ++t) {
+                const int b = t & 1, st = t % STAGES;
+                const int c0 = k_lo + kt * TILE + chunk * 32, lo = vis_lo - c0, hi = vis_hi - c0;
+                const bool any = __any_sync(0xffffffffu, lo < hi && lo < 32 && hi > 0);
+                const bool whole = __all_sync(0xffffffffu, lo <= 0 && hi >= 32);
+                if (!all(mbar_wait(bar(B_XF + b), (t >> 1) & 1, abort_flag))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t xt = lanes + TM_X1 + b * TILE + chunk * 32;
+                if (!any) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(B_X2R));
+                    uint32_t zero[16] = {};
+                    tmem_st16_u(xt, zero);
+                    tmem_st16_u(xt + 16, zero);
+                } else {
+                    // 16 columns at a time: dS as bf16 pairs over the first 8 columns of their S, P over the others
+                    float x1[16], x2[2][16];
+                    tmem_ld16_issue(lanes + TM_X2 + chunk * 32, x2[0]);
+                    tmem_ld16_issue(lanes + TM_X2 + chunk * 32 + 16, x2[1]);
+                    tmem_ld16_issue(xt, x1);
+                    tmem_wait_ld();
+                    tmem_tie16(x2[0]);
+                    tmem_tie16(x2[1]);
+                    tmem_tie16(x1);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(B_X2R));
+                    if (keys && !all(mbar_wait(bar(B_SF + st), (t / STAGES) & 1, abort_flag))) {
+                        ok = false;
+                        break;
+                    }
+                    const float* stats = reinterpret_cast<const float*>(smem + OFF_STATS) + st * 2 * TILE + chunk * 32;
+                    auto columns = [&](auto by_key, auto masked, int c, const float (&x2)[16]) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4) {
+                            uint64_t l2[2] = {nl2, nl2}, d2[2] = {nd2, nd2};
+                            if constexpr (decltype(by_key)::value) {
+                                const float4 a = *reinterpret_cast<const float4*>(stats + c + i);
+                                const float4 d = *reinterpret_cast<const float4*>(stats + TILE + c + i);
+                                l2[0] = f2_pack(a.x, a.y), l2[1] = f2_pack(a.z, a.w);
+                                d2[0] = f2_pack(d.x, d.y), d2[1] = f2_pack(d.z, d.w);
+                            }
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const int k = i + 2 * j;
+                                float e0, e1, s0, s1;
+                                f2_unpack(f2_fma(f2_pack(x1[k], x1[k + 1]), sl2, l2[j]), e0, e1);
+                                e0 = ex2_approx(e0);
+                                e1 = ex2_approx(e1);
+                                f2_unpack(f2_mul(f2_pack(e0, e1), f2_add(f2_pack(x2[k], x2[k + 1]), d2[j])), s0, s1);
+                                if constexpr (decltype(masked)::value) {
+                                    const bool v0 = c + k >= lo && c + k < hi, v1 = c + k + 1 >= lo && c + k + 1 < hi;
+                                    e0 = v0 ? e0 : 0.f, s0 = v0 ? s0 : 0.f;
+                                    e1 = v1 ? e1 : 0.f, s1 = v1 ? s1 : 0.f;
+                                }
+                                pk[k / 2] = pack_bf16(s0, s1);
+                                pk[8 + k / 2] = pack_bf16(e0, e1);
+                            }
+                        }
+                        tmem_st16_u(xt + c, pk);
+                    };
+                    constexpr std::true_type yes{};
+                    constexpr std::false_type no{};
+                    auto both = [&](auto by_key, auto masked) {
+                        columns(by_key, masked, 0, x2[0]);
+                        tmem_ld16_issue(xt + 16, x1);
+                        tmem_wait_ld();
+                        tmem_tie16(x1);
+                        columns(by_key, masked, 16, x2[1]);
+                    };
+                    if (keys) whole ? both(yes, no) : both(yes, yes);
+                    else whole ? both(no, no) : both(no, yes);
+                }
+                // rows behind the last column's text (dS and P there are 0, and they may hold anything)
+                const int cols = k_hi - (k_lo + kt * TILE);
+                if (cols < TILE && k_hi < p.T) {
+                    // (the copy's barrier has completed; waiting on it makes the tiles visible)
+                    if (!all(mbar_wait(bar(B_CF + st), (t / STAGES) & 1, abort_flag))) {
+                        ok = false;
+                        break;
+                    }
+                    uint4* v16 = reinterpret_cast<uint4*>(smem + OFF_COLS + st * 2 * TILE_BYTES);
+                    for (int c = cols * 8 + (int)threadIdx.x - 32 * FIRST_WORKER; c < TILE * 8; c += 32 * WORKERS) {
+                        v16[c] = make_uint4(0, 0, 0, 0);
+                        v16[TILE * 8 + c] = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_PF + b));
+                if (kt == 0 && pending && !finish()) {
+                    ok = false;
+                    break;
+                }
+            }
+            if (!ok) break;
+            pending = true;
+            ui_p = ui, keys_p = keys, head_p = head;
+            row_p = r < q_len ? row : -1;
+            lo_p = alone ? 0 : vis_lo, hi_p = alone ? 0 : vis_hi;
+        }
+        if (ok && pending) finish();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc<1>(tmem_base, TMEM_COLS);
+    }
+    if (threadIdx.x == 0 && *abort_flag) atomicOr(p.status, TEE_STATUS_TIMEOUT);
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+size_t carve(int T, int n_texts, int n_heads, bool backward, void* base, AttnPlan* plan) {
+    WsCarve ws(base);
+    plan->n_items = ws.take<int>(1);
+    plan->items = ws.take<int4>(attention_max_items(T, n_texts));
+    plan->row_tb = ws.take<int2>(T);
+    plan->scratch = n_texts > PLAN_SHARED_TEXTS ? ws.take<int>(3 * ((size_t)n_texts + 1)) : nullptr;
+    plan->nlse2 = backward ? ws.take<float>((size_t)n_heads * T) : nullptr;
+    plan->ndelta = backward ? ws.take<float>((size_t)n_heads * T) : nullptr;
+    return ws.off;
+}
+
+cudaError_t launch_plan(const PlanArgs& a, cudaStream_t s) {
+    return launch_pdl(attn_plan_kernel, dim3(1 + (a.T + PLAN_ROWS - 1) / PLAN_ROWS), dim3(PLAN_THREADS), 0, s, a);
+}
+
+}  // namespace
+
+// Whole texts: at most T / 128 whole tiles, and one more for each long text and each
+// run of short ones.  Of those, the runs' tiles pair up to more than 128 tokens but for
+// the last between two long texts.
+int attention_max_items(int T, int n_texts) {
+    const int tiles = T / TILE;
+    return std::max(1, std::min(T, tiles + std::min(n_texts, 4 * tiles + 8) + 1));
+}
+
+size_t attention_train_ws(int T, int n_texts, int n_heads, bool backward) {
+    AttnPlan plan;
+    return carve(T, n_texts, n_heads, backward, nullptr, &plan);
+}
+
+cudaError_t launch_attention_train_forward(const void* qkv, const int32_t* cu, void* o, float* lse, int T, int n_texts,
+                                           int n_heads, int window, void* ws, unsigned int* status, cudaStream_t s) {
+    const int max_items = attention_max_items(T, n_texts);
+    PlanArgs a{cu, T, n_texts, n_heads, window, max_items, {}, nullptr, nullptr, nullptr, status};
+    carve(T, n_texts, n_heads, false, ws, &a.plan);
+    const cudaError_t e = launch_plan(a, s);
+    if (e != cudaSuccess) return e;
+    return launch_attention_train_tc(qkv, T, n_heads, window, a.plan, max_items, o, lse, status, s);
+}
+
+cudaError_t launch_attention_train_backward(const void* qkv, const int32_t* cu, const void* o, const float* lse,
+                                            const void* d_o, void* dqkv, int T, int n_texts, int n_heads, int window,
+                                            void* ws, unsigned int* status, cudaStream_t s) {
+    static std::mutex mu;
+    static bool attr_set[TEE_MAX_DEVICES] = {};
+    int dev = 0, num_sms = 0;
+    cudaError_t e = tee_current_device(&dev, &num_sms);
+    if (e != cudaSuccess) return e;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (!attr_set[dev]) {
+            e = cudaFuncSetAttribute(attn_bwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_TOTAL);
+            if (e != cudaSuccess) return e;
+            attr_set[dev] = true;
+        }
+    }
+    const int max_items = attention_max_items(T, n_texts), H = n_heads * HD;
+    PlanArgs a{cu, T, n_texts, n_heads, window, max_items, {}, (const bf16*)o, (const bf16*)d_o, lse, status};
+    carve(T, n_texts, n_heads, true, ws, &a.plan);
+    CUtensorMap tm_qkv, tm_do;
+    if ((e = make_tensor_map_2d(&tm_qkv, false, qkv, T, 3 * (uint64_t)H, 3 * (uint64_t)H, TILE, HD)) != cudaSuccess) return e;
+    if ((e = make_tensor_map_2d(&tm_do, false, d_o, T, H, H, TILE, HD)) != cudaSuccess) return e;
+    if ((e = launch_plan(a, s)) != cudaSuccess) return e;
+    BwdParams p{a.plan, T, n_heads, H, window, (const bf16*)qkv, (const bf16*)d_o, (bf16*)dqkv, status};
+    const int grid = (int)std::min<long long>(num_sms, 2LL * max_items * n_heads);
+    return launch_pdl(attn_bwd_kernel, dim3(grid), dim3(NUM_THREADS), SMEM_TOTAL, s, tm_qkv, tm_do, p);
+}

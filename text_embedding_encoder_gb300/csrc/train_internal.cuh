@@ -107,3 +107,54 @@ cudaError_t launch_vocab_loss_backward(const void* x, const void* wt, const int3
                                        const float* gloss, void* dx, void* dw, int N, int V, int H, int ignore_id, void* ws,
                                        unsigned int* status, cudaStream_t s);
 size_t vocab_loss_ws(int N, int V, int H, bool backward);
+
+// Rotary positions of packed qkv [T, 3 * 64 heads]; out may be x.
+cudaError_t launch_rope_train(const void* x, bool is_bf16, const int32_t* pos, void* out, int T, int heads, float base,
+                              bool backward, cudaStream_t s);
+
+// Norm of all tensors and their scaling; the arrays are the host's.
+cudaError_t launch_clip_gradients(const void* const* src, const int32_t* types, const int64_t* counts,
+                                  const void* const* dst, int n_tensors, float max_norm, float* norm, void* ws, cudaStream_t s);
+size_t clip_gradients_ws(int n_tensors);
+
+// ---- attention (training) ----------------------------------------------------------
+#define TEE_ATTN_MAX_TEXT TEE_ATTN_MAX_TEXT_TOKENS
+
+// What the plan kernel leaves on the device for the attention kernels.
+struct AttnPlan {
+    int* n_items;       // work items in use (0 where the texts' offsets are not valid)
+    int4* items;        // {q_start, q_len, k_lo, k_hi}, the longest first: up to 128 rows and the keys they may see
+    int2* row_tb;       // per token: {start, end} of its text, {0, 0} behind the last
+    int* scratch;
+    float* nlse2;       // backward: -lse / ln 2, [n_heads, T]
+    float* ndelta;      // backward: -sum_d do o, [n_heads, T]
+};
+
+// The units of CTA c of G: one of each round of G, in turn from the first CTA on and
+// from the last on.  Units are listed the longest first, so that evens the sums out
+// without the host knowing the texts.
+__device__ __forceinline__ int attn_unit(int i, int c, int G) { return i * G + ((i & 1) ? G - 1 - c : c); }
+__device__ __forceinline__ int attn_units_of(int n, int c, int G) {
+    const int rounds = n / G;
+    return rounds + (((rounds & 1) ? G - 1 - c : c) < n - rounds * G);
+}
+
+int attention_max_items(int T, int n_texts);
+size_t attention_train_ws(int T, int n_texts, int n_heads, bool backward);
+// window < 0: whole texts.
+cudaError_t launch_attention_train_forward(const void* qkv, const int32_t* cu, void* o, float* lse, int T, int n_texts,
+                                           int n_heads, int window, void* ws, unsigned int* status, cudaStream_t s);
+cudaError_t launch_attention_train_backward(const void* qkv, const int32_t* cu, const void* o, const float* lse,
+                                            const void* d_o, void* dqkv, int T, int n_texts, int n_heads, int window,
+                                            void* ws, unsigned int* status, cudaStream_t s);
+// The forward kernel over a plan (the attention kernel of the encoder's pass).
+cudaError_t launch_attention_train_tc(const void* qkv, int T, int n_heads, int window, const AttnPlan& plan, int max_items,
+                                      void* o, float* lse, unsigned int* status, cudaStream_t s);
+
+// ---- gated feed-forward -------------------------------------------------------------
+cudaError_t launch_geglu_train_forward(const void* x, const void* wi, void* z, int T, int H, int I, unsigned int* status,
+                                       cudaStream_t s);
+// dx and dwi may each be NULL.
+cudaError_t launch_geglu_train_backward(const void* x, const void* wi, const void* dz, void* dx, void* dwi, int T, int H,
+                                        int I, void* ws, unsigned int* status, cudaStream_t s);
+size_t geglu_backward_ws(int T, int H, int I);
