@@ -15,6 +15,8 @@
 #include "gemm_tc.cuh"
 #include "train_internal.cuh"
 
+#include <string.h>
+
 #include <algorithm>
 #include <mutex>
 #include <type_traits>
@@ -220,13 +222,21 @@ __global__ void __launch_bounds__(PLAN_THREADS) attn_plan_kernel(const PlanArgs 
 // ---------------------------------------------------------------------------
 
 constexpr int STAGES = 4;
-constexpr int FIRST_WORKER = 3, WORKERS = 16;   // warps 3 .. 18
+constexpr int FIRST_WORKER = 4, WORKERS = 8;   // warps 4 .. 11, two to a quarter of the rows, 64 columns each
+
 constexpr int NUM_THREADS = 32 * (FIRST_WORKER + WORKERS);
 constexpr uint32_t TILE_BYTES = TILE * HD * 2;                       // 16 KB
 constexpr uint32_t OFF_ROWS = 0;                                     // 2 buffers of two tiles
 constexpr uint32_t OFF_COLS = OFF_ROWS + 4 * TILE_BYTES;             // STAGES of two tiles
-constexpr uint32_t OFF_STATS = OFF_COLS + STAGES * 2 * TILE_BYTES;   // STAGES of {-lse2[128], -delta[128]}
-constexpr uint32_t OFF_BAR = OFF_STATS + STAGES * 2 * TILE * 4;
+// Where columns are queries, their lse and delta come as 16 more columns of the
+// operands: the stage's rows hold -8 lse in three bf16 that add up to it, then -delta in
+// three, and the rows' side is ones against the three that S, or dP, is to get.  (Read
+// from shared memory by the workers, a column's two numbers go to 128 threads each: 512
+// bytes a warp for 16 of them, 1024 cycles a tile for what the tensor cores do in 128.)
+constexpr uint32_t EXT_BYTES = TILE * 16 * 2;                        // 4 KB, not swizzled: 8 rows x 16 bytes together
+constexpr uint32_t OFF_EXT = OFF_COLS + STAGES * 2 * TILE_BYTES;     // STAGES
+constexpr uint32_t OFF_ONES = OFF_EXT + STAGES * EXT_BYTES;          // for S, for dP
+constexpr uint32_t OFF_BAR = OFF_ONES + 2 * EXT_BYTES;
 constexpr int B_RF = 0, B_RE = 2, B_CF = 4, B_CE = B_CF + STAGES, B_SF = B_CE + STAGES, B_XF = B_SF + STAGES, B_X2R = B_XF + 2, B_PF = B_X2R + 1,
               B_OF = B_PF + 2, B_OE = B_OF + 1, B_DONE = B_OE + 1, N_BARS = B_DONE + 1;
 constexpr uint32_t SMEM_TOTAL = OFF_BAR + N_BARS * 8 + 16 + 1024;
@@ -235,7 +245,23 @@ static_assert(SMEM_TOTAL <= 227 * 1024, "shared memory");
 // A worker writes dS and P over columns of S that it read itself, so workers need not
 // wait for one another.
 constexpr uint32_t TM_X1 = 0, TM_X2 = 256, TM_O = 384, TMEM_COLS = 512;
+constexpr uint32_t TILE_DESC = TILE_BYTES >> 4, PAIR_DESC = 2 * TILE_DESC;   // a tile, and two, as descriptors count
 constexpr float SCALE_LOG2 = 1.4426950408889634f / 8.0f;
+
+// Descriptor of the 16 further columns: K-major, no swizzle; the two 16-byte columns of
+// 8 rows are 128 bytes apart, 8 rows and the next 8 256.
+__device__ __forceinline__ uint64_t ext_desc(uint32_t saddr) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(128 >> 4) << 16 | (uint64_t)(256 >> 4) << 32 | (uint64_t)1 << 46;
+}
+__device__ __forceinline__ uint32_t ext_offset(int row) { return (row >> 3) * 256 + (row & 7) * 16; }
+// v as three bf16 whose sum is within 2^-24 of it.
+__device__ __forceinline__ void three_bf16(float v, bf16 (&o)[3]) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        o[i] = __float2bfloat16_rn(v);
+        v -= __bfloat162float(o[i]);
+    }
+}
 
 struct BwdParams {
     AttnPlan plan;
@@ -255,6 +281,19 @@ __device__ __forceinline__ int4 bwd_unit(const BwdParams& p, int i) {
     return it;
 }
 __device__ __forceinline__ int unit_tiles(const int4& it) { return (it.w - it.z + TILE - 1) / TILE; }
+
+// A whole warp's wait for what it has not found done; gives up as mbar_wait does.
+__device__ __noinline__ bool warp_wait_longer(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+    const long long t0 = clock64();
+    while (true) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        const bool late = clock64() - t0 > WAIT_CYCLES;
+        if (__any_sync(0xffffffffu, late || *abort_flag)) {
+            *abort_flag = 1;
+            return false;
+        }
+    }
+}
 
 // Column `first` .. of one row's gradients again, outside the tensor cores, by a whole
 // warp: of a row whose products met NaN or infinities of rows that it does not see.
@@ -283,14 +322,15 @@ __device__ __noinline__ void bwd_row_again(const BwdParams& p, int row, int head
         o1.x = fmaf(d, b1.x, o1.x), o1.y = fmaf(d, b1.y, o1.y);
         o2.x = fmaf(e, b2.x, o2.x), o2.y = fmaf(e, b2.y, o2.y);
     }
-    if (lane / 8 != chunk) return;
+    if (lane / 16 != chunk) return;
     bf16* dst = p.dqkv + row * stride + head * HD + 2 * lane;
     *reinterpret_cast<uint32_t*>(dst + (keys ? H : 0)) = pack_bf16x2(o1.x * 0.125f, o1.y * 0.125f);
     if (keys) *reinterpret_cast<uint32_t*>(dst + 2 * H) = pack_bf16x2(o2.x, o2.y);
 }
 
 __global__ void __launch_bounds__(NUM_THREADS, 1)
-    attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __grid_constant__ CUtensorMap tm_do, const BwdParams p) {
+    attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __grid_constant__ CUtensorMap tm_do,
+                    const __grid_constant__ BwdParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
@@ -303,8 +343,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     if (threadIdx.x == 0) {
         for (int b = 0; b < 2; ++b) {
             mbar_init(bar(B_RF + b), 1);
-            mbar_init(bar(B_RE + b), 1);
-            mbar_init(bar(B_XF + b), 1);
+            mbar_init(bar(B_RE + b), 2);          // S and dP of the unit's last tile
+            mbar_init(bar(B_XF + b), 2);          // S and dP
             mbar_init(bar(B_PF + b), WORKERS);
         }
         for (int s = 0; s < STAGES; ++s) {
@@ -315,11 +355,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         mbar_init(bar(B_X2R), WORKERS);
         mbar_init(bar(B_OF), 1);
         mbar_init(bar(B_OE), WORKERS);
-        mbar_init(bar(B_DONE), 1);
+        mbar_init(bar(B_DONE), 3);            // all issuers
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) tmem_alloc<1>(smem_u32(tmem_slot), TMEM_COLS);
+    // ones against -lse, ones against -delta, and the zero halves of the further columns
+    for (int i = threadIdx.x; i < (STAGES + 2) * TILE * 2; i += NUM_THREADS) {
+        const int tile = i / (TILE * 2), row = i / 2 % TILE;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (i % 2 == 0 && tile == STAGES) v = make_uint4(0x3f803f80u, 0x00003f80u, 0, 0);
+        if (i % 2 == 0 && tile == STAGES + 1) v = make_uint4(0, 0x3f800000u, 0x3f803f80u, 0);
+        *reinterpret_cast<uint4*>(smem + OFF_EXT + tile * EXT_BYTES + ext_offset(row) + i % 2 * 128) = v;
+    }
+    fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -328,156 +377,163 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     pdl_trigger();
 
     const int n_units = attn_units_of(*p.plan.n_items * 2 * p.n_heads, blockIdx.x, gridDim.x);
-    // a wait that gives up does so for the whole warp
-    auto all = [](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
+    // a whole warp's wait: true for all lanes, or false for all
+    auto warp_wait = [&](int b, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_try_wait(bar(b), parity)) || warp_wait_longer(bar(b), parity, abort_flag);
+    };
 
     if (warp == 0) {
-        // ---------------- TMA producer ----------------
-        if (lane == 0) {
-            uint32_t t = 0;
-            int ui = 0;
-            bool ok = true;
-            for (; ui < n_units && ok; ++ui) {
-                const int4 it = bwd_unit(p, ui);
-                const int head = it.y >> 16, nk = unit_tiles(it), rb = ui & 1;
-                const bool keys = it.y >> 8 & 1;
-                const int xq = head * HD, xk = p.hidden + head * HD, xv = 2 * p.hidden + head * HD;
-                if (!mbar_wait(bar(B_RE + rb), ((ui >> 1) & 1) ^ 1, abort_flag)) break;
+        // ---------------- producer: copies, and the further columns where columns are queries ----------------
+        uint32_t t = 0;
+        int ui = 0;
+        bool ok = true;
+        for (; ui < n_units && ok; ++ui) {
+            const int4 it = bwd_unit(p, ui);
+            const int head = it.y >> 16, nk = unit_tiles(it), rb = ui & 1;
+            const bool keys = it.y >> 8 & 1;
+            const int xq = head * HD, xk = p.hidden + head * HD, xv = 2 * p.hidden + head * HD;
+            if (!warp_wait(B_RE + rb, ((ui >> 1) & 1) ^ 1)) break;
+            if (elect_one()) {
                 mbar_expect_tx(bar(B_RF + rb), 2 * TILE_BYTES);
                 const uint32_t a = sbase + OFF_ROWS + rb * 2 * TILE_BYTES;
                 tma_load_2d(a, &tm_qkv, keys ? xk : xq, it.x, bar(B_RF + rb));
                 tma_load_2d(a + TILE_BYTES, keys ? &tm_qkv : &tm_do, keys ? xv : xq, it.x, bar(B_RF + rb));
-                for (int kt = 0; kt < nk; ++kt, ++t) {
-                    const int s = t % STAGES, y = it.z + kt * TILE;
-                    if (!mbar_wait(bar(B_CE + s), ((t / STAGES) & 1) ^ 1, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    mbar_expect_tx(bar(B_CF + s), 2 * TILE_BYTES);
-                    const uint32_t b = sbase + OFF_COLS + s * 2 * TILE_BYTES;
-                    tma_load_2d(b, &tm_qkv, keys ? xq : xk, y, bar(B_CF + s));
-                    tma_load_2d(b + TILE_BYTES, keys ? &tm_do : &tm_qkv, keys ? xq : xv, y, bar(B_CF + s));
-                }
             }
-            // no copy may still be landing in shared memory when the CTA exits
-            for (int b = 0; b < 2 && b < ui; ++b) {
-                const int u = (ui - 1 - b);
-                mbar_wait_drain(bar(B_RF + (u & 1)), (u >> 1) & 1);
-            }
-            for (uint32_t s = 0; s < STAGES && s < t; ++s) {
-                const uint32_t u = t - 1 - s;
-                mbar_wait_drain(bar(B_CF + u % STAGES), (u / STAGES) & 1);
-            }
-        }
-        __syncwarp();
-    } else if (warp == 2) {
-        // ---------------- statistics of the columns, where columns are queries ----------------
-        uint32_t t = 0;
-        bool ok = true;
-        for (int ui = 0; ui < n_units && ok; ++ui) {
-            const int4 it = bwd_unit(p, ui);
-            const int head = it.y >> 16, nk = unit_tiles(it);
-            const bool keys = it.y >> 8 & 1;
+            __syncwarp();
             for (int kt = 0; kt < nk; ++kt, ++t) {
-                const int s = t % STAGES;
+                const int s = t % STAGES, y = it.z + kt * TILE;
                 float v[2][4];
                 if (keys) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int row = it.z + kt * TILE + i * 32 + lane;
+                        const int row = y + i * 32 + lane;
                         const size_t at = (size_t)head * p.T + row;
                         v[0][i] = row < it.w ? p.plan.nlse2[at] : 0.f;
                         v[1][i] = row < it.w ? p.plan.ndelta[at] : 0.f;
                     }
                 }
-                if (!all(mbar_wait(bar(B_CE + s), ((t / STAGES) & 1) ^ 1, abort_flag))) {
+                if (!warp_wait(B_CE + s, ((t / STAGES) & 1) ^ 1)) {
                     ok = false;
                     break;
                 }
+                if (elect_one()) {
+                    mbar_expect_tx(bar(B_CF + s), 2 * TILE_BYTES);
+                    const uint32_t b = sbase + OFF_COLS + s * 2 * TILE_BYTES;
+                    tma_load_2d(b, &tm_qkv, keys ? xq : xk, y, bar(B_CF + s));
+                    tma_load_2d(b + TILE_BYTES, keys ? &tm_do : &tm_qkv, keys ? xq : xv, y, bar(B_CF + s));
+                }
+                __syncwarp();
                 if (keys) {
-                    float* stats = reinterpret_cast<float*>(smem + OFF_STATS) + s * 2 * TILE;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        stats[i * 32 + lane] = v[0][i];
-                        stats[TILE + i * 32 + lane] = v[1][i];
+                        // S + 8 (-lse), of which log2(e) / 8 is the exponent
+                        bf16 a[3], b[3];
+                        three_bf16(v[0][i] * (1.0f / SCALE_LOG2), a);
+                        three_bf16(v[1][i], b);
+                        const bf16 row[8] = {a[0], a[1], a[2], b[0], b[1], b[2], bf16(0.f), bf16(0.f)};
+                        uint4 q;
+                        memcpy(&q, row, 16);
+                        *reinterpret_cast<uint4*>(smem + OFF_EXT + s * EXT_BYTES + ext_offset(i * 32 + lane)) = q;
                     }
+                    fence_proxy_async_smem();
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(B_SF + s));
             }
         }
-    } else if (warp == 1) {
-        // ---------------- MMA issuer ----------------
-        if (lane == 0) {
-            constexpr uint32_t idesc_x = make_idesc(TILE, TILE), idesc_o = make_idesc(TILE, HD) | IDESC_B_MN_MAJOR;
-            struct Pend {
-                uint32_t t;
-                int ui;
-                bool any, first, last, keys;
-            };
-            Pend pend{};
-            // the outputs' products of a tile whose P and dS the workers have written
-            auto outputs = [&](const Pend& q) -> bool {
-                if (!q.any) return true;
-                if (!mbar_wait(bar(B_PF + (q.t & 1)), (q.t >> 1) & 1, abort_flag)) return false;
-                // the unit's first: the workers have read the one before
-                if (q.first && !mbar_wait(bar(B_OE), (q.ui & 1) ^ 1, abort_flag)) return false;
-                tc_fence_after();
-                const int st = q.t % STAGES;
-                const uint32_t x = tmem_base + TM_X1 + (q.t & 1) * TILE, b = sbase + OFF_COLS + st * 2 * TILE_BYTES;
-#pragma unroll
-                for (int k = 0; k < TILE / 16; ++k)
-                    mma_bf16_ts(tmem_base + TM_O, x + k * 16, sw128_desc_mn(b + k * 2048), idesc_o,
-                                !(q.first && k == 0));
-                if (q.keys) {
-#pragma unroll
-                    for (int k = 0; k < TILE / 16; ++k)
-                        mma_bf16_ts(tmem_base + TM_O + HD, x + k * 16 + 8,
-                                    sw128_desc_mn(b + TILE_BYTES + k * 2048), idesc_o, !(q.first && k == 0));
-                }
-                mma_commit(bar(B_CE + st));
-                if (q.last) mma_commit(bar(B_OF));
-                return true;
-            };
-            uint32_t t = 0;
-            bool ok = true;
-            for (int ui = 0; ui < n_units && ok; ++ui) {
-                const int4 it = bwd_unit(p, ui);
-                const int nk = unit_tiles(it), rb = ui & 1;
-                if (!mbar_wait(bar(B_RF + rb), (ui >> 1) & 1, abort_flag)) break;
-                const uint32_t a = sbase + OFF_ROWS + rb * 2 * TILE_BYTES;
-                const uint64_t a1 = sw128_desc(a), a2 = sw128_desc(a + TILE_BYTES);
-                for (int kt = 0; kt < nk; ++kt, ++t) {
-                    const int st = t % STAGES;
-                    ok = mbar_wait(bar(B_CF + st), (t / STAGES) & 1, abort_flag);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t b = sbase + OFF_COLS + st * 2 * TILE_BYTES;
-                    const uint64_t b1 = sw128_desc(b), b2 = sw128_desc(b + TILE_BYTES);
-                    // (the products of tile t - 2, which read this half of X1, were issued before)
-#pragma unroll
-                    for (int k = 0; k < HD / 16; ++k)
-                        mma_bf16(tmem_base + TM_X1 + (t & 1) * TILE, a1 + 2 * k, b1 + 2 * k, idesc_x, k != 0);
-                    ok = t == 0 || mbar_wait(bar(B_X2R), (t - 1) & 1, abort_flag);
-                    if (!ok) break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int k = 0; k < HD / 16; ++k) mma_bf16(tmem_base + TM_X2, a2 + 2 * k, b2 + 2 * k, idesc_x, k != 0);
-                    mma_commit(bar(B_XF + (t & 1)));
-                    if (kt == nk - 1) mma_commit(bar(B_RE + rb));
-                    ok = outputs(pend);
-                    if (!ok) break;
-                    pend = Pend{t, ui, true, kt == 0, kt == nk - 1, (it.y >> 8 & 1) != 0};
-                }
-            }
-            if (ok) outputs(pend);
-            // every MMA issued must be finished before TMEM is freed
-            mma_commit(bar(B_DONE));
-            mbar_wait_drain(bar(B_DONE), 0);
+        // no copy may still be landing in shared memory when the CTA exits
+        for (int b = 0; b < 2 && b < ui; ++b) {
+            const int u = (ui - 1 - b);
+            mbar_wait_drain(bar(B_RF + (u & 1)), (u >> 1) & 1);
         }
+        for (uint32_t s = 0; s < STAGES && s < t; ++s) {
+            const uint32_t u = t - 1 - s;
+            mbar_wait_drain(bar(B_CF + u % STAGES), (u / STAGES) & 1);
+        }
+    } else if (warp <= 2) {
+        // ---------------- issuers of S (warp 1) and of dP (warp 2): the whole warp, one lane issuing ----------------
+        // The tensor cores take a product when the one before is nearly done, so a warp that waits for the workers leaves
+        // them idle unless another has products to issue: S, dP and the outputs have a warp each.
+        constexpr uint32_t idesc = make_idesc(TILE, TILE);
+        const bool is_s = warp == 1;
+        const uint32_t op = is_s ? 0 : TILE_DESC;
+        const uint64_t rows0 = sw128_desc(sbase + OFF_ROWS) + op, cols0 = sw128_desc(sbase + OFF_COLS) + op;
+        const uint64_t ones = ext_desc(sbase + OFF_ONES + (is_s ? 0 : EXT_BYTES)), ext0 = ext_desc(sbase + OFF_EXT);
+        uint32_t t = 0;
+        bool ok = true;
+        for (int ui = 0; ui < n_units && ok; ++ui) {
+            const int4 it = bwd_unit(p, ui);
+            const int nk = unit_tiles(it), rb = ui & 1;
+            const bool keys = it.y >> 8 & 1;
+            if (!warp_wait(B_RF + rb, (ui >> 1) & 1)) break;
+            const uint64_t a = rows0 + rb * PAIR_DESC;
+            for (int kt = 0; kt < nk; ++kt, ++t) {
+                const uint32_t st = t % STAGES;
+                ok = warp_wait(B_CF + st, (t / STAGES) & 1);
+                if (ok && keys) ok = warp_wait(B_SF + st, (t / STAGES) & 1);
+                // S: the products of tile t - 2, which read this half of X1, are done; dP: the workers have read the tile before's
+                if (ok && is_s && t >= 2) ok = warp_wait(B_CE + (t - 2) % STAGES, ((t - 2) / STAGES) & 1);
+                if (ok && !is_s && t >= 1) ok = warp_wait(B_X2R, (t - 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t b = cols0 + st * PAIR_DESC, ext = ext0 + st * (EXT_BYTES >> 4);
+                const uint32_t x = tmem_base + (is_s ? TM_X1 + (t & 1) * TILE : TM_X2);
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < HD / 16; ++k) mma_bf16(x, a + 2 * k, b + 2 * k, idesc, k != 0);
+                    if (keys) mma_bf16(x, ones, ext, idesc, 1);
+                    mma_commit(bar(B_XF) + 8 * (t & 1));
+                    if (kt == nk - 1) mma_commit(bar(B_RE) + 8 * rb);
+                }
+                __syncwarp();
+            }
+        }
+        // every MMA issued must be finished before TMEM is freed
+        if (elect_one()) mma_commit(bar(B_DONE));
         __syncwarp();
+        mbar_wait_drain(bar(B_DONE), 0);
+    } else if (warp == 3) {
+        // ---------------- issuer of the outputs' products, of tiles whose P and dS the workers have written ----------------
+        constexpr uint32_t idesc = make_idesc(TILE, HD) | IDESC_B_MN_MAJOR;
+        const uint64_t cols0 = sw128_desc_mn(sbase + OFF_COLS);
+        uint32_t t = 0;
+        bool ok = true;
+        for (int ui = 0; ui < n_units && ok; ++ui) {
+            const int4 it = bwd_unit(p, ui);
+            const int nk = unit_tiles(it);
+            const bool keys = it.y >> 8 & 1;
+            for (int kt = 0; kt < nk; ++kt, ++t) {
+                const uint32_t st = t % STAGES;
+                ok = warp_wait(B_PF + (t & 1), (t >> 1) & 1);
+                // the unit's first: the workers have read the one before
+                if (ok && kt == 0) ok = warp_wait(B_OE, (ui & 1) ^ 1);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t x = tmem_base + TM_X1 + (t & 1) * TILE, o = tmem_base + TM_O;
+                const uint64_t b = cols0 + st * PAIR_DESC;
+                if (elect_one()) {
+                    if (keys) {
+#pragma unroll
+                        for (int k = 0; k < TILE / 16; ++k) mma_bf16_ts(o, x + k * 16, b + k * 128, idesc, (kt | k) != 0);
+#pragma unroll
+                        for (int k = 0; k < TILE / 16; ++k)
+                            mma_bf16_ts(o + HD, x + k * 16 + 8, b + TILE_DESC + k * 128, idesc, (kt | k) != 0);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < TILE / 16; ++k)
+                            mma_bf16_ts(o, x + (k >> 2) * 64 + (k & 3) * 8, b + k * 128, idesc, (kt | k) != 0);
+                    }
+                    mma_commit(bar(B_CE) + 8 * st);
+                    if (kt == nk - 1) mma_commit(bar(B_OF));
+                }
+                __syncwarp();
+            }
+        }
+        if (elect_one()) mma_commit(bar(B_DONE));
+        __syncwarp();
+        mbar_wait_drain(bar(B_DONE), 0);
     } else {
-        // ---------------- workers: thread = row, 32 columns of each tile ----------------
+        // ---------------- workers: thread = row, 64 columns of each tile ----------------
         const int quad = warp & 3, chunk = (warp - FIRST_WORKER) >> 2;
         const int r = quad * 32 + lane;
         const uint32_t lanes = tmem_base + ((uint32_t)(quad * 32) << 16);
@@ -485,41 +541,41 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         uint32_t t = 0;
         bool ok = true;
 
-        // the unit before's outputs, read once this unit's first tile is handed over
-        bool pending = false, keys_p = false;
-        int ui_p = 0, row_p = 0, head_p = 0, lo_p = 0, hi_p = 0;
-        auto finish = [&]() -> bool {
-            if (!all(mbar_wait(bar(B_OF), ui_p & 1, abort_flag))) return false;
+        // the columns that row r of a unit sees: its own text, and in window layers the window in it; whether the
+        // unit's rows all see the same columns, and those alone
+        auto seen = [&](const int4& it, int& lo, int& hi) -> bool {
+            lo = hi = 0;
+            if (r >= (it.y & 0xff)) return true;
+            const int row = it.x + r;
+            const int2 tb = p.plan.row_tb[row];
+            lo = max(tb.x, it.z), hi = min(tb.y, it.w);
+            if (p.window >= 0) lo = max(lo, row - p.window), hi = min(hi, row + p.window + 1);
+            return p.window < 0 && tb.x == it.z && tb.y == it.w;
+        };
+        // a unit's outputs, read once the next one's first tile is handed over
+        auto finish = [&](int ui_p) -> bool {
+            const int4 it_p = bwd_unit(p, ui_p);
+            const int row_p = r < (it_p.y & 0xff) ? it_p.x + r : -1, head_p = it_p.y >> 16;
+            const bool keys_p = it_p.y >> 8 & 1;
+            int lo_p, hi_p;
+            const bool alone = seen(it_p, lo_p, hi_p);
+            if (!warp_wait(B_OF, ui_p & 1)) return false;
             tc_fence_after();
-            float o1[16], o2[16];
-            tmem_ld16_issue(lanes + TM_O + chunk * 16, o1);
-            if (keys_p) tmem_ld16_issue(lanes + TM_O + HD + chunk * 16, o2);
-            tmem_wait_ld();
-            tmem_tie16(o1);
-            if (keys_p) tmem_tie16(o2);
+            float z = 0.f;   // not a number where one of the sums is not finite
+            bf16* const dst = p.dqkv + (size_t)max(row_p, 0) * 3 * p.hidden + head_p * HD + chunk * 32;
+#pragma unroll 1
+            for (int i = 0; i < (keys_p ? 2 : 1); ++i) {   // dq, or dk and dv
+                float o[32];
+                tmem_ld32(lanes + TM_O + i * HD + chunk * 32, o);
+                const float scale = i ? 1.f : 0.125f;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] *= scale, z = fmaf(o[j], 0.f, z);
+                if (row_p >= 0) store_bf16x32(dst + (keys_p ? (i + 1) * p.hidden : 0), o);
+            }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(B_OE));
-            float z = 0.f;   // not a number where one of the sums is not finite
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o1[i] *= 0.125f, z = fmaf(o1[i], 0.f, z);
-            if (keys_p) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) z = fmaf(o2[i], 0.f, z);
-            }
-            auto store = [&](bf16* dst, const float (&v)[16]) {
-                float a[8], b[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) a[i] = v[i], b[i] = v[8 + i];
-                store_vec(dst, a);
-                store_vec(dst + 8, b);
-            };
-            if (row_p >= 0) {
-                bf16* dst = p.dqkv + (size_t)row_p * 3 * p.hidden + head_p * HD + chunk * 16;
-                store(dst + (keys_p ? p.hidden : 0), o1);
-                if (keys_p) store(dst + 2 * p.hidden, o2);
-            }
-            unsigned again = __ballot_sync(0xffffffffu, row_p >= 0 && lo_p < hi_p && !(z == 0.f));
+            unsigned again = __ballot_sync(0xffffffffu, row_p >= 0 && !alone && !(z == 0.f));
             while (again) {
                 const int l = __ffs(again) - 1;
                 again &= again - 1;
@@ -527,134 +583,112 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                               __shfl_sync(0xffffffffu, hi_p, l), chunk);
             }
             __syncwarp();
-            pending = false;
             return true;
         };
 
-        for (int ui = 0; ui < n_units && ok; ++ui) {
-            const int4 it = bwd_unit(p, ui);
+        for (int ui = 0; ui <= n_units && ok; ++ui) {
+            const int4 it = ui < n_units ? bwd_unit(p, ui) : make_int4(0, 0, 0, 0);
             const int head = it.y >> 16, q_len = it.y & 0xff, k_lo = it.z, k_hi = it.w, nk = unit_tiles(it);
             const bool keys = it.y >> 8 & 1;
-            const int row = it.x + r;
-            // the columns that this row sees: its own text, and in window layers the window in it
-            int vis_lo = 0, vis_hi = 0;
-            bool alone = false;
+            int vis_lo, vis_hi;
+            seen(it, vis_lo, vis_hi);
             float nl = 0.f, nd = 0.f;
-            if (r < q_len) {
-                const int2 tb = p.plan.row_tb[row];
-                vis_lo = max(tb.x, k_lo), vis_hi = min(tb.y, k_hi);
-                if (p.window >= 0) vis_lo = max(vis_lo, row - p.window), vis_hi = min(vis_hi, row + p.window + 1);
-                alone = p.window < 0 && tb.x == k_lo && tb.y == k_hi;
-                if (!keys) nl = p.plan.nlse2[(size_t)head * p.T + row], nd = p.plan.ndelta[(size_t)head * p.T + row];
+            if (!keys && r < q_len) {
+                const size_t at = (size_t)head * p.T + it.x + r;
+                nl = p.plan.nlse2[at], nd = p.plan.ndelta[at];
             }
             const uint64_t nl2 = f2_pack(nl, nl), nd2 = f2_pack(nd, nd);
-            for (int kt = 0; kt < nk; ++kt, ++t) {
-                const int b = t & 1, st = t % STAGES;
-                const int c0 = k_lo + kt * TILE + chunk * 32, lo = vis_lo - c0, hi = vis_hi - c0;
-                const bool any = __any_sync(0xffffffffu, lo < hi && lo < 32 && hi > 0);
-                const bool whole = __all_sync(0xffffffffu, lo <= 0 && hi >= 32);
-                if (!all(mbar_wait(bar(B_XF + b), (t >> 1) & 1, abort_flag))) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t xt = lanes + TM_X1 + b * TILE + chunk * 32;
-                if (!any) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(B_X2R));
-                    uint32_t zero[16] = {};
-                    tmem_st16_u(xt, zero);
-                    tmem_st16_u(xt + 16, zero);
-                } else {
-                    // 16 columns at a time: dS as bf16 pairs over the first 8 columns of their S, P over the others
-                    float x1[16], x2[2][16];
-                    tmem_ld16_issue(lanes + TM_X2 + chunk * 32, x2[0]);
-                    tmem_ld16_issue(lanes + TM_X2 + chunk * 32 + 16, x2[1]);
-                    tmem_ld16_issue(xt, x1);
-                    tmem_wait_ld();
-                    tmem_tie16(x2[0]);
-                    tmem_tie16(x2[1]);
-                    tmem_tie16(x1);
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(B_X2R));
-                    if (keys && !all(mbar_wait(bar(B_SF + st), (t / STAGES) & 1, abort_flag))) {
-                        ok = false;
-                        break;
-                    }
-                    const float* stats = reinterpret_cast<const float*>(smem + OFF_STATS) + st * 2 * TILE + chunk * 32;
-                    auto columns = [&](auto by_key, auto masked, int c, const float (&x2)[16]) {
-                        uint32_t pk[16];
+            // (a loop for each kind: one with both kinds' steps in branches takes 239 registers)
+            auto tiles = [&](auto by_key, int kt, int end) {
+                constexpr bool KEYS = decltype(by_key)::value;
+                for (; kt < end; ++kt, ++t) {
+                    const int b = t & 1, st = t % STAGES;
+                    const int c0 = k_lo + kt * TILE + chunk * 64, lo = vis_lo - c0, hi = vis_hi - c0;
+                    const bool any = __any_sync(0xffffffffu, lo < hi && lo < 64 && hi > 0);
+                    const bool whole = __all_sync(0xffffffffu, lo <= 0 && hi >= 64);
+                    if (!warp_wait(B_XF + b, (t >> 1) & 1)) return false;
+                    tc_fence_after();
+                    const uint32_t xt = lanes + TM_X1 + b * TILE + chunk * 64;
+                    if (!any) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(B_X2R));
+                        uint32_t zero[32] = {};
+                        tmem_st32_u(xt, zero);
+                        if (KEYS) tmem_st32_u(xt + 32, zero);
+                    } else {
+                        float x1[32], x2[64];
+                        tmem_ld64_issue(lanes + TM_X2 + chunk * 64, x2);
+                        tmem_ld32_issue(xt, x1);
+                        tmem_wait_ld();
+                        tmem_tie64(x2);
+                        tmem_tie32(x1);
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(B_X2R));
+                        // 32 columns at a time: the operands of the outputs' products, as bf16 pairs over columns of S that
+                        // this warp has read: dS and P in turn, 16 columns (8 words) of each; where rows are queries dS alone
 #pragma unroll
-                        for (int i = 0; i < 16; i += 4) {
-                            uint64_t l2[2] = {nl2, nl2}, d2[2] = {nd2, nd2};
-                            if constexpr (decltype(by_key)::value) {
-                                const float4 a = *reinterpret_cast<const float4*>(stats + c + i);
-                                const float4 d = *reinterpret_cast<const float4*>(stats + TILE + c + i);
-                                l2[0] = f2_pack(a.x, a.y), l2[1] = f2_pack(a.z, a.w);
-                                d2[0] = f2_pack(d.x, d.y), d2[1] = f2_pack(d.z, d.w);
-                            }
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t pk[KEYS ? 32 : 16];
 #pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                const int k = i + 2 * j;
+                            for (int j = 0; j < 16; ++j) {
+                                const int k = 32 * h + 2 * j;
+                                const uint64_t s2 = f2_pack(x1[2 * j], x1[2 * j + 1]);
+                                uint64_t d2 = f2_pack(x2[k], x2[k + 1]);
                                 float e0, e1, s0, s1;
-                                f2_unpack(f2_fma(f2_pack(x1[k], x1[k + 1]), sl2, l2[j]), e0, e1);
+                                f2_unpack(KEYS ? f2_mul(s2, sl2) : f2_fma(s2, sl2, nl2), e0, e1);
+                                if (!KEYS) d2 = f2_add(d2, nd2);
                                 e0 = ex2_approx(e0);
                                 e1 = ex2_approx(e1);
-                                f2_unpack(f2_mul(f2_pack(e0, e1), f2_add(f2_pack(x2[k], x2[k + 1]), d2[j])), s0, s1);
-                                if constexpr (decltype(masked)::value) {
-                                    const bool v0 = c + k >= lo && c + k < hi, v1 = c + k + 1 >= lo && c + k + 1 < hi;
-                                    e0 = v0 ? e0 : 0.f, s0 = v0 ? s0 : 0.f;
-                                    e1 = v1 ? e1 : 0.f, s1 = v1 ? s1 : 0.f;
-                                }
-                                pk[k / 2] = pack_bf16(s0, s1);
-                                pk[8 + k / 2] = pack_bf16(e0, e1);
+                                f2_unpack(f2_mul(f2_pack(e0, e1), d2), s0, s1);
+                                pk[KEYS ? (j >> 3) * 16 + (j & 7) : j] = pack_bf16(s0, s1);
+                                if (KEYS) pk[(j >> 3) * 16 + 8 + (j & 7)] = pack_bf16(e0, e1);
                             }
+                            if (!whole) {   // columns that the row does not see, bit by bit: they may be NaN
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) {
+                                    const int k = 32 * h + 2 * j;
+                                    const uint32_t m = (k >= lo && k < hi ? 0xffffu : 0u) | (k + 1 >= lo && k + 1 < hi ? 0xffff0000u : 0u);
+                                    pk[KEYS ? (j >> 3) * 16 + (j & 7) : j] &= m;
+                                    if (KEYS) pk[(j >> 3) * 16 + 8 + (j & 7)] &= m;
+                                }
+                            }
+                            if (h == 0) {   // the other half of S, before anything is written over it
+                                tmem_ld32_issue(xt + 32, x1);
+                                tmem_wait_ld();
+                                tmem_tie32(x1);
+                            }
+                            if constexpr (KEYS) tmem_st32_issue(xt + 32 * h, pk);
+                            else tmem_st16_issue(xt + 16 * h, pk);
                         }
-                        tmem_st16_u(xt + c, pk);
-                    };
-                    constexpr std::true_type yes{};
-                    constexpr std::false_type no{};
-                    auto both = [&](auto by_key, auto masked) {
-                        columns(by_key, masked, 0, x2[0]);
-                        tmem_ld16_issue(xt + 16, x1);
-                        tmem_wait_ld();
-                        tmem_tie16(x1);
-                        columns(by_key, masked, 16, x2[1]);
-                    };
-                    if (keys) whole ? both(yes, no) : both(yes, yes);
-                    else whole ? both(no, no) : both(no, yes);
-                }
-                // rows behind the last column's text (dS and P there are 0, and they may hold anything)
-                const int cols = k_hi - (k_lo + kt * TILE);
-                if (cols < TILE && k_hi < p.T) {
-                    // (the copy's barrier has completed; waiting on it makes the tiles visible)
-                    if (!all(mbar_wait(bar(B_CF + st), (t / STAGES) & 1, abort_flag))) {
-                        ok = false;
-                        break;
+                        tmem_wait_st();
                     }
-                    uint4* v16 = reinterpret_cast<uint4*>(smem + OFF_COLS + st * 2 * TILE_BYTES);
-                    for (int c = cols * 8 + (int)threadIdx.x - 32 * FIRST_WORKER; c < TILE * 8; c += 32 * WORKERS) {
-                        v16[c] = make_uint4(0, 0, 0, 0);
-                        v16[TILE * 8 + c] = make_uint4(0, 0, 0, 0);
+                    // rows behind the last column's text (dS and P there are 0, and they may hold anything)
+                    const int cols = k_hi - (k_lo + kt * TILE);
+                    if (cols < TILE && k_hi < p.T) {
+                        // (the copy's barrier has completed; waiting on it makes the tiles visible)
+                        if (!warp_wait(B_CF + st, (t / STAGES) & 1)) return false;
+                        uint4* v16 = reinterpret_cast<uint4*>(smem + OFF_COLS + st * 2 * TILE_BYTES);
+                        for (int c = cols * 8 + (int)threadIdx.x - 32 * FIRST_WORKER; c < TILE * 8; c += 32 * WORKERS) {
+                            v16[c] = make_uint4(0, 0, 0, 0);
+                            v16[TILE * 8 + c] = make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async_smem();
                     }
-                    fence_proxy_async_smem();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(B_PF + b));
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(B_PF + b));
-                if (kt == 0 && pending && !finish()) {
-                    ok = false;
-                    break;
-                }
+                return true;
+            };
+            // its first tile, the outputs of the unit before, the other tiles (the unit behind the last has none)
+            for (int part = 0; part < 2 && ok; ++part) {
+                const int from = part ? 1 : 0, to = part ? nk : min(nk, 1);
+                ok = keys ? tiles(std::true_type{}, from, to) : tiles(std::false_type{}, from, to);
+                if (ok && part == 0 && ui > 0) ok = finish(ui - 1);
             }
-            if (!ok) break;
-            pending = true;
-            ui_p = ui, keys_p = keys, head_p = head;
-            row_p = r < q_len ? row : -1;
-            lo_p = alone ? 0 : vis_lo, hi_p = alone ? 0 : vis_hi;
         }
-        if (ok && pending) finish();
     }
 
     tc_fence_before();
