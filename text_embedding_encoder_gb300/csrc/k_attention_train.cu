@@ -15,6 +15,7 @@
 #include "gemm_tc.cuh"
 #include "train_internal.cuh"
 
+#include <limits.h>
 #include <string.h>
 
 #include <algorithm>
@@ -74,8 +75,9 @@ __global__ void __launch_bounds__(PLAN_THREADS) attn_plan_kernel(const PlanArgs 
     __shared__ int bucket[PLAN_BUCKETS + 1];
     __shared__ int bad;
     __shared__ float stage[PLAN_HEADS][PLAN_ROWS + 1];
+    // No early trigger: the attention kernel's blocks, one to an SM, would take the SMs from the
+    // blocks that are still to come (window layer of 32768 tokens, backward: 200 us instead of 152).
     pdl_wait();
-    pdl_trigger();
     const int n = a.n_texts, tid = threadIdx.x;
     if (blockIdx.x > 0) {
         const int row0 = (blockIdx.x - 1) * PLAN_ROWS;
@@ -280,6 +282,21 @@ __device__ __forceinline__ int4 bwd_unit(const BwdParams& p, int i) {
     it.y |= ((k & 1) ^ 1) << 8 | head << 16;
     return it;
 }
+// A CTA's units in turn, each read while the one before is worked on.
+struct UnitStream {
+    const BwdParams& p;
+    int n, i = 0;
+    int4 ahead;
+    __device__ __forceinline__ UnitStream(const BwdParams& p_, int n_) : p(p_), n(n_), ahead(make_int4(0, 0, 0, 0)) {
+        if (n > 0) ahead = bwd_unit(p, 0);
+    }
+    __device__ __forceinline__ int4 next() {
+        const int4 it = ahead;
+        ++i;
+        ahead = i < n ? bwd_unit(p, i) : make_int4(0, 0, 0, 0);
+        return it;
+    }
+};
 __device__ __forceinline__ int unit_tiles(const int4& it) { return (it.w - it.z + TILE - 1) / TILE; }
 
 // A whole warp's wait for what it has not found done; gives up as mbar_wait does.
@@ -387,8 +404,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         uint32_t t = 0;
         int ui = 0;
         bool ok = true;
+        UnitStream units(p, n_units);
+        float v[2][4];   // of the tile to come
+        auto statistics = [&](const int4& it, int kt) {
+            if (!(it.y >> 8 & 1)) return;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = it.z + kt * TILE + i * 32 + lane;
+                const size_t at = (size_t)(it.y >> 16) * p.T + row;
+                v[0][i] = row < it.w ? p.plan.nlse2[at] : 0.f;
+                v[1][i] = row < it.w ? p.plan.ndelta[at] : 0.f;
+            }
+        };
+        if (n_units > 0) statistics(units.ahead, 0);
         for (; ui < n_units && ok; ++ui) {
-            const int4 it = bwd_unit(p, ui);
+            const int4 it = units.next();
             const int head = it.y >> 16, nk = unit_tiles(it), rb = ui & 1;
             const bool keys = it.y >> 8 & 1;
             const int xq = head * HD, xk = p.hidden + head * HD, xv = 2 * p.hidden + head * HD;
@@ -402,16 +432,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             __syncwarp();
             for (int kt = 0; kt < nk; ++kt, ++t) {
                 const int s = t % STAGES, y = it.z + kt * TILE;
-                float v[2][4];
-                if (keys) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int row = y + i * 32 + lane;
-                        const size_t at = (size_t)head * p.T + row;
-                        v[0][i] = row < it.w ? p.plan.nlse2[at] : 0.f;
-                        v[1][i] = row < it.w ? p.plan.ndelta[at] : 0.f;
-                    }
-                }
                 if (!warp_wait(B_CE + s, ((t / STAGES) & 1) ^ 1)) {
                     ok = false;
                     break;
@@ -439,6 +459,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(B_SF + s));
+                if (kt + 1 < nk) statistics(it, kt + 1);
+                else statistics(units.ahead, 0);
             }
         }
         // no copy may still be landing in shared memory when the CTA exits
@@ -461,8 +483,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const uint64_t ones = ext_desc(sbase + OFF_ONES + (is_s ? 0 : EXT_BYTES)), ext0 = ext_desc(sbase + OFF_EXT);
         uint32_t t = 0;
         bool ok = true;
+        UnitStream units(p, n_units);
         for (int ui = 0; ui < n_units && ok; ++ui) {
-            const int4 it = bwd_unit(p, ui);
+            const int4 it = units.next();
             const int nk = unit_tiles(it), rb = ui & 1;
             const bool keys = it.y >> 8 & 1;
             if (!warp_wait(B_RF + rb, (ui >> 1) & 1)) break;
@@ -498,8 +521,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const uint64_t cols0 = sw128_desc_mn(sbase + OFF_COLS);
         uint32_t t = 0;
         bool ok = true;
+        UnitStream units(p, n_units);
         for (int ui = 0; ui < n_units && ok; ++ui) {
-            const int4 it = bwd_unit(p, ui);
+            const int4 it = units.next();
             const int nk = unit_tiles(it);
             const bool keys = it.y >> 8 & 1;
             for (int kt = 0; kt < nk; ++kt, ++t) {
@@ -541,24 +565,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         uint32_t t = 0;
         bool ok = true;
 
-        // the columns that row r of a unit sees: its own text, and in window layers the window in it; whether the
-        // unit's rows all see the same columns, and those alone
-        auto seen = [&](const int4& it, int& lo, int& hi) -> bool {
-            lo = hi = 0;
-            if (r >= (it.y & 0xff)) return true;
+        // the text of row r of a unit, {0, 0} behind its rows
+        auto text_of = [&](const int4& it) -> int2 { return r < (it.y & 0xff) ? p.plan.row_tb[it.x + r] : make_int2(0, 0); };
+        // the columns that the row sees: its own text, and in window layers the window in it
+        auto seen = [&](const int4& it, const int2& tb, int& lo, int& hi) {
             const int row = it.x + r;
-            const int2 tb = p.plan.row_tb[row];
             lo = max(tb.x, it.z), hi = min(tb.y, it.w);
             if (p.window >= 0) lo = max(lo, row - p.window), hi = min(hi, row + p.window + 1);
-            return p.window < 0 && tb.x == it.z && tb.y == it.w;
         };
         // a unit's outputs, read once the next one's first tile is handed over
-        auto finish = [&](int ui_p) -> bool {
-            const int4 it_p = bwd_unit(p, ui_p);
+        auto finish = [&](int ui_p, const int4& it_p, const int2& tb_p) -> bool {
             const int row_p = r < (it_p.y & 0xff) ? it_p.x + r : -1, head_p = it_p.y >> 16;
             const bool keys_p = it_p.y >> 8 & 1;
-            int lo_p, hi_p;
-            const bool alone = seen(it_p, lo_p, hi_p);
+            // rows of one text that all see the same columns meet no others' values
+            const bool alone = p.window < 0 && tb_p.x == it_p.z && tb_p.y == it_p.w;
             if (!warp_wait(B_OF, ui_p & 1)) return false;
             tc_fence_after();
             float z = 0.f;   // not a number where one of the sums is not finite
@@ -576,6 +596,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(B_OE));
             unsigned again = __ballot_sync(0xffffffffu, row_p >= 0 && !alone && !(z == 0.f));
+            int lo_p, hi_p;
+            seen(it_p, tb_p, lo_p, hi_p);
             while (again) {
                 const int l = __ffs(again) - 1;
                 again &= again - 1;
@@ -586,30 +608,46 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             return true;
         };
 
+        // a unit's rows' texts and statistics are read while the unit before is worked on
+        UnitStream units(p, n_units);
+        int4 it = make_int4(0, 0, 0, 0), it_next = units.next();
+        int2 tb = make_int2(0, 0), tb_next = text_of(it_next);
+        float nl_next = 0.f, nd_next = 0.f;
+        auto statistics = [&]() {
+            if ((it_next.y >> 8 & 1) || r >= (it_next.y & 0xff)) return;
+            const size_t at = (size_t)(it_next.y >> 16) * p.T + it_next.x + r;
+            nl_next = p.plan.nlse2[at], nd_next = p.plan.ndelta[at];
+        };
+        statistics();
         for (int ui = 0; ui <= n_units && ok; ++ui) {
-            const int4 it = ui < n_units ? bwd_unit(p, ui) : make_int4(0, 0, 0, 0);
-            const int head = it.y >> 16, q_len = it.y & 0xff, k_lo = it.z, k_hi = it.w, nk = unit_tiles(it);
+            const int4 it_p = it;
+            const int2 tb_p = tb;
+            it = it_next, tb = tb_next;
+            const float nl = nl_next, nd = nd_next;
+            it_next = units.next();
+            tb_next = text_of(it_next);
+            statistics();
+            const int q_len = it.y & 0xff, k_lo = it.z, k_hi = it.w, nk = unit_tiles(it);
             const bool keys = it.y >> 8 & 1;
             int vis_lo, vis_hi;
-            seen(it, vis_lo, vis_hi);
-            float nl = 0.f, nd = 0.f;
-            if (!keys && r < q_len) {
-                const size_t at = (size_t)head * p.T + it.x + r;
-                nl = p.plan.nlse2[at], nd = p.plan.ndelta[at];
-            }
+            seen(it, tb, vis_lo, vis_hi);
             const uint64_t nl2 = f2_pack(nl, nl), nd2 = f2_pack(nd, nd);
+            // columns that any row of the warp sees, and that all see.  A row behind the item's sees them all: what it adds
+            // up is not stored, and what it multiplies is 0 behind the last column
+            if (r >= q_len) vis_lo = INT_MIN / 2, vis_hi = INT_MAX / 2;
+            const int any_lo = __reduce_min_sync(0xffffffffu, r < q_len ? vis_lo : INT_MAX);
+            const int any_hi = __reduce_max_sync(0xffffffffu, r < q_len ? vis_hi : INT_MIN);
+            const int all_lo = __reduce_max_sync(0xffffffffu, vis_lo), all_hi = __reduce_min_sync(0xffffffffu, vis_hi);
             // (a loop for each kind: one with both kinds' steps in branches takes 239 registers)
             auto tiles = [&](auto by_key, int kt, int end) {
                 constexpr bool KEYS = decltype(by_key)::value;
                 for (; kt < end; ++kt, ++t) {
                     const int b = t & 1, st = t % STAGES;
-                    const int c0 = k_lo + kt * TILE + chunk * 64, lo = vis_lo - c0, hi = vis_hi - c0;
-                    const bool any = __any_sync(0xffffffffu, lo < hi && lo < 64 && hi > 0);
-                    const bool whole = __all_sync(0xffffffffu, lo <= 0 && hi >= 64);
+                    const int c0 = k_lo + kt * TILE + chunk * 64;
                     if (!warp_wait(B_XF + b, (t >> 1) & 1)) return false;
                     tc_fence_after();
                     const uint32_t xt = lanes + TM_X1 + b * TILE + chunk * 64;
-                    if (!any) {
+                    if (c0 >= any_hi || c0 + 64 <= any_lo) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(B_X2R));
@@ -617,47 +655,52 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         tmem_st32_u(xt, zero);
                         if (KEYS) tmem_st32_u(xt + 32, zero);
                     } else {
-                        float x1[32], x2[64];
-                        tmem_ld64_issue(lanes + TM_X2 + chunk * 64, x2);
-                        tmem_ld32_issue(xt, x1);
-                        tmem_wait_ld();
-                        tmem_tie64(x2);
-                        tmem_tie32(x1);
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar(B_X2R));
                         // 32 columns at a time: the operands of the outputs' products, as bf16 pairs over columns of S that
                         // this warp has read: dS and P in turn, 16 columns (8 words) of each; where rows are queries dS alone
-#pragma unroll
+                        constexpr int WORDS = KEYS ? 32 : 16;
+                        auto word = [](int j) { return KEYS ? (j >> 3) * 16 + (j & 7) : j; };
+#pragma unroll 1
                         for (int h = 0; h < 2; ++h) {
-                            uint32_t pk[KEYS ? 32 : 16];
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                const int k = 32 * h + 2 * j;
-                                const uint64_t s2 = f2_pack(x1[2 * j], x1[2 * j + 1]);
-                                uint64_t d2 = f2_pack(x2[k], x2[k + 1]);
-                                float e0, e1, s0, s1;
-                                f2_unpack(KEYS ? f2_mul(s2, sl2) : f2_fma(s2, sl2, nl2), e0, e1);
-                                if (!KEYS) d2 = f2_add(d2, nd2);
-                                e0 = ex2_approx(e0);
-                                e1 = ex2_approx(e1);
-                                f2_unpack(f2_mul(f2_pack(e0, e1), d2), s0, s1);
-                                pk[KEYS ? (j >> 3) * 16 + (j & 7) : j] = pack_bf16(s0, s1);
-                                if (KEYS) pk[(j >> 3) * 16 + 8 + (j & 7)] = pack_bf16(e0, e1);
+                            uint32_t pk[WORDS];
+                            const int c = c0 + 32 * h;
+                            float x1[32], x2[32];
+                            tmem_ld32_issue(lanes + TM_X2 + chunk * 64 + 32 * h, x2);
+                            tmem_ld32_issue(xt + 32 * h, x1);
+                            tmem_wait_ld();
+                            tmem_tie32(x2);
+                            tmem_tie32(x1);
+                            if (h == 1) {
+                                tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(bar(B_X2R));
                             }
-                            if (!whole) {   // columns that the row does not see, bit by bit: they may be NaN
+                            if (c >= any_hi || c + 32 <= any_lo) {   // no row of the warp sees any of them
+#pragma unroll
+                                for (int j = 0; j < WORDS; ++j) pk[j] = 0u;
+                            } else {
 #pragma unroll
                                 for (int j = 0; j < 16; ++j) {
-                                    const int k = 32 * h + 2 * j;
-                                    const uint32_t m = (k >= lo && k < hi ? 0xffffu : 0u) | (k + 1 >= lo && k + 1 < hi ? 0xffff0000u : 0u);
-                                    pk[KEYS ? (j >> 3) * 16 + (j & 7) : j] &= m;
-                                    if (KEYS) pk[(j >> 3) * 16 + 8 + (j & 7)] &= m;
+                                    const uint64_t s2 = f2_pack(x1[2 * j], x1[2 * j + 1]);
+                                    uint64_t d2 = f2_pack(x2[2 * j], x2[2 * j + 1]);
+                                    float e0, e1, s0, s1;
+                                    f2_unpack(KEYS ? f2_mul(s2, sl2) : f2_fma(s2, sl2, nl2), e0, e1);
+                                    if (!KEYS) d2 = f2_add(d2, nd2);
+                                    e0 = ex2_approx(e0);
+                                    e1 = ex2_approx(e1);
+                                    f2_unpack(f2_mul(f2_pack(e0, e1), d2), s0, s1);
+                                    pk[word(j)] = pack_bf16(s0, s1);
+                                    if (KEYS) pk[word(j) + 8] = pack_bf16(e0, e1);
                                 }
-                            }
-                            if (h == 0) {   // the other half of S, before anything is written over it
-                                tmem_ld32_issue(xt + 32, x1);
-                                tmem_wait_ld();
-                                tmem_tie32(x1);
+                                if (c < all_lo || c + 32 > all_hi) {   // columns that the row does not see, bit by bit: they may be NaN
+                                    const uint32_t from = (uint32_t)(vis_lo - c), many = (uint32_t)(vis_hi - vis_lo);
+#pragma unroll
+                                    for (int j = 0; j < 16; ++j) {
+                                        const uint32_t m = ((uint32_t)(2 * j) - from < many ? 0xffffu : 0u) |
+                                                           ((uint32_t)(2 * j + 1) - from < many ? 0xffff0000u : 0u);
+                                        pk[word(j)] &= m;
+                                        if (KEYS) pk[word(j) + 8] &= m;
+                                    }
+                                }
                             }
                             if constexpr (KEYS) tmem_st32_issue(xt + 32 * h, pk);
                             else tmem_st16_issue(xt + 16 * h, pk);
@@ -686,7 +729,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             for (int part = 0; part < 2 && ok; ++part) {
                 const int from = part ? 1 : 0, to = part ? nk : min(nk, 1);
                 ok = keys ? tiles(std::true_type{}, from, to) : tiles(std::false_type{}, from, to);
-                if (ok && part == 0 && ui > 0) ok = finish(ui - 1);
+                if (ok && part == 0 && ui > 0) ok = finish(ui - 1, it_p, tb_p);
             }
         }
     }
