@@ -171,7 +171,7 @@ def _ptr(a) -> int:
     if isinstance(a, np.ndarray):
         if not a.flags.c_contiguous:
             raise ValueError("array must be C-contiguous")
-        return a.ctypes.data
+        return a.__array_interface__["data"][0]
     raise TypeError(type(a))
 
 

@@ -35,12 +35,19 @@ constexpr int NUM_THREADS = 64 + 32 * EPI_WARPS;
 constexpr int MAX_PAIRS = 128;
 constexpr uint32_t HALF_BYTES = 128 * BK * 2;
 constexpr uint32_t STAGE_BYTES = 2 * HALF_BYTES;
-constexpr int STAGES = 6;
-constexpr uint32_t OUT_OFF = STAGES * STAGE_BYTES;     // a 4 KB staging box per epilogue warp
-constexpr uint32_t BAR_OFF = OUT_OFF + EPI_WARPS * 4096;
-constexpr int N_BARS = 2 * STAGES + 5;
-constexpr uint32_t SMEM_BYTES = BAR_OFF + N_BARS * 8 + 16 + 1024;
-static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
+// Stages of operands, and 4 KB boxes of each epilogue warp: one for stores, backward
+// another that dz comes in.  (Read by the threads from their rows instead, dz comes 2.7
+// times out of DRAM: 16 bytes of a sector each, and hardly any L1 beside this much shared
+// memory.)
+template <bool BWD>
+struct Smem {
+    static constexpr int STAGES = BWD ? 5 : 6, BOXES = BWD ? 2 : 1;
+    static constexpr uint32_t OUT_OFF = STAGES * STAGE_BYTES;
+    static constexpr uint32_t BAR_OFF = OUT_OFF + EPI_WARPS * BOXES * 4096;
+    static constexpr int N_BARS = 2 * STAGES + 5 + EPI_WARPS;
+    static constexpr uint32_t BYTES = BAR_OFF + N_BARS * 8 + 16 + 1024;
+};
+static_assert(Smem<true>::BYTES <= 227 * 1024 && Smem<false>::BYTES <= 227 * 1024, "shared memory");
 constexpr uint32_t TMEM_COLS = 512;    // two accumulators of 256 columns
 constexpr int EPILOGUE_K_STEPS = 8;    // a tile's epilogue, in K steps of products
 // Slices of a sum: tiles that are too few for all CTA pairs are split along K, into so
@@ -55,19 +62,21 @@ struct Maps {
     CUtensorMap du;                     // dU of the part being multiplied, K-major
     CUtensorMap wi_mn, du_mn, x_mn;     // MN-major operands: boxes of 64 columns x 64 rows
     CUtensorMap z;                      // z, or da of the part being made (backward): boxes of 32 rows x 64 columns
+    CUtensorMap dz;                     // boxes of 32 rows x 64 columns
     CUtensorMap dg, dx, dw;             // outputs (dx and dw: bf16, or the slices' fp32 sums in boxes of 32 columns)
 };
 
-// A CTA pair's share of a launch: of each kind the units [first, first + n).
+// The CTA pairs' shares of a launch: of each kind so many units.  A pair's r-th unit is
+// taken in round r: the kind's units go to the pairs that have one in the round in turn,
+// so that pairs running at the same time share operands in L2.
 struct Shares {
-    int first[3][MAX_PAIRS], n[3][MAX_PAIRS];   // by Kind
+    int n[3][MAX_PAIRS];   // by Kind
 };
 
 struct Params {
     int T, H, I;
     // part being made: rows [up0, up0 + up_rows); being multiplied: rows [mul0, mul0 + mul_rows)
     int up0, up_rows, mul0, mul_rows;
-    const bf16* dz;
     int dx_slices, dw_slices, dx_steps, dw_steps;   // slices, and K steps of each
     int dx_f32, dw_f32, dw_add;         // sums in fp32; dw added to what is there
     unsigned int* status;
@@ -81,9 +90,9 @@ struct Unit {
 __host__ __device__ __forceinline__ int tiles_of(int v, int tile) { return (v + tile - 1) / tile; }
 
 struct Tiles {
-    int mt_up, ht, kh, mt_mul, it, k_rows, k_cols, dx_steps, dw_steps;
+    int nt_up, ht, kh, mt_mul, it, k_rows, k_cols, dx_steps, dw_steps;
     __device__ __forceinline__ Tiles(const Params& p) {
-        mt_up = tiles_of(p.up_rows, TILE);
+        nt_up = tiles_of(p.I, HALF);
         ht = tiles_of(p.H, TILE);
         kh = tiles_of(p.H, BK);
         mt_mul = tiles_of(p.mul_rows, TILE);
@@ -93,7 +102,7 @@ struct Tiles {
         dx_steps = p.dx_steps, dw_steps = p.dw_steps;
     }
     __device__ __forceinline__ Unit unit(int kind, int u) const {
-        if (kind == UP) return Unit{UP, u % mt_up, u / mt_up, 0, kh, 0};
+        if (kind == UP) return Unit{UP, u / nt_up, u % nt_up, 0, kh, 0};
         const int n = u % ht, rest = u / ht;
         if (kind == DX) {
             const int s = rest / mt_mul, k0 = s * dx_steps;
@@ -104,49 +113,61 @@ struct Tiles {
     }
 };
 
-// The units a CTA pair takes, in the order it takes them.
+// The units a CTA pair takes, in the order it takes them (by a whole warp).
 template <bool BWD>
 struct Walk {
-    int pos = 0, end, first[3], n[3];
-    __device__ __forceinline__ Walk(const Params& p, int pair) {
-        end = 0;
-#pragma unroll
-        for (int k = 0; k < (BWD ? 3 : 1); ++k) {
-            first[k] = p.shares.first[k][pair];
-            n[k] = p.shares.n[k][pair];
-            end += n[k];
-        }
+    const Params& p;
+    int pair, pairs, kind, round;
+    __device__ __forceinline__ Walk(const Params& p_, int pair_, int pairs_)
+        : p(p_), pair(pair_), pairs(pairs_), kind(BWD ? (int)DW : (int)UP), round(0) { skip(); }
+    __device__ __forceinline__ void skip() {
+        while (BWD && kind > UP && round >= p.shares.n[kind][pair]) --kind, round = 0;   // DW, DX, UP
     }
-    __device__ __forceinline__ bool done() const { return pos >= end; }
+    __device__ __forceinline__ bool done() const { return kind == UP && round >= p.shares.n[UP][pair]; }
     __device__ __forceinline__ Unit next(const Tiles& t) {
-        int u = pos++;
-        if constexpr (BWD) {
-            if (u < n[DW]) return t.unit(DW, first[DW] + u);
-            u -= n[DW];
-            if (u < n[DX]) return t.unit(DX, first[DX] + u);
-            u -= n[DX];
+        int u = 0;   // units of the rounds before, and of this round for the pairs before
+        for (int q = threadIdx.x & 31; q < pairs; q += 32) {
+            const int n = p.shares.n[kind][q];
+            u += min(n, round) + (q < pair && n > round);
         }
-        return t.unit(UP, first[UP] + u);
+        const Unit w = t.unit(kind, __reduce_add_sync(0xffffffffu, u));
+        ++round;
+        skip();
+        return w;
     }
 };
 
-// da and dg of one element.  GELU(a) = a Phi(a) and GELU'(a) = Phi(a) + a phi(a); Phi by
+// da and dg of two elements.  GELU(a) = a Phi(a) and GELU'(a) = Phi(a) + a phi(a); Phi by
 // the rational approximation of erf of Abramowitz & Stegun, formula 7.1.26, as in
 // gelu_as, whose exponential is phi's too: with q = t (a1 + t (a2 + ...)) exp(-a^2 / 2),
-// t = 1 / (1 + p |a| / sqrt 2), Phi(-|a|) = q / 2 (error below 1e-7).
-__device__ __forceinline__ void geglu_grad(float a, float g, float dz, float& da, float& dg) {
+// t = 1 / (1 + p |a| / sqrt 2), Phi(-|a|) = q / 2 (error below 1e-7).  On the packed fp32x2
+// instructions.
+__device__ __forceinline__ void geglu_grad2(float& a0, float& a1, float& g0, float& g1, float z0, float z1) {
     constexpr float P = 0.3275911f * 0.70710678118654752f;
     constexpr float H1 = 0.5f * 0.254829592f, H2 = 0.5f * -0.284496736f, H3 = 0.5f * 1.421413741f,
                     H4 = 0.5f * -1.453152027f, H5 = 0.5f * 1.061405429f;
     constexpr float NEG_HALF_LOG2E = -0.72134752044448170f, INV_SQRT_2PI = 0.39894228040143268f;
-    float t;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(fabsf(a), P, 1.0f)));
-    const float e = ex2_approx(a * a * NEG_HALF_LOG2E);
-    const float q = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, H5, H4), H3), H2), H1) * e;
-    const float phi = a < 0.f ? q : 1.f - q;
-    const float u = dz * a;
-    dg = u * phi;
-    da = g * fmaf(u * INV_SQRT_2PI, e, dz * phi);
+    auto both = [](float v) { return f2_pack(v, v); };
+    float x0, x1, y0, y1;
+    const uint64_t A = f2_pack(a0, a1), Z = f2_pack(z0, z1);
+    f2_unpack(f2_fma(f2_pack(fabsf(a0), fabsf(a1)), both(P), both(1.0f)), x0, x1);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(x0) : "f"(x0));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(x1) : "f"(x1));
+    const uint64_t T = f2_pack(x0, x1);
+    f2_unpack(f2_mul(f2_mul(A, A), both(NEG_HALF_LOG2E)), y0, y1);
+    const uint64_t E = f2_pack(ex2_approx(y0), ex2_approx(y1));
+    uint64_t q = f2_fma(T, both(H5), both(H4));
+    q = f2_fma(T, q, both(H3));
+    q = f2_fma(T, q, both(H2));
+    q = f2_fma(T, q, both(H1));
+    q = f2_mul(f2_mul(T, q), E);
+    float q0, q1;
+    f2_unpack(q, q0, q1);
+    const uint64_t phi = f2_pack(a0 < 0.f ? q0 : 1.f - q0, a1 < 0.f ? q1 : 1.f - q1);
+    const uint64_t u = f2_mul(Z, A);
+    const uint64_t da = f2_mul(f2_pack(g0, g1), f2_fma(f2_mul(u, both(INV_SQRT_2PI)), E, f2_mul(Z, phi)));
+    f2_unpack(f2_mul(u, phi), g0, g1);
+    f2_unpack(da, a0, a1);
 }
 
 template <bool BWD>
@@ -154,12 +175,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     geglu_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    using S = Smem<BWD>;
+    constexpr int STAGES = S::STAGES;
     const uint32_t sbase = smem_u32(smem);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + BAR_OFF);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + N_BARS);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::BAR_OFF);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + S::N_BARS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     auto bar = [&](int i) { return smem_u32(bars + i); };
-    constexpr int FULL = 0, EMPTY = STAGES, TFULL = 2 * STAGES, TEMPTY = 2 * STAGES + 2, MMA_DONE = 2 * STAGES + 4;
+    constexpr int FULL = 0, EMPTY = STAGES, TFULL = 2 * STAGES, TEMPTY = 2 * STAGES + 2, MMA_DONE = 2 * STAGES + 4,
+                  DZ = 2 * STAGES + 5;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t crank = cluster_ctarank();
     // the even CTA's barriers, which both signal
@@ -175,6 +199,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
             mbar_init(bar(TEMPTY + a), 2 * EPI_WARPS);   // every epilogue warp of both CTAs
         }
         mbar_init(bar(MMA_DONE), 1);
+        for (int w = 0; w < EPI_WARPS; ++w) mbar_init(bar(DZ + w), 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -188,7 +213,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     pdl_trigger();
 
     const Tiles tiles(p);
-    Walk<BWD> walk(p, blockIdx.x / 2);
+    Walk<BWD> walk(p, blockIdx.x / 2, gridDim.x / 2);
     // a wait that gives up does so for the whole warp
     auto all = [](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
 
@@ -297,9 +322,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     } else {
         // ---------------- epilogue: thread = row; of each tile half its columns ----------------
         const int quad = warp & 3, half = (warp - 2) >> 2;
-        uint8_t* stage = smem + OUT_OFF + (warp - 2) * 4096;   // this warp's staging box
-        auto send = [&](auto&& write, auto&& issue) {          // writes the box, and lane 0 stores it
-            if (lane == 0) bulk_wait_read<0>();                // its last store has read it
+        uint8_t* const stage = smem + S::OUT_OFF + (warp - 2) * S::BOXES * 4096;   // this warp's staging box
+        uint8_t* const dz_box = stage + 4096;                  // (backward) dz comes here, and dg leaves
+        const uint32_t dz_bar = bar(DZ + warp - 2);
+        int dz_asked = 0, dz_taken = 0;                        // boxes of dz
+        auto ask_dz = [&](const Unit& w) {                     // of the warp's rows and columns of a tile
+            const int x = w.n * HALF + half * 64, y = w.m * TILE + (int)crank * 128 + quad * 32;
+            if (x >= p.I || y >= p.up_rows) return;
+            if (lane == 0) {
+                bulk_wait_read<0>();
+                mbar_expect_tx(dz_bar, 4096);
+                tma_load_2d(smem_u32(dz_box), &maps.dz, x, p.up0 + y, dz_bar);
+            }
+            ++dz_asked;
+            __syncwarp();
+        };
+        auto send_box = [&](uint8_t* box, auto&& write, auto&& issue) {   // writes the box, and lane 0 stores it
+            write(box);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                issue(smem_u32(box));
+                bulk_commit();
+            }
+        };
+        auto send = [&](auto&& write, auto&& issue) {
+            if (lane == 0) bulk_wait_read<0>();                // the box's last store has read it
             __syncwarp();
             write();
             fence_proxy_async_smem();
@@ -311,18 +359,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         };
         for (int it = 0; !walk.done(); ++it) {
             const Unit w = walk.next(tiles);
+            if (BWD && w.kind == UP) ask_dz(w);
             const int acc = it & 1, use = it >> 1;
             const int row0 = w.m * TILE + (int)crank * 128 + quad * 32, row = row0 + lane;
             const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + acc * TILE;
             if (!BWD || w.kind == UP) {
                 const int col = w.n * HALF + half * 64;        // of z
-                uint4 dz[8];                                   // fetched while the products run
-                if constexpr (BWD) {
-                    const uint4* at = reinterpret_cast<const uint4*>(p.dz + (size_t)(p.up0 + row) * p.I + col);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        dz[c] = row < p.up_rows && col + 8 * c < p.I ? __ldg(at + c) : make_uint4(0, 0, 0, 0);
-                }
                 if (!all(mbar_wait(bar(TFULL + acc), use & 1, abort_flag))) break;
                 tc_fence_after();
                 float a[64], g[64];
@@ -340,25 +382,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                     if (col < p.I && row0 < p.up_rows)
                         send([&]() { stage_row_bf16x64(stage, lane, a); },
                              [&](uint32_t src) { tma_store_2d(&maps.z, src, col, row0); });
-                } else {
+                } else if (col < p.I && row0 < p.up_rows) {
+                    if (!all(mbar_wait(dz_bar, dz_taken & 1, abort_flag))) break;
+                    ++dz_taken;
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
-                        const uint32_t d[4] = {dz[c].x, dz[c].y, dz[c].z, dz[c].w};
+                        const uint4 q = *reinterpret_cast<const uint4*>(dz_box + lane * 128 + ((c ^ (lane & 7)) << 4));
+                        const uint32_t d[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             float d0, d1;
                             unpack_bf16x2(d[j], d0, d1);
                             const int k = 8 * c + 2 * j;
-                            geglu_grad(a[k], g[k], d0, a[k], g[k]);
-                            geglu_grad(a[k + 1], g[k + 1], d1, a[k + 1], g[k + 1]);
+                            geglu_grad2(a[k], a[k + 1], g[k], g[k + 1], d0, d1);
                         }
                     }
-                    if (col < p.I && row0 < p.up_rows) {
-                        send([&]() { stage_row_bf16x64(stage, lane, a); },
+                    // (asking for dz waited until the stores from both boxes had read them)
+                    send_box(stage, [&](uint8_t* box) { stage_row_bf16x64(box, lane, a); },
                              [&](uint32_t src) { tma_store_2d(&maps.z, src, col, row0); });
-                        send([&]() { stage_row_bf16x64(stage, lane, g); },
+                    send_box(dz_box, [&](uint8_t* box) { stage_row_bf16x64(box, lane, g); },
                              [&](uint32_t src) { tma_store_2d(&maps.dg, src, col, row0); });
-                    }
                 }
                 continue;
             }
@@ -412,6 +455,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                 }
             }
         }
+        if (dz_asked > dz_taken) mbar_wait_drain(dz_bar, dz_taken & 1);   // no copy may still be landing
         if (lane == 0) bulk_wait_all();   // stores complete before the CTA exits
     }
 
@@ -514,13 +558,10 @@ void make_shares(const int (&units)[3], const int (&steps)[3], int pairs, Shares
             else hi = mid;
         }
         long long left = units[kind] - taken_by_all(lo);
-        int first = 0;
         for (int p = 0; p < pairs; ++p) {
             long long k = taken(lo, p);
             if (left > 0 && load[p] + k * cost == lo) ++k, --left;
-            sh.first[kind][p] = first;
             sh.n[kind][p] = (int)k;
-            first += (int)k;
             load[p] += k * cost;
         }
     }
@@ -532,12 +573,12 @@ cudaError_t max_pairs(int dev, int num_sms, int* pairs) {
     static int of[TEE_MAX_DEVICES] = {};
     std::lock_guard<std::mutex> lock(mu);
     if (!of[dev]) {
-        cudaError_t e = cudaFuncSetAttribute(geglu_kernel<BWD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+        cudaError_t e = cudaFuncSetAttribute(geglu_kernel<BWD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Smem<BWD>::BYTES);
         if (e != cudaSuccess) return e;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(num_sms / 2 * 2);
         cfg.blockDim = dim3(NUM_THREADS);
-        cfg.dynamicSmemBytes = SMEM_BYTES;
+        cfg.dynamicSmemBytes = Smem<BWD>::BYTES;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = 2;
@@ -580,7 +621,7 @@ cudaError_t launch_geglu_train_forward(const void* x, const void* wi, void* z, i
     const int units = tiles_of(T, TILE) * tiles_of(I, HALF);
     pairs = std::min(pairs, units);
     make_shares({units, 0, 0}, {tiles_of(H, BK), 0, 0}, pairs, p.shares);
-    return launch_pdl(geglu_kernel<false>, dim3(2 * pairs), dim3(NUM_THREADS), SMEM_BYTES, s, maps, p);
+    return launch_pdl(geglu_kernel<false>, dim3(2 * pairs), dim3(NUM_THREADS), Smem<false>::BYTES, s, maps, p);
 }
 
 cudaError_t launch_geglu_train_backward(const void* x, const void* wi, const void* dz, void* dx, void* dwi, int T, int H,
@@ -599,7 +640,7 @@ cudaError_t launch_geglu_train_backward(const void* x, const void* wi, const voi
     TRY(make_tensor_map_2d(&maps.x_mn, false, x, T, H, H, 64, 64));
     Params p{};
     p.T = T, p.H = H, p.I = I;
-    p.dz = (const bf16*)dz;
+    TRY(make_tensor_map_2d(&maps.dz, false, dz, T, I, I, 32, 64));
     p.status = status;
     Sum sum_dx{}, sum_dw{};
     for (int i = 0; i <= parts; ++i) {
@@ -651,7 +692,7 @@ cudaError_t launch_geglu_train_backward(const void* x, const void* wi, const voi
             }
         }
         make_shares(units, steps, pairs, p.shares);
-        TRY(launch_pdl(geglu_kernel<true>, dim3(2 * pairs), dim3(NUM_THREADS), SMEM_BYTES, s, maps, p));
+        TRY(launch_pdl(geglu_kernel<true>, dim3(2 * pairs), dim3(NUM_THREADS), Smem<true>::BYTES, s, maps, p));
     }
     const size_t n8 = sum_dx.n8 + sum_dw.n8;
     if (!n8) return cudaSuccess;

@@ -1,8 +1,9 @@
 // Rotary positions on packed qkv rows, forward and backward (tee_train.h has the
 // formulas): the backward pass of a rotation is the rotation by the negated angle.
 //
-// Bound by memory: every element is read and written once.  Measured: 65536 rows of 12
-// heads, bf16, 604 MB: 92 us, 6.5 TB/s.
+// Bound by memory: every element is read and written once.  Measured, 65536 rows of 12
+// heads, bf16, 604 MB: 91 us, 6.6 TB/s (16 rows to a block 93, 32 100; two pairs of loads
+// together 96, six 103).
 #include "train_internal.cuh"
 
 #include <math.h>
@@ -10,8 +11,10 @@
 namespace {
 
 constexpr int THREADS = 256;
-constexpr int MAX_ROWS = 16;   // rows of a block
+constexpr int MAX_ROWS = 8;    // rows of a block
 constexpr int HALF = 32;       // pairs of a head
+constexpr int AT_ONCE = 3;     // pairs of loads on their way together
+constexpr int BLOCKS_PER_SM = 4;
 
 // Turns of the 32 pairs per position: base^(-j / 32) / (2 pi).
 struct Turns {
@@ -29,56 +32,87 @@ __device__ __forceinline__ float2 cos_sin_of_turns(double turns) {
     return make_float2(fmaf(-lo, s, c), fmaf(lo, c, s));
 }
 
-// A thread moves vectors of W elements, 16 bytes: one of a head's first half and the
-// one it pairs with, 32 elements on.  out may be x.
-template <typename E, int W>
-__global__ void __launch_bounds__(THREADS)
-    rope_kernel(const E* x, const int32_t* __restrict__ pos, E* out, int T, int heads, int rows, float sign,
+// 16 bytes as fp32 elements, and back.
+__device__ __forceinline__ void widen(const uint4& q, float (&v)[4]) {
+    v[0] = __uint_as_float(q.x), v[1] = __uint_as_float(q.y), v[2] = __uint_as_float(q.z), v[3] = __uint_as_float(q.w);
+}
+__device__ __forceinline__ void widen(const uint4& q, float (&v)[8]) {
+    unpack_bf16x2(q.x, v[0], v[1]);
+    unpack_bf16x2(q.y, v[2], v[3]);
+    unpack_bf16x2(q.z, v[4], v[5]);
+    unpack_bf16x2(q.w, v[6], v[7]);
+}
+__device__ __forceinline__ uint4 narrow(const float (&v)[4]) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+}
+__device__ __forceinline__ uint4 narrow(const float (&v)[8]) {
+    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+
+// A thread moves vectors of W elements, 16 bytes: one of a head's first half and the one
+// it pairs with, 32 elements on.  out may be x.  The first loads are on their way while
+// the block makes its rows' cos and sin.
+template <int W>
+__global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM)
+    rope_kernel(const uint4* x, const int32_t* __restrict__ pos, uint4* out, int T, int heads, int rows, float sign,
                 const __grid_constant__ Turns turns) {
     __shared__ float2 cs[MAX_ROWS][HALF];
     pdl_wait();
     pdl_trigger();
     const int row0 = blockIdx.x * rows, n = min(rows, T - row0);
-    for (int i = threadIdx.x; i < n * HALF; i += THREADS) {
-        float2 v = cos_sin_of_turns((double)pos[row0 + i / HALF] * turns.per_position[i % HALF]);
-        v.y *= sign;
-        cs[i / HALF][i % HALF] = v;
-    }
-    __syncthreads();
-    constexpr int VECS = HALF / W;                 // vectors of half a head
+    constexpr int VECS = HALF / W;                        // vectors of half a head
     const int moved = out == x ? 2 * heads : 3 * heads;   // in place the values stay
     const int per_row = moved * VECS, items = n * per_row;
-    constexpr int AT_ONCE = 3;                     // pairs of loads on their way together
-    for (int i0 = threadIdx.x; i0 < items; i0 += AT_ONCE * THREADS) {
-        float u[AT_ONCE][W], v[AT_ONCE][W];
-        size_t at[AT_ONCE];
-        int row[AT_ONCE], head[AT_ONCE], vec[AT_ONCE];
+    uint4 u[AT_ONCE], v[AT_ONCE];
+    auto place = [&](int i, int& row, int& head, int& vec) {
+        row = i / per_row;
+        const int k = i - row * per_row;
+        head = k / VECS, vec = k % VECS;
+        return ((size_t)(row0 + row) * 3 * heads + head) * 2 * VECS + vec;
+    };
+    auto load = [&](int i0) {
 #pragma unroll
         for (int q = 0; q < AT_ONCE; ++q) {
-            const int i = i0 + q * THREADS;
-            if (i >= items) break;
-            row[q] = i / per_row;
-            const int k = i - row[q] * per_row;
-            head[q] = k / VECS, vec[q] = k % VECS;
-            at[q] = (size_t)(row0 + row[q]) * 3 * heads * 64 + head[q] * 64 + vec[q] * W;
-            load_vec(x + at[q], u[q]);
-            load_vec(x + at[q] + HALF, v[q]);
-        }
-#pragma unroll
-        for (int q = 0; q < AT_ONCE; ++q) {
+            int row, head, vec;
             if (i0 + q * THREADS >= items) break;
-            if (head[q] < 2 * heads) {
+            const size_t at = place(i0 + q * THREADS, row, head, vec);
+            u[q] = x[at];
+            v[q] = x[at + VECS];
+        }
+    };
+    int i0 = threadIdx.x;
+    load(i0);
+    for (int i = threadIdx.x; i < n * HALF; i += THREADS) {
+        float2 t = cos_sin_of_turns((double)pos[row0 + i / HALF] * turns.per_position[i % HALF]);
+        t.y *= sign;
+        cs[i / HALF][i % HALF] = t;
+    }
+    __syncthreads();
+    while (i0 < items) {
+#pragma unroll
+        for (int q = 0; q < AT_ONCE; ++q) {
+            int row, head, vec;
+            if (i0 + q * THREADS >= items) break;
+            const size_t at = place(i0 + q * THREADS, row, head, vec);
+            if (head < 2 * heads) {
+                float a[W], b[W];
+                widen(u[q], a);
+                widen(v[q], b);
 #pragma unroll
                 for (int j = 0; j < W; ++j) {
-                    const float2 t = cs[row[q]][vec[q] * W + j];
-                    const float a = u[q][j], b = v[q][j];
-                    u[q][j] = a * t.x - b * t.y;
-                    v[q][j] = b * t.x + a * t.y;
+                    const float2 t = cs[row][vec * W + j];
+                    const float c = a[j], d = b[j];
+                    a[j] = c * t.x - d * t.y;
+                    b[j] = d * t.x + c * t.y;
                 }
+                u[q] = narrow(a);
+                v[q] = narrow(b);
             }
-            store_vec(out + at[q], u[q]);
-            store_vec(out + at[q] + HALF, v[q]);
+            out[at] = u[q];
+            out[at + VECS] = v[q];
         }
+        i0 += AT_ONCE * THREADS;
+        load(i0);
     }
 }
 
@@ -96,9 +130,6 @@ cudaError_t launch_rope_train(const void* x, bool is_bf16, const int32_t* pos, v
     const int fit = (T + 4 * num_sms - 1) / (4 * num_sms), rows = fit < MAX_ROWS ? fit : MAX_ROWS;
     const dim3 grid((T + rows - 1) / rows);
     const float sign = backward ? -1.f : 1.f;
-    if (is_bf16)
-        return launch_pdl(rope_kernel<bf16, 8>, grid, dim3(THREADS), 0, s, (const bf16*)x, pos, (bf16*)out, T, heads, rows,
-                          sign, turns);
-    return launch_pdl(rope_kernel<float, 4>, grid, dim3(THREADS), 0, s, (const float*)x, pos, (float*)out, T, heads, rows,
-                      sign, turns);
+    auto kernel = is_bf16 ? rope_kernel<8> : rope_kernel<4>;
+    return launch_pdl(kernel, grid, dim3(THREADS), 0, s, (const uint4*)x, pos, (uint4*)out, T, heads, rows, sign, turns);
 }
