@@ -337,15 +337,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
             ++dz_asked;
             __syncwarp();
         };
-        auto send_box = [&](uint8_t* box, auto&& write, auto&& issue) {   // writes the box, and lane 0 stores it
-            write(box);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                issue(smem_u32(box));
-                bulk_commit();
-            }
-        };
         auto send = [&](auto&& write, auto&& issue) {
             if (lane == 0) bulk_wait_read<0>();                // the box's last store has read it
             __syncwarp();
@@ -367,41 +358,72 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                 const int col = w.n * HALF + half * 64;        // of z
                 if (!all(mbar_wait(bar(TFULL + acc), use & 1, abort_flag))) break;
                 tc_fence_after();
-                float a[64], g[64];
-                tmem_ld64_issue(taddr + half * 64, a);
-                tmem_ld64_issue(taddr + HALF + half * 64, g);
-                tmem_wait_ld();
-                tmem_tie64(a);
-                tmem_tie64(g);
+                // 16 columns of a and g at a time, the next on their way while these are worked on: beside the products a
+                // load takes 1000 cycles and more
+                const bool used = col < p.I && row0 < p.up_rows;
+                if (used) {
+                    if (BWD) {
+                        if (!all(mbar_wait(dz_bar, dz_taken & 1, abort_flag))) break;
+                        ++dz_taken;
+                        // (asking for dz waited until the stores from both boxes had read them)
+                    } else {
+                        if (lane == 0) bulk_wait_read<0>();
+                        __syncwarp();
+                    }
+                    float a[2][16], g[2][16];
+                    tmem_ld16_issue(taddr + half * 64, a[0]);
+                    tmem_ld16_issue(taddr + HALF + half * 64, g[0]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        float(&ca)[16] = a[c & 1], (&cg)[16] = g[c & 1];
+                        tmem_wait_ld();
+                        tmem_tie16(ca);
+                        tmem_tie16(cg);
+                        if (c < 3) {
+                            tmem_ld16_issue(taddr + half * 64 + 16 * (c + 1), a[(c + 1) & 1]);
+                            tmem_ld16_issue(taddr + HALF + half * 64 + 16 * (c + 1), g[(c + 1) & 1]);
+                        }
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {   // eight columns, a 16-byte piece of a box's row
+                            const uint32_t at = lane * 128 + ((2 * c + h) ^ (lane & 7)) * 16;
+                            uint32_t x[4], y[4];
+                            if constexpr (BWD) {
+                                const uint4 q = *reinterpret_cast<const uint4*>(dz_box + at);
+                                const uint32_t d[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    const int k = 8 * h + 2 * j;
+                                    float d0, d1;
+                                    unpack_bf16x2(d[j], d0, d1);
+                                    geglu_grad2(ca[k], ca[k + 1], cg[k], cg[k + 1], d0, d1);
+                                    x[j] = pack_bf16(ca[k], ca[k + 1]);
+                                    y[j] = pack_bf16(cg[k], cg[k + 1]);
+                                }
+                                *reinterpret_cast<uint4*>(dz_box + at) = make_uint4(y[0], y[1], y[2], y[3]);
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    const int k = 8 * h + 2 * j;
+                                    float z0, z1;
+                                    gelu_mul2(ca[k], ca[k + 1], cg[k], cg[k + 1], z0, z1);
+                                    x[j] = pack_bf16(z0, z1);
+                                }
+                            }
+                            *reinterpret_cast<uint4*>(stage + at) = make_uint4(x[0], x[1], x[2], x[3]);
+                        }
+                    }
+                }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(tempty0 + 8 * acc);
-                if constexpr (!BWD) {
-#pragma unroll
-                    for (int j = 0; j < 64; j += 2) gelu_mul2(a[j], a[j + 1], g[j], g[j + 1], a[j], a[j + 1]);
-                    if (col < p.I && row0 < p.up_rows)
-                        send([&]() { stage_row_bf16x64(stage, lane, a); },
-                             [&](uint32_t src) { tma_store_2d(&maps.z, src, col, row0); });
-                } else if (col < p.I && row0 < p.up_rows) {
-                    if (!all(mbar_wait(dz_bar, dz_taken & 1, abort_flag))) break;
-                    ++dz_taken;
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const uint4 q = *reinterpret_cast<const uint4*>(dz_box + lane * 128 + ((c ^ (lane & 7)) << 4));
-                        const uint32_t d[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            float d0, d1;
-                            unpack_bf16x2(d[j], d0, d1);
-                            const int k = 8 * c + 2 * j;
-                            geglu_grad2(a[k], a[k + 1], g[k], g[k + 1], d0, d1);
-                        }
+                if (used) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_2d(&maps.z, smem_u32(stage), col, row0);
+                        if (BWD) tma_store_2d(&maps.dg, smem_u32(dz_box), col, row0);
+                        bulk_commit();
                     }
-                    // (asking for dz waited until the stores from both boxes had read them)
-                    send_box(stage, [&](uint8_t* box) { stage_row_bf16x64(box, lane, a); },
-                             [&](uint32_t src) { tma_store_2d(&maps.z, src, col, row0); });
-                    send_box(dz_box, [&](uint8_t* box) { stage_row_bf16x64(box, lane, g); },
-                             [&](uint32_t src) { tma_store_2d(&maps.dg, src, col, row0); });
                 }
                 continue;
             }
