@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     auto bar = [&](int i) { return smem_u32(bars + i); };
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int b = 0; b < 2; ++b) {
@@ -282,85 +282,91 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         __syncwarp();
     } else if (warp == 1) {
-        // ---------------- MMA issuer ----------------
-        if (lane == 0) {
-            constexpr uint32_t idesc_s = make_idesc(BQ, BKV);
-            constexpr uint32_t idesc_pv = make_idesc(BQ, HD) | IDESC_B_MN_MAJOR;
-            // P_tt V_tt accumulated into the unit's TMEM O buffer; the first
-            // tile of a unit overwrites it once the softmax warps have read the
-            // unit two back out of that buffer
-            auto issue_pv = [&](uint32_t tt, bool first, int ub, uint32_t uuse) -> bool {
-                const int sb = tt % SP_BUFS, st = tt % KV_STAGES;
-                if (!mbar_wait(bar(B_PF + sb), (tt / SP_BUFS) & 1, abort_flag)) return false;
-                if (first && !mbar_wait(bar(B_OE + ub), (uuse & 1) ^ 1, abort_flag)) return false;
-                tc_fence_after();
-                const uint32_t pbase = tmem_base + TM_S + sb * BKV;
-                const uint32_t vbase = sbase + OFF_V + st * TILE_BYTES;
+        // ---------------- MMA issuer (the whole warp, one lane issuing: addresses and descriptors stay uniform) ----------------
+        constexpr uint32_t idesc_s = make_idesc(BQ, BKV);
+        constexpr uint32_t idesc_pv = make_idesc(BQ, HD) | IDESC_B_MN_MAJOR;
+        const uint64_t q0desc = sw128_desc(sbase + OFF_Q), k0desc = sw128_desc(sbase + OFF_K);
+        const uint64_t v0desc = sw128_desc_mn(sbase + OFF_V);
+        constexpr uint32_t TILE_DESC = TILE_BYTES >> 4;
+        auto wait = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar(b), parity, abort_flag)) != 0; };
+        // P_tt V_tt accumulated into the unit's TMEM O buffer; the first
+        // tile of a unit overwrites it once the softmax warps have read the
+        // unit two back out of that buffer
+        auto issue_pv = [&](uint32_t tt, bool first, int ub, uint32_t uuse) -> bool {
+            const uint32_t sb = tt % SP_BUFS, st = tt % KV_STAGES;
+            if (!wait(B_PF + sb, (tt / SP_BUFS) & 1)) return false;
+            if (first && !wait(B_OE + ub, (uuse & 1) ^ 1)) return false;
+            tc_fence_after();
+            const uint32_t pbase = tmem_base + TM_S + sb * BKV, obase = tmem_base + TM_O + ub * HD;
+            const uint64_t vdesc = v0desc + st * TILE_DESC;
+            if (elect_one()) {
 #pragma unroll
-                for (int s = 0; s < BKV / 16; ++s) {
-                    const uint64_t vdesc = sw128_desc_mn(vbase + s * 2048);
-                    mma_bf16_ts(tmem_base + TM_O + ub * HD, pbase + 8 * s, vdesc, idesc_pv, !(first && s == 0));
-                }
+                for (int s = 0; s < BKV / 16; ++s)
+                    mma_bf16_ts(obase, pbase + 8 * s, vdesc + s * 128, idesc_pv, !(first && s == 0));
                 // one commit frees the K/V stage and tells the softmax warps
                 // that P_tt V_tt is in O
-                mma_commit(bar(B_KVE + st));
-                return true;
-            };
-            struct Pend {
-                uint32_t t, use;
-                bool first;
-                int ub;
-            };
-            Pend q0{}, q1{};         // tiles whose S is issued and whose P V is not (at most two)
-            int nq = 0;
-            uint32_t t = 0;          // tiles whose S has been issued (global)
-            bool ok = true;
-            int ui = 0;
-            int4 it_next = i0 < i1 ? slot(i0) : make_int4(0, 0, 0, 0);
-            for (int i = i0; i < i1 && ok; ++i, ++ui) {
-                const int nk = n_kv_tiles(it_next);
-                if (i + 1 < i1) it_next = slot(i + 1);
-                const int qb = ui & 1;
-                if (!mbar_wait(bar(B_QF + qb), (ui >> 1) & 1, abort_flag)) break;
-                const uint64_t qdesc = sw128_desc(sbase + OFF_Q + qb * TILE_BYTES);
-                for (int kt = 0; kt < nk; ++kt, ++t) {
-                    // buffer t % 3 last held tile t - 3, whose P V was issued
-                    // before this S (and runs before it): no wait for it here
-                    const int st = t % KV_STAGES, sb = t % SP_BUFS;
-                    if (!mbar_wait(bar(B_KVF + st), (t / KV_STAGES) & 1, abort_flag)) {
+                mma_commit(bar(B_KVE) + 8 * st);
+            }
+            __syncwarp();
+            return true;
+        };
+        struct Pend {
+            uint32_t t, use;
+            bool first;
+            int ub;
+        };
+        Pend q0{}, q1{};         // tiles whose S is issued and whose P V is not (at most two)
+        int nq = 0;
+        uint32_t t = 0;          // tiles whose S has been issued (global)
+        bool ok = true;
+        int ui = 0;
+        int4 it_next = i0 < i1 ? slot(i0) : make_int4(0, 0, 0, 0);
+        for (int i = i0; i < i1 && ok; ++i, ++ui) {
+            const int nk = n_kv_tiles(it_next);
+            if (i + 1 < i1) it_next = slot(i + 1);
+            const int qb = ui & 1;
+            if (!wait(B_QF + qb, (ui >> 1) & 1)) break;
+            const uint64_t qdesc = q0desc + qb * TILE_DESC;
+            for (int kt = 0; kt < nk; ++kt, ++t) {
+                // buffer t % 3 last held tile t - 3, whose P V was issued
+                // before this S (and runs before it): no wait for it here
+                const uint32_t st = t % KV_STAGES, sb = t % SP_BUFS;
+                if (!wait(B_KVF + st, (t / KV_STAGES) & 1)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t kdesc = k0desc + st * TILE_DESC;
+                const uint32_t sbuf = tmem_base + TM_S + sb * BKV;
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < HD / 16; ++k) mma_bf16(sbuf, qdesc + 2 * k, kdesc + 2 * k, idesc_s, k != 0);
+                    mma_commit(bar(B_SF) + 8 * sb);
+                    if (kt == nk - 1) mma_commit(bar(B_QE) + 8 * qb);   // Q buffer free once these S MMAs finish
+                }
+                __syncwarp();
+                const Pend cur{t, (uint32_t)ui >> 1, kt == 0, ui & 1};
+                if (nq == 2) {   // P V two tiles behind S
+                    if (!issue_pv(q0.t, q0.first, q0.ub, q0.use)) {
                         ok = false;
                         break;
                     }
-                    tc_fence_after();
-                    const uint64_t kdesc = sw128_desc(sbase + OFF_K + st * TILE_BYTES);
-#pragma unroll
-                    for (int k = 0; k < HD / 16; ++k)
-                        mma_bf16(tmem_base + TM_S + sb * BKV, qdesc + 2 * k, kdesc + 2 * k, idesc_s, k != 0);
-                    mma_commit(bar(B_SF + sb));
-                    if (kt == nk - 1) mma_commit(bar(B_QE + qb));   // Q buffer free once these S MMAs finish
-                    const Pend cur{t, (uint32_t)ui >> 1, kt == 0, ui & 1};
-                    if (nq == 2) {   // P V two tiles behind S
-                        if (!issue_pv(q0.t, q0.first, q0.ub, q0.use)) {
-                            ok = false;
-                            break;
-                        }
-                        q0 = q1;
-                        q1 = cur;
-                    } else if (nq == 1) {
-                        q1 = cur;
-                        nq = 2;
-                    } else {
-                        q0 = cur;
-                        nq = 1;
-                    }
+                    q0 = q1;
+                    q1 = cur;
+                } else if (nq == 1) {
+                    q1 = cur;
+                    nq = 2;
+                } else {
+                    q0 = cur;
+                    nq = 1;
                 }
             }
-            if (ok && nq >= 1) ok = issue_pv(q0.t, q0.first, q0.ub, q0.use);
-            if (ok && nq == 2) ok = issue_pv(q1.t, q1.first, q1.ub, q1.use);
-            mma_commit(bar(B_DONE));
-            mbar_wait_drain(bar(B_DONE), 0);
         }
+        if (ok && nq >= 1) ok = issue_pv(q0.t, q0.first, q0.ub, q0.use);
+        if (ok && nq == 2) ok = issue_pv(q1.t, q1.first, q1.ub, q1.use);
+        if (elect_one()) mma_commit(bar(B_DONE));
         __syncwarp();
+        mbar_wait_drain(bar(B_DONE), 0);
     } else {
         // ---------------- softmax / output (warps 2..9) ----------------
         // Warps w and w + 4 share a TMEM lane quadrant (rows 32*quad ..) and
