@@ -181,7 +181,7 @@ __device__ __noinline__ float attn_row_again(const AttnParams& p, int row, int h
 // items whose rows see different keys, is computed again from its own.
 template <bool WINDOW, bool TRAIN>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
-    attn_tc_kernel(const __grid_constant__ CUtensorMap tm, AttnParams p) {
+    attn_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ AttnParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
