@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) attn_plan_kernel(const PlanArgs 
 // the backward kernel
 // ---------------------------------------------------------------------------
 
-constexpr int STAGES = 4;
+constexpr int STAGES = 3;
 constexpr int FIRST_WORKER = 4, WORKERS = 8;   // warps 4 .. 11, two to a quarter of the rows, 64 columns each
 
 constexpr int NUM_THREADS = 32 * (FIRST_WORKER + WORKERS);
@@ -238,7 +238,8 @@ constexpr uint32_t OFF_COLS = OFF_ROWS + 4 * TILE_BYTES;             // STAGES o
 constexpr uint32_t EXT_BYTES = TILE * 16 * 2;                        // 4 KB, not swizzled: 8 rows x 16 bytes together
 constexpr uint32_t OFF_EXT = OFF_COLS + STAGES * 2 * TILE_BYTES;     // STAGES
 constexpr uint32_t OFF_ONES = OFF_EXT + STAGES * EXT_BYTES;          // for S, for dP
-constexpr uint32_t OFF_BAR = OFF_ONES + 2 * EXT_BYTES;
+constexpr uint32_t OFF_OUT = OFF_ONES + 2 * EXT_BYTES;               // a 4 KB box per worker warp
+constexpr uint32_t OFF_BAR = OFF_OUT + WORKERS * 4096;
 constexpr int B_RF = 0, B_RE = 2, B_CF = 4, B_CE = B_CF + STAGES, B_SF = B_CE + STAGES, B_XF = B_SF + STAGES, B_X2R = B_XF + 2, B_PF = B_X2R + 1,
               B_OF = B_PF + 2, B_OE = B_OF + 1, B_DONE = B_OE + 1, N_BARS = B_DONE + 1;
 constexpr uint32_t SMEM_TOTAL = OFF_BAR + N_BARS * 8 + 16 + 1024;
@@ -274,26 +275,28 @@ struct BwdParams {
     unsigned int* status;
 };
 
-// A unit as {q_start, q_len | keys << 8 | head << 16, k_lo, k_hi}; the units of an item:
-// its rows as keys, the longer kind, for every head, then its rows as queries.
-__device__ __forceinline__ int4 bwd_unit(const BwdParams& p, int i) {
+// A unit as {q_start, q_len | keys << 8 | head << 16, k_lo, k_hi}: first the items' rows as
+// keys, the longer kind, for every head, then as queries.
+__device__ __forceinline__ int4 bwd_unit(const BwdParams& p, int n_items, int i) {
     const int u = attn_unit(i, blockIdx.x, gridDim.x), k = u / p.n_heads, head = u - k * p.n_heads;
-    int4 it = p.plan.items[k >> 1];
-    it.y |= ((k & 1) ^ 1) << 8 | head << 16;
+    const bool keys = k < n_items;
+    int4 it = p.plan.items[keys ? k : k - n_items];
+    it.y |= (keys ? 1 : 0) << 8 | head << 16;
     return it;
 }
 // A CTA's units in turn, each read while the one before is worked on.
 struct UnitStream {
     const BwdParams& p;
-    int n, i = 0;
+    int n_items, n, i = 0;
     int4 ahead;
-    __device__ __forceinline__ UnitStream(const BwdParams& p_, int n_) : p(p_), n(n_), ahead(make_int4(0, 0, 0, 0)) {
-        if (n > 0) ahead = bwd_unit(p, 0);
+    __device__ __forceinline__ UnitStream(const BwdParams& p_, int n_items_, int n_)
+        : p(p_), n_items(n_items_), n(n_), ahead(make_int4(0, 0, 0, 0)) {
+        if (n > 0) ahead = bwd_unit(p, n_items, 0);
     }
     __device__ __forceinline__ int4 next() {
         const int4 it = ahead;
         ++i;
-        ahead = i < n ? bwd_unit(p, i) : make_int4(0, 0, 0, 0);
+        ahead = i < n ? bwd_unit(p, n_items, i) : make_int4(0, 0, 0, 0);
         return it;
     }
 };
@@ -312,10 +315,9 @@ __device__ __noinline__ bool warp_wait_longer(uint32_t bar, uint32_t parity, vol
     }
 }
 
-// Column `first` .. of one row's gradients again, outside the tensor cores, by a whole
+// One row's dq, or its dk or dv (`second`), again, outside the tensor cores, by a whole
 // warp: of a row whose products met NaN or infinities of rows that it does not see.
-// Lanes 2k and 2k + 1 of the result hold the row's columns as pairs.
-__device__ __noinline__ void bwd_row_again(const BwdParams& p, int row, int head, bool keys, int lo, int hi, int chunk) {
+__device__ __noinline__ void bwd_row_again(const BwdParams& p, int row, int head, bool keys, int lo, int hi, bool second) {
     const int lane = threadIdx.x & 31, H = p.hidden;
     auto two = [&](const bf16* base, size_t at) {
         return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(base + at + head * HD + 2 * lane));
@@ -339,14 +341,14 @@ __device__ __noinline__ void bwd_row_again(const BwdParams& p, int row, int head
         o1.x = fmaf(d, b1.x, o1.x), o1.y = fmaf(d, b1.y, o1.y);
         o2.x = fmaf(e, b2.x, o2.x), o2.y = fmaf(e, b2.y, o2.y);
     }
-    if (lane / 16 != chunk) return;
     bf16* dst = p.dqkv + row * stride + head * HD + 2 * lane;
-    *reinterpret_cast<uint32_t*>(dst + (keys ? H : 0)) = pack_bf16x2(o1.x * 0.125f, o1.y * 0.125f);
-    if (keys) *reinterpret_cast<uint32_t*>(dst + 2 * H) = pack_bf16x2(o2.x, o2.y);
+    if (second) *reinterpret_cast<uint32_t*>(dst + 2 * H) = pack_bf16x2(o2.x, o2.y);
+    else *reinterpret_cast<uint32_t*>(dst + (keys ? H : 0)) = pack_bf16x2(o1.x * 0.125f, o1.y * 0.125f);
 }
 
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __grid_constant__ CUtensorMap tm_do,
+                    const __grid_constant__ CUtensorMap tm_out,
                     const __grid_constant__ BwdParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -393,7 +395,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     pdl_wait();
     pdl_trigger();
 
-    const int n_units = attn_units_of(*p.plan.n_items * 2 * p.n_heads, blockIdx.x, gridDim.x);
+    const int n_items = *p.plan.n_items, n_units = attn_units_of(n_items * 2 * p.n_heads, blockIdx.x, gridDim.x);
     // a whole warp's wait: true for all lanes, or false for all
     auto warp_wait = [&](int b, uint32_t parity) -> bool {
         return __all_sync(0xffffffffu, mbar_try_wait(bar(b), parity)) || warp_wait_longer(bar(b), parity, abort_flag);
@@ -404,7 +406,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         uint32_t t = 0;
         int ui = 0;
         bool ok = true;
-        UnitStream units(p, n_units);
+        UnitStream units(p, n_items, n_units);
         float v[2][4];   // of the tile to come
         auto statistics = [&](const int4& it, int kt) {
             if (!(it.y >> 8 & 1)) return;
@@ -483,7 +485,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const uint64_t ones = ext_desc(sbase + OFF_ONES + (is_s ? 0 : EXT_BYTES)), ext0 = ext_desc(sbase + OFF_EXT);
         uint32_t t = 0;
         bool ok = true;
-        UnitStream units(p, n_units);
+        UnitStream units(p, n_items, n_units);
         for (int ui = 0; ui < n_units && ok; ++ui) {
             const int4 it = units.next();
             const int nk = unit_tiles(it), rb = ui & 1;
@@ -521,7 +523,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const uint64_t cols0 = sw128_desc_mn(sbase + OFF_COLS);
         uint32_t t = 0;
         bool ok = true;
-        UnitStream units(p, n_units);
+        UnitStream units(p, n_items, n_units);
         for (int ui = 0; ui < n_units && ok; ++ui) {
             const int4 it = units.next();
             const int nk = unit_tiles(it);
@@ -573,29 +575,58 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             lo = max(tb.x, it.z), hi = min(tb.y, it.w);
             if (p.window >= 0) lo = max(lo, row - p.window), hi = min(hi, row + p.window + 1);
         };
-        // a unit's outputs, read once the next one's first tile is handed over
+        // A unit's outputs, read once the next one's first tile is handed over: dq, or dk by one warp of the two and dv by
+        // the other.  They leave as copies of 32 rows (row by row from the threads, a warp's store touches 32 lines: 1024
+        // to 2048 cycles a unit for the 8 warps).
         auto finish = [&](int ui_p, const int4& it_p, const int2& tb_p) -> bool {
-            const int row_p = r < (it_p.y & 0xff) ? it_p.x + r : -1, head_p = it_p.y >> 16;
+            const int q_len_p = it_p.y & 0xff, row_p = r < q_len_p ? it_p.x + r : -1, head_p = it_p.y >> 16;
             const bool keys_p = it_p.y >> 8 & 1;
-            // rows of one text that all see the same columns meet no others' values
-            const bool alone = p.window < 0 && tb_p.x == it_p.z && tb_p.y == it_p.w;
             if (!warp_wait(B_OF, ui_p & 1)) return false;
+            if (lane == 0) bulk_wait_read<0>();   // the box's last copy has read it
+            __syncwarp();
             tc_fence_after();
+            const bool mine = keys_p || chunk == 0, whole = quad * 32 + 32 <= q_len_p;
+            const float scale = chunk ? 1.f : 0.125f;
             float z = 0.f;   // not a number where one of the sums is not finite
-            bf16* const dst = p.dqkv + (size_t)max(row_p, 0) * 3 * p.hidden + head_p * HD + chunk * 32;
+            const int x = (keys_p ? (chunk + 1) * p.hidden : 0) + head_p * HD;
+            uint8_t* const box = smem + OFF_OUT + (warp - FIRST_WORKER) * 4096;
+            bf16* const dst = p.dqkv + (size_t)max(row_p, 0) * 3 * p.hidden + x;
+            if (mine) {
 #pragma unroll 1
-            for (int i = 0; i < (keys_p ? 2 : 1); ++i) {   // dq, or dk and dv
-                float o[32];
-                tmem_ld32(lanes + TM_O + i * HD + chunk * 32, o);
-                const float scale = i ? 1.f : 0.125f;
+                for (int h = 0; h < 2; ++h) {
+                    float o[32];
+                    tmem_ld32(lanes + TM_O + chunk * HD + 32 * h, o);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) o[j] *= scale, z = fmaf(o[j], 0.f, z);
-                if (row_p >= 0) store_bf16x32(dst + (keys_p ? (i + 1) * p.hidden : 0), o);
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t q[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float u = o[8 * c + 2 * j] * scale, v = o[8 * c + 2 * j + 1] * scale;
+                            z = fmaf(u, 0.f, fmaf(v, 0.f, z));
+                            q[j] = pack_bf16(u, v);
+                        }
+                        const uint4 piece = make_uint4(q[0], q[1], q[2], q[3]);
+                        if (whole) *reinterpret_cast<uint4*>(box + lane * 128 + (((4 * h + c) ^ (lane & 7)) << 4)) = piece;
+                        else if (row_p >= 0) *reinterpret_cast<uint4*>(dst + 32 * h + 8 * c) = piece;
+                    }
+                }
             }
             tc_fence_before();
+            fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(B_OE));
+            if (!mine) return true;
+            if (whole && lane == 0) {
+                tma_store_2d(&tm_out, smem_u32(box), x, it_p.x + quad * 32);
+                bulk_commit();
+            }
+            // rows of one text that all see the same columns meet no others' values
+            const bool alone = p.window < 0 && tb_p.x == it_p.z && tb_p.y == it_p.w;
             unsigned again = __ballot_sync(0xffffffffu, row_p >= 0 && !alone && !(z == 0.f));
+            if (again) {
+                if (lane == 0) bulk_wait_all();
+                __syncwarp();
+            }
             int lo_p, hi_p;
             seen(it_p, tb_p, lo_p, hi_p);
             while (again) {
@@ -609,7 +640,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         };
 
         // a unit's rows' texts and statistics are read while the unit before is worked on
-        UnitStream units(p, n_units);
+        UnitStream units(p, n_items, n_units);
         int4 it = make_int4(0, 0, 0, 0), it_next = units.next();
         int2 tb = make_int2(0, 0), tb_next = text_of(it_next);
         float nl_next = 0.f, nd_next = 0.f;
@@ -734,6 +765,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
     }
 
+    if (warp >= FIRST_WORKER && lane == 0) bulk_wait_all();   // stores complete before the CTA exits
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
@@ -806,11 +838,12 @@ cudaError_t launch_attention_train_backward(const void* qkv, const int32_t* cu, 
     const int max_items = attention_max_items(T, n_texts), H = n_heads * HD;
     PlanArgs a{cu, T, n_texts, n_heads, window, max_items, {}, (const bf16*)o, (const bf16*)d_o, lse, status};
     carve(T, n_texts, n_heads, true, ws, &a.plan);
-    CUtensorMap tm_qkv, tm_do;
+    CUtensorMap tm_qkv, tm_do, tm_out;
     if ((e = make_tensor_map_2d(&tm_qkv, false, qkv, T, 3 * (uint64_t)H, 3 * (uint64_t)H, TILE, HD)) != cudaSuccess) return e;
     if ((e = make_tensor_map_2d(&tm_do, false, d_o, T, H, H, TILE, HD)) != cudaSuccess) return e;
+    if ((e = make_tensor_map_2d(&tm_out, false, dqkv, T, 3 * (uint64_t)H, 3 * (uint64_t)H, 32, HD)) != cudaSuccess) return e;
     if ((e = launch_plan(a, s)) != cudaSuccess) return e;
     BwdParams p{a.plan, T, n_heads, H, window, (const bf16*)qkv, (const bf16*)d_o, (bf16*)dqkv, status};
     const int grid = (int)std::min<long long>(num_sms, 2LL * max_items * n_heads);
-    return launch_pdl(attn_bwd_kernel, dim3(grid), dim3(NUM_THREADS), SMEM_TOTAL, s, tm_qkv, tm_do, p);
+    return launch_pdl(attn_bwd_kernel, dim3(grid), dim3(NUM_THREADS), SMEM_TOTAL, s, tm_qkv, tm_do, tm_out, p);
 }
