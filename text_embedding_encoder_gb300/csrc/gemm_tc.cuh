@@ -46,3 +46,6 @@ inline int geglu_source_row(int r, int I) {
 // a row (row_elems elements) a multiple of 16 bytes.
 cudaError_t make_tensor_map_2d(CUtensorMap* map, bool is_f32, const void* base, uint64_t rows, uint64_t cols,
                                uint64_t row_elems, uint32_t box_rows, uint32_t box_cols);
+// The same of bf16 in boxes of box_rows x 32 columns with the 64-byte swizzle.
+cudaError_t make_tensor_map_2d_64(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint64_t row_elems,
+                                  uint32_t box_rows);

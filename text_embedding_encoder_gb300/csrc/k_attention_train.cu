@@ -275,31 +275,46 @@ struct BwdParams {
     unsigned int* status;
 };
 
-// A unit as {q_start, q_len | keys << 8 | head << 16, k_lo, k_hi}: first the items' rows as
-// keys, the longer kind, for every head, then as queries.
-__device__ __forceinline__ int4 bwd_unit(const BwdParams& p, int n_items, int i) {
-    const int u = attn_unit(i, blockIdx.x, gridDim.x), k = u / p.n_heads, head = u - k * p.n_heads;
-    const bool keys = k < n_items;
-    int4 it = p.plan.items[keys ? k : k - n_items];
-    it.y |= (keys ? 1 : 0) << 8 | head << 16;
-    return it;
-}
-// A CTA's units in turn, each read while the one before is worked on.
+// A CTA's units in turn, each read while the one before is worked on: {q_start, q_len |
+// keys << 8 | head << 16, k_lo, k_hi}.  First the items' rows as keys, the longer kind, for
+// every head, then as queries.  From unit to unit (attn_unit) the steps are two in turn,
+// so one division each does for all.
 struct UnitStream {
     const BwdParams& p;
-    int n_items, n, i = 0;
+    int n_items, n, i = 0, item, head, step_item[2], step_head[2];
     int4 ahead;
-    __device__ __forceinline__ UnitStream(const BwdParams& p_, int n_items_, int n_)
-        : p(p_), n_items(n_items_), n(n_), ahead(make_int4(0, 0, 0, 0)) {
-        if (n > 0) ahead = bwd_unit(p, n_items, 0);
+    __device__ __forceinline__ UnitStream(const BwdParams& p_, int n_items_, int n_) : p(p_), n_items(n_items_), n(n_) {
+        const int c = blockIdx.x, G = gridDim.x, heads = p.n_heads;
+        item = c / heads, head = c - item * heads;
+        step_item[0] = (2 * (G - c) - 1) / heads, step_head[0] = 2 * (G - c) - 1 - step_item[0] * heads;
+        step_item[1] = (2 * c + 1) / heads, step_head[1] = 2 * c + 1 - step_item[1] * heads;
+        read();
+    }
+    __device__ __forceinline__ void read() {
+        ahead = make_int4(0, 0, 0, 0);
+        if (i >= n) return;
+        const bool keys = item < n_items;
+        ahead = p.plan.items[keys ? item : item - n_items];
+        ahead.y |= (keys ? 1 : 0) << 8 | head << 16;
     }
     __device__ __forceinline__ int4 next() {
         const int4 it = ahead;
+        item += i & 1 ? step_item[1] : step_item[0];
+        head += i & 1 ? step_head[1] : step_head[0];
+        if (head >= p.n_heads) head -= p.n_heads, ++item;
         ++i;
-        ahead = i < n ? bwd_unit(p, n_items, i) : make_int4(0, 0, 0, 0);
+        read();
         return it;
     }
 };
+// Four bytes, each a byte of v's top bit over: the byte that the digit of SELECT less 8 names.
+template <int SELECT>
+__device__ __forceinline__ uint32_t byte_signs(uint32_t v) {
+    uint32_t r;
+    asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(v), "n"(SELECT));
+    return r;
+}
+__device__ __forceinline__ uint32_t ones_below(int n) { return n < 32 ? (1u << n) - 1 : 0xffffffffu; }   // 0 <= n <= 32
 __device__ __forceinline__ int unit_tiles(const int4& it) { return (it.w - it.z + TILE - 1) / TILE; }
 
 // A whole warp's wait for what it has not found done; gives up as mbar_wait does.
@@ -315,9 +330,9 @@ __device__ __noinline__ bool warp_wait_longer(uint32_t bar, uint32_t parity, vol
     }
 }
 
-// One row's dq, or its dk or dv (`second`), again, outside the tensor cores, by a whole
+// What a worker warp writes of one row, 32 columns of dq, or its dk (chunk 0) or dv, again, outside the tensor cores, by a whole
 // warp: of a row whose products met NaN or infinities of rows that it does not see.
-__device__ __noinline__ void bwd_row_again(const BwdParams& p, int row, int head, bool keys, int lo, int hi, bool second) {
+__device__ __noinline__ void bwd_row_again(const BwdParams& p, int row, int head, bool keys, int lo, int hi, int chunk) {
     const int lane = threadIdx.x & 31, H = p.hidden;
     auto two = [&](const bf16* base, size_t at) {
         return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(base + at + head * HD + 2 * lane));
@@ -342,8 +357,13 @@ __device__ __noinline__ void bwd_row_again(const BwdParams& p, int row, int head
         o2.x = fmaf(e, b2.x, o2.x), o2.y = fmaf(e, b2.y, o2.y);
     }
     bf16* dst = p.dqkv + row * stride + head * HD + 2 * lane;
-    if (second) *reinterpret_cast<uint32_t*>(dst + 2 * H) = pack_bf16x2(o2.x, o2.y);
-    else *reinterpret_cast<uint32_t*>(dst + (keys ? H : 0)) = pack_bf16x2(o1.x * 0.125f, o1.y * 0.125f);
+    if (!keys) {
+        if (lane / 16 == chunk) *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(o1.x * 0.125f, o1.y * 0.125f);
+    } else if (chunk) {
+        *reinterpret_cast<uint32_t*>(dst + 2 * H) = pack_bf16x2(o2.x, o2.y);
+    } else {
+        *reinterpret_cast<uint32_t*>(dst + H) = pack_bf16x2(o1.x * 0.125f, o1.y * 0.125f);
+    }
 }
 
 __global__ void __launch_bounds__(NUM_THREADS, 1)
@@ -575,8 +595,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             lo = max(tb.x, it.z), hi = min(tb.y, it.w);
             if (p.window >= 0) lo = max(lo, row - p.window), hi = min(hi, row + p.window + 1);
         };
-        // A unit's outputs, read once the next one's first tile is handed over: dq, or dk by one warp of the two and dv by
-        // the other.  They leave as copies of 32 rows (row by row from the threads, a warp's store touches 32 lines: 1024
+        // A unit's outputs, read once the next one's first tile is handed over: dq, half by
+        // each warp of the two, or dk by one and dv by the other.  They leave as copies of 32 rows (row by row from the threads, a warp's store touches 32 lines: 1024
         // to 2048 cycles a unit for the 8 warps).
         auto finish = [&](int ui_p, const int4& it_p, const int2& tb_p) -> bool {
             const int q_len_p = it_p.y & 0xff, row_p = r < q_len_p ? it_p.x + r : -1, head_p = it_p.y >> 16;
@@ -585,48 +605,50 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             if (lane == 0) bulk_wait_read<0>();   // the box's last copy has read it
             __syncwarp();
             tc_fence_after();
-            const bool mine = keys_p || chunk == 0, whole = quad * 32 + 32 <= q_len_p;
-            const float scale = chunk ? 1.f : 0.125f;
+            // where rows are keys this warp's 64 columns of dk or dv, else its 32 of dq: boxes of 32
+            const bool whole = quad * 32 + 32 <= q_len_p;
+            const float scale = keys_p && chunk ? 1.f : 0.125f;
             float z = 0.f;   // not a number where one of the sums is not finite
-            const int x = (keys_p ? (chunk + 1) * p.hidden : 0) + head_p * HD;
+            const int x = (keys_p ? (chunk + 1) * p.hidden : chunk * 32) + head_p * HD;
+            const uint32_t from = lanes + TM_O + (keys_p ? HD : 32) * chunk;
             uint8_t* const box = smem + OFF_OUT + (warp - FIRST_WORKER) * 4096;
             bf16* const dst = p.dqkv + (size_t)max(row_p, 0) * 3 * p.hidden + x;
-            if (mine) {
+            const int boxes = keys_p ? 2 : 1;
 #pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
-                    float o[32];
-                    tmem_ld32(lanes + TM_O + chunk * HD + 32 * h, o);
+            for (int h = 0; h < boxes; ++h) {
+                float o[32];
+                tmem_ld32(from + 32 * h, o);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t q[4];
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t q[4];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float u = o[8 * c + 2 * j] * scale, v = o[8 * c + 2 * j + 1] * scale;
-                            z = fmaf(u, 0.f, fmaf(v, 0.f, z));
-                            q[j] = pack_bf16(u, v);
-                        }
-                        const uint4 piece = make_uint4(q[0], q[1], q[2], q[3]);
-                        if (whole) *reinterpret_cast<uint4*>(box + lane * 128 + (((4 * h + c) ^ (lane & 7)) << 4)) = piece;
-                        else if (row_p >= 0) *reinterpret_cast<uint4*>(dst + 32 * h + 8 * c) = piece;
+                    for (int j = 0; j < 4; ++j) {
+                        const float u = o[8 * c + 2 * j] * scale, v = o[8 * c + 2 * j + 1] * scale;
+                        z = fmaf(u, 0.f, fmaf(v, 0.f, z));
+                        q[j] = pack_bf16(u, v);
                     }
+                    const uint4 piece = make_uint4(q[0], q[1], q[2], q[3]);
+                    // rows of 64 bytes, swizzled: 16-byte piece c of row r at piece c ^ (r / 2 & 3)
+                    if (whole) *reinterpret_cast<uint4*>(box + h * 2048 + lane * 64 + ((c ^ (lane >> 1 & 3)) << 4)) = piece;
+                    else if (row_p >= 0) *reinterpret_cast<uint4*>(dst + 32 * h + 8 * c) = piece;
                 }
             }
             tc_fence_before();
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_OE));
-            if (!mine) return true;
-            if (whole && lane == 0) {
-                tma_store_2d(&tm_out, smem_u32(box), x, it_p.x + quad * 32);
-                bulk_commit();
+            if (lane == 0) {
+                mbar_arrive(bar(B_OE));
+                if (whole) {
+                    for (int h = 0; h < boxes; ++h) tma_store_2d(&tm_out, smem_u32(box + h * 2048), x + 32 * h, it_p.x + quad * 32);
+                    bulk_commit();
+                }
             }
             // rows of one text that all see the same columns meet no others' values
             const bool alone = p.window < 0 && tb_p.x == it_p.z && tb_p.y == it_p.w;
             unsigned again = __ballot_sync(0xffffffffu, row_p >= 0 && !alone && !(z == 0.f));
-            if (again) {
-                if (lane == 0) bulk_wait_all();
-                __syncwarp();
-            }
+            if (!again) return true;
+            if (lane == 0) bulk_wait_all();
+            __syncwarp();
             int lo_p, hi_p;
             seen(it_p, tb_p, lo_p, hi_p);
             while (again) {
@@ -663,12 +685,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             int vis_lo, vis_hi;
             seen(it, tb, vis_lo, vis_hi);
             const uint64_t nl2 = f2_pack(nl, nl), nd2 = f2_pack(nd, nd);
-            // columns that any row of the warp sees, and that all see.  A row behind the item's sees them all: what it adds
-            // up is not stored, and what it multiplies is 0 behind the last column
+            // Columns that any row of the warp sees, and that all see: a row's first and last column never lie before those
+            // of the row before.  A row behind the item's sees them all: what it adds up is not stored, and what it
+            // multiplies is 0 behind the last column.
+            const int rows = min(32, q_len - quad * 32);
+            const int any_lo = rows > 0 ? __shfl_sync(0xffffffffu, vis_lo, 0) : INT_MAX;
+            const int all_hi = __shfl_sync(0xffffffffu, vis_hi, 0);
+            const int all_lo = __shfl_sync(0xffffffffu, vis_lo, max(rows, 1) - 1);
+            const int any_hi = rows > 0 ? __shfl_sync(0xffffffffu, vis_hi, max(rows, 1) - 1) : INT_MIN;
             if (r >= q_len) vis_lo = INT_MIN / 2, vis_hi = INT_MAX / 2;
-            const int any_lo = __reduce_min_sync(0xffffffffu, r < q_len ? vis_lo : INT_MAX);
-            const int any_hi = __reduce_max_sync(0xffffffffu, r < q_len ? vis_hi : INT_MIN);
-            const int all_lo = __reduce_max_sync(0xffffffffu, vis_lo), all_hi = __reduce_min_sync(0xffffffffu, vis_hi);
             // (a loop for each kind: one with both kinds' steps in branches takes 239 registers)
             auto tiles = [&](auto by_key, int kt, int end) {
                 constexpr bool KEYS = decltype(by_key)::value;
@@ -723,13 +748,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                                     if (KEYS) pk[word(j) + 8] = pack_bf16(e0, e1);
                                 }
                                 if (c < all_lo || c + 32 > all_hi) {   // columns that the row does not see, bit by bit: they may be NaN
-                                    const uint32_t from = (uint32_t)(vis_lo - c), many = (uint32_t)(vis_hi - vis_lo);
+                                    // bit k: column c + k is seen.  Four bits come to the tops of four bytes by a product (no two of
+                                    // its terms meet), and a byte's top bit fills half a word
+                                    const int from = min(max(vis_lo - c, 0), 32), to = min(max(vis_hi - c, 0), 32);
+                                    const uint32_t seen_bits = ones_below(to) & ~ones_below(from);
 #pragma unroll
-                                    for (int j = 0; j < 16; ++j) {
-                                        const uint32_t m = ((uint32_t)(2 * j) - from < many ? 0xffffu : 0u) |
-                                                           ((uint32_t)(2 * j + 1) - from < many ? 0xffff0000u : 0u);
-                                        pk[word(j)] &= m;
-                                        if (KEYS) pk[word(j) + 8] &= m;
+                                    for (int j = 0; j < 16; j += 2) {
+                                        const uint32_t tops = (seen_bits >> (2 * j) & 15u) * 0x10204080u;
+                                        const uint32_t m0 = byte_signs<0x9988>(tops), m1 = byte_signs<0xbbaa>(tops);
+                                        pk[word(j)] &= m0, pk[word(j + 1)] &= m1;
+                                        if (KEYS) pk[word(j) + 8] &= m0, pk[word(j + 1) + 8] &= m1;
                                     }
                                 }
                             }
@@ -841,7 +869,7 @@ cudaError_t launch_attention_train_backward(const void* qkv, const int32_t* cu, 
     CUtensorMap tm_qkv, tm_do, tm_out;
     if ((e = make_tensor_map_2d(&tm_qkv, false, qkv, T, 3 * (uint64_t)H, 3 * (uint64_t)H, TILE, HD)) != cudaSuccess) return e;
     if ((e = make_tensor_map_2d(&tm_do, false, d_o, T, H, H, TILE, HD)) != cudaSuccess) return e;
-    if ((e = make_tensor_map_2d(&tm_out, false, dqkv, T, 3 * (uint64_t)H, 3 * (uint64_t)H, 32, HD)) != cudaSuccess) return e;
+    if ((e = make_tensor_map_2d_64(&tm_out, dqkv, T, 3 * (uint64_t)H, 3 * (uint64_t)H, 32)) != cudaSuccess) return e;
     if ((e = launch_plan(a, s)) != cudaSuccess) return e;
     BwdParams p{a.plan, T, n_heads, H, window, (const bf16*)qkv, (const bf16*)d_o, (bf16*)dqkv, status};
     const int grid = (int)std::min<long long>(num_sms, 2LL * max_items * n_heads);
