@@ -45,6 +45,7 @@
 //                   unit's O / l is read and stored as bf16 after the next
 //                   unit's first P hand-off.
 // Pipeline counters run across units; every wait is bounded.
+#include "gemm_tc.cuh"
 #include "train_internal.cuh"
 
 #include <cuda.h>
@@ -77,7 +78,9 @@ constexpr int B_QF = 0, B_QE = 2, B_KVF = 4, B_KVE = B_KVF + KV_STAGES, B_SF = B
               B_PF = B_SF + SP_BUFS, B_OE = B_PF + SP_BUFS, B_DONE = B_OE + 2, N_BARS = B_DONE + 1;
 constexpr uint32_t OFF_RED = OFF_BAR + N_BARS * 8 + 16;       // row-maximum exchange: [2 tiles][2 halves][128 rows]
 constexpr uint32_t OFF_REDL = OFF_RED + 2 * 2 * 128 * 4;       // row-sum exchange: [2 units][2 halves][128 rows]
-constexpr uint32_t SMEM_TOTAL = OFF_REDL + 2 * 2 * 128 * 4 + 1024;
+constexpr uint32_t OFF_OUT = (OFF_REDL + 2 * 2 * 128 * 4 + 1023) / 1024 * 1024;   // a 2 KB box per softmax warp: 32 rows of 64 bytes
+constexpr uint32_t SMEM_TOTAL = OFF_OUT + 8 * 2048 + 1024;
+static_assert(SMEM_TOTAL <= 227 * 1024, "shared memory");
 constexpr uint32_t TMEM_COLS = 512;                 // S/P: 3 x 128 columns (by tile), O: 2 x 64 (by unit)
 constexpr uint32_t TM_S = 0, TM_O = SP_BUFS * BKV;
 
@@ -152,6 +155,33 @@ __device__ __forceinline__ void zero_pack(uint32_t* pk) {
     for (int c = B / 2; c < E / 2; ++c) pk[c] = 0u;
 }
 
+// A CTA's units in turn, i0 .. i1 - 1; none behind the last.  TRAIN: from unit to unit
+// (attn_unit) the steps are two in turn, so one division each does for all.
+template <bool TRAIN>
+struct Slots {
+    const AttnParams& p;
+    int i, i1, n = 0, item = 0, head = 0, step_item[2], step_head[2];
+    __device__ __forceinline__ Slots(const AttnParams& p_, int i0, int i1_) : p(p_), i(i0), i1(i1_) {
+        if constexpr (TRAIN) {
+            const int c = blockIdx.x, G = gridDim.x, heads = p.n_heads;
+            item = c / heads, head = c - item * heads;
+            step_item[0] = (2 * (G - c) - 1) / heads, step_head[0] = 2 * (G - c) - 1 - step_item[0] * heads;
+            step_item[1] = (2 * c + 1) / heads, step_head[1] = 2 * c + 1 - step_item[1] * heads;
+        }
+    }
+    __device__ __forceinline__ int4 next() {
+        if (i >= i1) return make_int4(0, 0, 0, 0);
+        if constexpr (!TRAIN) return p.slots[i++];
+        int4 it = p.slots[item];
+        it.y |= head << 16;
+        item += i & 1 ? step_item[1] : step_item[0];
+        head += i & 1 ? step_head[1] : step_head[0];
+        if (head >= p.n_heads) head -= p.n_heads, ++item;
+        ++i;
+        return it;
+    }
+};
+
 // The output of one row whose products met NaN or infinities of keys that it does not
 // see (their probability is 0, but 0 x NaN is NaN): the row's own keys [lo, hi) again,
 // outside the tensor cores, by a whole warp.  Returns o[half * 32 + lane].
@@ -181,7 +211,8 @@ __device__ __noinline__ float attn_row_again(const AttnParams& p, int row, int h
 // items whose rows see different keys, is computed again from its own.
 template <bool WINDOW, bool TRAIN>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
-    attn_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ AttnParams p) {
+    attn_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUtensorMap tm_o,
+                   const __grid_constant__ AttnParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
@@ -220,24 +251,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     pdl_wait();
     pdl_trigger();
 
-    // this CTA's units are slot(i0) .. slot(i1 - 1)
-    int i0, i1;
+    // this CTA's units
+    int i0 = 0, i1;
     if constexpr (TRAIN) {
-        i0 = 0;
         i1 = attn_units_of(*p.n_items * p.n_heads, blockIdx.x, gridDim.x);
     } else {
         i0 = p.slot_off[blockIdx.x], i1 = p.slot_off[blockIdx.x + 1];
     }
-    auto slot = [&](int i) -> int4 {
-        if constexpr (TRAIN) {
-            const int u = attn_unit(i, blockIdx.x, gridDim.x), item = u / p.n_heads;
-            int4 it = p.slots[item];
-            it.y |= (u - item * p.n_heads) << 16;
-            return it;
-        } else {
-            return p.slots[i];
-        }
-    };
 
     if (warp == 0) {
         // ---------------- TMA producer ----------------
@@ -247,10 +267,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             uint32_t g = 0;   // KV tiles issued
             int ui = 0;
             bool ok = true;
-            int4 it_next = i0 < i1 ? slot(i0) : make_int4(0, 0, 0, 0);   // units are read one ahead
+            Slots<TRAIN> slots(p, i0, i1);
+            int4 it_next = slots.next();   // units are read one ahead
             for (int i = i0; i < i1 && ok; ++i, ++ui) {
                 const int4 it = it_next;
-                if (i + 1 < i1) it_next = slot(i + 1);
+                it_next = slots.next();
                 const int head = it.y >> 16;
                 const int nk = n_kv_tiles(it);
                 const int qb = ui & 1;
@@ -320,10 +341,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         uint32_t t = 0;          // tiles whose S has been issued (global)
         bool ok = true;
         int ui = 0;
-        int4 it_next = i0 < i1 ? slot(i0) : make_int4(0, 0, 0, 0);
+        Slots<TRAIN> slots(p, i0, i1);
+        int4 it_next = slots.next();
         for (int i = i0; i < i1 && ok; ++i, ++ui) {
             const int nk = n_kv_tiles(it_next);
-            if (i + 1 < i1) it_next = slot(i + 1);
+            it_next = slots.next();
             const int qb = ui & 1;
             if (!wait(B_QF + qb, (ui >> 1) & 1)) break;
             const uint64_t qdesc = q0desc + qb * TILE_DESC;
@@ -409,9 +431,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         float l_p = 0.f, l_tot_p = 0.f;
         uint32_t t_p = 0;
         int ub_p = 0;
-        bf16* dst_p = nullptr;
-        float m_p = 0.f;                      // TRAIN: the unit's reference maximum, row, and the keys it sees
-        int row_p = 0, head_p = 0, lo_p = 0, hi_p = 0;
+        bool row_is_p = false;                // the unit has the row
+        int row_p = 0, head_p = 0, q_len_p = 0;
+        float m_p = 0.f;                      // TRAIN: the unit's reference maximum, and the keys the row sees
+        int lo_p = 0, hi_p = 0;
+        uint8_t* const box = smem + OFF_OUT + (warp - 2) * 2048;
         auto finalize = [&](bool exchanged) -> bool {
             if (!pv_done(t_p)) return false;
             tc_fence_after();
@@ -427,14 +451,39 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const float inv = 1.0f / l_tot_p;
 #pragma unroll
             for (int d = 0; d < 32; ++d) o[d] *= inv;
-            if (dst_p) store_bf16x32(dst_p, o);
+            // 32 whole rows leave as one bulk copy (row by row from the threads, each store touches 32 lines)
+            if (quad * 32 + 32 <= q_len_p) {
+                if (lane == 0) bulk_wait_read<0>();   // the box's last copy has read it
+                __syncwarp();
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {         // 64-byte swizzle: 16-byte piece c of row r at piece c ^ (r / 2 & 3)
+                    uint4 q;
+                    q.x = pack_bf16(o[8 * c + 0], o[8 * c + 1]);
+                    q.y = pack_bf16(o[8 * c + 2], o[8 * c + 3]);
+                    q.z = pack_bf16(o[8 * c + 4], o[8 * c + 5]);
+                    q.w = pack_bf16(o[8 * c + 6], o[8 * c + 7]);
+                    *reinterpret_cast<uint4*>(box + lane * 64 + ((c ^ (lane >> 1 & 3)) << 4)) = q;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_2d(&tm_o, smem_u32(box), head_p * HD + half * 32, row_p);
+                    bulk_commit();
+                }
+            } else if (row_is_p) {
+                store_bf16x32(p.o + (size_t)row_p * p.hidden + head_p * HD + half * 32, o);
+            }
             if constexpr (TRAIN) {
                 const float lse2 = m_p + log2f(l_tot_p);
-                if (dst_p && half == 0) p.lse[(size_t)head_p * p.T + row_p] = lse2 * 0.69314718055994531f;
+                if (row_is_p && half == 0) p.lse[(size_t)head_p * p.T + row_p] = lse2 * 0.69314718055994531f;
                 float z = 0.f;                // not a number where one of the row's outputs is not finite
 #pragma unroll
                 for (int d = 0; d < 32; ++d) z = fmaf(o[d], 0.f, z);
-                unsigned again = __ballot_sync(0xffffffffu, dst_p != nullptr && lo_p < hi_p && !(z == 0.f));
+                unsigned again = __ballot_sync(0xffffffffu, row_is_p && lo_p < hi_p && !(z == 0.f));
+                if (again) {
+                    if (lane == 0) bulk_wait_all();
+                    __syncwarp();
+                }
                 while (again) {
                     const int l = __ffs(again) - 1;
                     again &= again - 1;
@@ -455,15 +504,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             return r < (x.y & 0xffff) ? p.row_tb[x.x + r] : make_int2(0, 0);
         };
         int ui = 0;
-        int4 it_next = i0 < i1 ? slot(i0) : make_int4(0, 0, 0, 0);
-        int4 it_next2 = i0 + 1 < i1 ? slot(i0 + 1) : make_int4(0, 0, 0, 0);
+        Slots<TRAIN> slots(p, i0, i1);
+        int4 it_next = slots.next(), it_next2 = slots.next();
         int2 tb_next = row_bounds(it_next);
         for (int i = i0; i < i1 && ok; ++i, ++ui) {
             const int4 it = it_next;
             const int2 tb = tb_next;
             it_next = it_next2;
             if (i + 1 < i1) tb_next = row_bounds(it_next);
-            if (i + 2 < i1) it_next2 = slot(i + 2);
+            it_next2 = slots.next();
             const int head = it.y >> 16;
             const int q_start = it.x, q_len = it.y & 0xffff, k_lo = it.z, k_hi = it.w;
             const int nk = n_kv_tiles(it);
@@ -623,10 +672,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             l_p = l;
             t_p = t - 1;
             ub_p = ub;
-            dst_p = r < q_len ? p.o + (size_t)qg * p.hidden + head * HD + half * 32 : nullptr;
+            row_is_p = r < q_len;
+            row_p = qg, head_p = head, q_len_p = q_len;
             if constexpr (TRAIN) {
                 m_p = m_ref;
-                row_p = qg, head_p = head;
                 // rows of one text that all see the same keys meet no others' values
                 const bool alone = !WINDOW && tb.x == k_lo && tb.y == k_hi;
                 lo_p = alone ? 0 : vis_lo, hi_p = alone ? 0 : vis_hi;
@@ -639,6 +688,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // next sees the abort flag at its next, bounded, wait: every path
         // between two pair barriers passes one).  Unawaited, it is harmless.
         if (!ok) asm volatile("bar.arrive %0, 64;" ::"r"(pair_bar) : "memory");
+        if (lane == 0) bulk_wait_all();   // stores complete before the CTA exits
     }
 
     tc_fence_before();
@@ -672,7 +722,7 @@ void init_once() {
 namespace {
 
 // Tensor map and attributes of a launch on the current device.
-cudaError_t prepare_launch(const void* qkv, int T, int H, const void* o, CUtensorMap* tm, int* num_sms) {
+cudaError_t prepare_launch(const void* qkv, int T, int H, const void* o, CUtensorMap* tm, CUtensorMap* tm_o, int* num_sms) {
     std::call_once(g_once, init_once);
     if (g_init_err != cudaSuccess) return g_init_err;
     if ((reinterpret_cast<uintptr_t>(qkv) & 15) || (reinterpret_cast<uintptr_t>(o) & 15)) return cudaErrorInvalidValue;
@@ -684,8 +734,10 @@ cudaError_t prepare_launch(const void* qkv, int T, int H, const void* o, CUtenso
                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
+    cudaError_t e = make_tensor_map_2d_64(tm_o, o, T, H, H, 32);
+    if (e != cudaSuccess) return e;
     int dev = 0;
-    cudaError_t e = tee_current_device(&dev, num_sms);
+    e = tee_current_device(&dev, num_sms);
     if (e != cudaSuccess) return e;
     std::lock_guard<std::mutex> lock(g_attr_mu);
     if (!g_attr_set[dev]) {
@@ -707,14 +759,14 @@ cudaError_t launch_attention_tc(const void* qkv, int T, int H, int n_heads, cons
     if (grid == 0 || T == 0) return cudaSuccess;
     if (H != n_heads * HD) return cudaErrorInvalidValue;
     if (!row_tb || !d_slots || !d_slot_off || grid < 0) return cudaErrorInvalidValue;
-    CUtensorMap tm;
+    CUtensorMap tm, tm_o;
     int num_sms = 0;
-    cudaError_t e = prepare_launch(qkv, T, H, o, &tm, &num_sms);
+    cudaError_t e = prepare_launch(qkv, T, H, o, &tm, &tm_o, &num_sms);
     if (e != cudaSuccess) return e;
     AttnParams p{d_slots, d_slot_off, row_tb, H, window, 1.4426950408889634f / 8.0f, (bf16*)o, status, nullptr, 0, 0, nullptr,
                  nullptr};
-    e = is_global ? launch_pdl(attn_tc_kernel<false, false>, dim3(grid), dim3(NUM_THREADS), SMEM_TOTAL, s, tm, p)
-                  : launch_pdl(attn_tc_kernel<true, false>, dim3(grid), dim3(NUM_THREADS), SMEM_TOTAL, s, tm, p);
+    e = is_global ? launch_pdl(attn_tc_kernel<false, false>, dim3(grid), dim3(NUM_THREADS), SMEM_TOTAL, s, tm, tm_o, p)
+                  : launch_pdl(attn_tc_kernel<true, false>, dim3(grid), dim3(NUM_THREADS), SMEM_TOTAL, s, tm, tm_o, p);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }
@@ -722,13 +774,13 @@ cudaError_t launch_attention_tc(const void* qkv, int T, int H, int n_heads, cons
 cudaError_t launch_attention_train_tc(const void* qkv, int T, int n_heads, int window, const AttnPlan& plan, int max_items,
                                       void* o, float* lse, unsigned int* status, cudaStream_t s) {
     const int H = n_heads * HD;
-    CUtensorMap tm;
+    CUtensorMap tm, tm_o;
     int num_sms = 0;
-    cudaError_t e = prepare_launch(qkv, T, H, o, &tm, &num_sms);
+    cudaError_t e = prepare_launch(qkv, T, H, o, &tm, &tm_o, &num_sms);
     if (e != cudaSuccess) return e;
     const int grid = (int)std::min<long long>(num_sms, (long long)max_items * n_heads);
     AttnParams p{plan.items, nullptr, plan.row_tb, H, window, 1.4426950408889634f / 8.0f, (bf16*)o, status,
                  plan.n_items, n_heads, T, lse, (const bf16*)qkv};
-    return window < 0 ? launch_pdl(attn_tc_kernel<false, true>, dim3(grid), dim3(NUM_THREADS), SMEM_TOTAL, s, tm, p)
-                      : launch_pdl(attn_tc_kernel<true, true>, dim3(grid), dim3(NUM_THREADS), SMEM_TOTAL, s, tm, p);
+    return window < 0 ? launch_pdl(attn_tc_kernel<false, true>, dim3(grid), dim3(NUM_THREADS), SMEM_TOTAL, s, tm, tm_o, p)
+                      : launch_pdl(attn_tc_kernel<true, true>, dim3(grid), dim3(NUM_THREADS), SMEM_TOTAL, s, tm, tm_o, p);
 }
