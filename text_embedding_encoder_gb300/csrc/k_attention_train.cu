@@ -71,7 +71,7 @@ __device__ __forceinline__ int first_above(const int32_t* cu, int n, int v) {
 // found by doubling the steps (log2 of the number of texts).
 // Items of window layers: 128 rows of the packed batch, whatever texts they are of.
 __global__ void __launch_bounds__(PLAN_THREADS) attn_plan_kernel(const PlanArgs a) {
-    __shared__ int lists[3 * (PLAN_SHARED_TEXTS + 1)];
+    __shared__ int lists[3 * (PLAN_SHARED_TEXTS + 1)], offsets[PLAN_SHARED_TEXTS + 1];
     __shared__ int bucket[PLAN_BUCKETS + 1];
     __shared__ int bad;
     __shared__ float stage[PLAN_HEADS][PLAN_ROWS + 1];
@@ -79,12 +79,20 @@ __global__ void __launch_bounds__(PLAN_THREADS) attn_plan_kernel(const PlanArgs 
     // blocks that are still to come (window layer of 32768 tokens, backward: 200 us instead of 152).
     pdl_wait();
     const int n = a.n_texts, tid = threadIdx.x;
+    // (searched out of shared memory where they fit: a search is a chain of loads)
+    const bool fits = n <= PLAN_SHARED_TEXTS;
+    const int32_t* cu = a.cu;
+    if (fits) {
+        for (int j = tid; j <= n; j += PLAN_THREADS) offsets[j] = a.cu[j];
+        __syncthreads();
+        cu = offsets;
+    }
     if (blockIdx.x > 0) {
         const int row0 = (blockIdx.x - 1) * PLAN_ROWS;
         if (tid < PLAN_ROWS && row0 + tid < a.T) {
-            const int t = row0 + tid, j = first_above(a.cu, n, t);
+            const int t = row0 + tid, j = first_above(cu, n, t);
             int2 tb = make_int2(0, 0);
-            if (j >= 1 && j <= n) tb = make_int2(max(a.cu[j - 1], 0), min(a.cu[j], a.T));
+            if (j >= 1 && j <= n) tb = make_int2(max(cu[j - 1], 0), min(cu[j], a.T));
             a.plan.row_tb[t] = tb;
         }
         if (!a.o) return;
@@ -126,7 +134,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) attn_plan_kernel(const PlanArgs 
     __syncthreads();
     int wrong = 0;
     for (int j = tid; j < n; j += PLAN_THREADS) {
-        const int c0 = a.cu[j], c1 = a.cu[j + 1];
+        const int c0 = cu[j], c1 = cu[j + 1];
         wrong |= c0 < 0 || c1 < c0 || c1 > a.T || c1 - c0 > TEE_ATTN_MAX_TEXT || (j == 0 && c0 != 0);
     }
     if (wrong) bad = 1;
@@ -138,27 +146,26 @@ __global__ void __launch_bounds__(PLAN_THREADS) attn_plan_kernel(const PlanArgs 
         }
         return;
     }
-    const int end = a.cu[n];
+    const int end = cu[n];
     if (a.window >= 0) {
         const int tiles = (end + TILE - 1) / TILE;
         for (int i = tid; i < tiles; i += PLAN_THREADS) {
             const int q0 = i * TILE, ql = min(TILE, end - q0);
-            const int j0 = first_above(a.cu, n, q0), j1 = first_above(a.cu, n, q0 + ql - 1);   // ends of the first and last row's texts
-            a.plan.items[i] = make_int4(q0, ql, max(a.cu[j0 - 1], q0 - a.window),
-                                        (int)min((long long)a.cu[j1], (long long)q0 + ql + a.window));
+            const int j0 = first_above(cu, n, q0), j1 = first_above(cu, n, q0 + ql - 1);   // ends of the first and last row's texts
+            a.plan.items[i] = make_int4(q0, ql, max(cu[j0 - 1], q0 - a.window),
+                                        (int)min((long long)cu[j1], (long long)q0 + ql + a.window));
         }
         if (tid == 0) *a.plan.n_items = tiles;
         return;
     }
-    const bool fits = n <= PLAN_SHARED_TEXTS;
     int* from = fits ? lists : a.plan.scratch;
     int* to = from + n + 1;
     int* mark = to + n + 1;
     for (int j = tid; j <= n; j += PLAN_THREADS) {
         int e = n;
         if (j < n) {
-            const int c = a.cu[j];
-            e = a.cu[j + 1] - c > TILE ? j + 1 : first_above(a.cu, n, c + TILE) - 1;
+            const int c = cu[j];
+            e = cu[j + 1] - c > TILE ? j + 1 : first_above(cu, n, c + TILE) - 1;
         }
         from[j] = e;
         mark[j] = j == 0;
@@ -177,12 +184,12 @@ __global__ void __launch_bounds__(PLAN_THREADS) attn_plan_kernel(const PlanArgs 
     // a start's items and their keys in tiles of 128
     auto start = [&](int j, int& tiles, int& c0, int& c1) {
         if (!mark[j]) return 0;
-        c0 = a.cu[j], c1 = a.cu[j + 1];
+        c0 = cu[j], c1 = cu[j + 1];
         if (c1 - c0 > TILE) {
             tiles = (c1 - c0 + TILE - 1) / TILE;
             return tiles;
         }
-        c1 = a.cu[first_above(a.cu, n, c0 + TILE) - 1];
+        c1 = cu[first_above(cu, n, c0 + TILE) - 1];
         tiles = 1;
         return c1 > c0 ? 1 : 0;
     };
