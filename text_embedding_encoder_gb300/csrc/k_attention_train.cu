@@ -36,7 +36,7 @@ constexpr int TILE = 128;
 // ---------------------------------------------------------------------------
 
 constexpr int PLAN_THREADS = 512;
-constexpr int PLAN_ROWS = 32;                 // rows of a row block
+constexpr int PLAN_ROWS = 16;                 // rows of a row block
 constexpr int PLAN_HEADS = 32;                // heads staged at once
 constexpr int PLAN_SHARED_TEXTS = 2048;       // texts whose lists fit shared memory
 constexpr int PLAN_BUCKETS = TEE_ATTN_MAX_TEXT / TILE + 1;
@@ -283,14 +283,14 @@ struct BwdParams {
 };
 
 // A CTA's units in turn, each read while the one before is worked on: {q_start, q_len |
-// keys << 8 | head << 16, k_lo, k_hi}.  First the items' rows as keys, the longer kind, for
-// every head, then as queries.  From unit to unit (attn_unit) the steps are two in turn,
-// so one division each does for all.
+// keys << 8 | head << 16, k_lo, k_hi}.  An item's rows as keys, the longer kind, for every
+// head, then as queries, which finds them in L2.  From unit to unit (attn_unit) the steps
+// are two in turn, so one division each does for all.
 struct UnitStream {
     const BwdParams& p;
-    int n_items, n, i = 0, item, head, step_item[2], step_head[2];
+    int n, i = 0, item, head, step_item[2], step_head[2];   // (of `item` there are two for each, by kind)
     int4 ahead;
-    __device__ __forceinline__ UnitStream(const BwdParams& p_, int n_items_, int n_) : p(p_), n_items(n_items_), n(n_) {
+    __device__ __forceinline__ UnitStream(const BwdParams& p_, int n_) : p(p_), n(n_) {
         const int c = blockIdx.x, G = gridDim.x, heads = p.n_heads;
         item = c / heads, head = c - item * heads;
         step_item[0] = (2 * (G - c) - 1) / heads, step_head[0] = 2 * (G - c) - 1 - step_item[0] * heads;
@@ -300,9 +300,8 @@ struct UnitStream {
     __device__ __forceinline__ void read() {
         ahead = make_int4(0, 0, 0, 0);
         if (i >= n) return;
-        const bool keys = item < n_items;
-        ahead = p.plan.items[keys ? item : item - n_items];
-        ahead.y |= (keys ? 1 : 0) << 8 | head << 16;
+        ahead = p.plan.items[item >> 1];
+        ahead.y |= (~item & 1) << 8 | head << 16;
     }
     __device__ __forceinline__ int4 next() {
         const int4 it = ahead;
@@ -422,7 +421,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     pdl_wait();
     pdl_trigger();
 
-    const int n_items = *p.plan.n_items, n_units = attn_units_of(n_items * 2 * p.n_heads, blockIdx.x, gridDim.x);
+    const int n_units = attn_units_of(*p.plan.n_items * 2 * p.n_heads, blockIdx.x, gridDim.x);
     // a whole warp's wait: true for all lanes, or false for all
     auto warp_wait = [&](int b, uint32_t parity) -> bool {
         return __all_sync(0xffffffffu, mbar_try_wait(bar(b), parity)) || warp_wait_longer(bar(b), parity, abort_flag);
@@ -433,7 +432,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         uint32_t t = 0;
         int ui = 0;
         bool ok = true;
-        UnitStream units(p, n_items, n_units);
+        UnitStream units(p, n_units);
         float v[2][4];   // of the tile to come
         auto statistics = [&](const int4& it, int kt) {
             if (!(it.y >> 8 & 1)) return;
@@ -512,7 +511,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const uint64_t ones = ext_desc(sbase + OFF_ONES + (is_s ? 0 : EXT_BYTES)), ext0 = ext_desc(sbase + OFF_EXT);
         uint32_t t = 0;
         bool ok = true;
-        UnitStream units(p, n_items, n_units);
+        UnitStream units(p, n_units);
         for (int ui = 0; ui < n_units && ok; ++ui) {
             const int4 it = units.next();
             const int nk = unit_tiles(it), rb = ui & 1;
@@ -550,7 +549,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const uint64_t cols0 = sw128_desc_mn(sbase + OFF_COLS);
         uint32_t t = 0;
         bool ok = true;
-        UnitStream units(p, n_items, n_units);
+        UnitStream units(p, n_units);
         for (int ui = 0; ui < n_units && ok; ++ui) {
             const int4 it = units.next();
             const int nk = unit_tiles(it);
@@ -669,7 +668,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         };
 
         // a unit's rows' texts and statistics are read while the unit before is worked on
-        UnitStream units(p, n_items, n_units);
+        UnitStream units(p, n_units);
         int4 it = make_int4(0, 0, 0, 0), it_next = units.next();
         int2 tb = make_int2(0, 0), tb_next = text_of(it_next);
         float nl_next = 0.f, nd_next = 0.f;
