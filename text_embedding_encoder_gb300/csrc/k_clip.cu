@@ -3,8 +3,9 @@
 //
 // Bound by memory: the norm has to be known before the first element is scaled, so the
 // gradients are read twice and written once.  The second pass goes through them from
-// the end, where the first left them in L2.  Measured: 151 tensors of the 310m
-// encoder, 315 M elements bf16: 315 us for 1.89 GB.
+// the end, where the first left them in L2.  Measured, 151 tensors of the 310m encoder,
+// 315 M elements bf16, 1.89 GB: 299 us, 6.3 TB/s (four 16-byte loads a thread together;
+// two 314, eight 308; loads and stores marked for eviction in the second pass 308).
 #include "train_internal.cuh"
 
 #include <float.h>
@@ -14,10 +15,10 @@
 namespace {
 
 constexpr int THREADS = 256;
-constexpr int BLOCKS_PER_SM = 4;
-// Elements of a chunk, which lies in one tensor: the largest, or fewer where the blocks
-// would have less than one each (3.0 M elements: 19 us instead of 22 for the two launches).
-constexpr int MIN_CHUNK = 2048, MAX_CHUNK = 16384;
+constexpr int BLOCKS_PER_SM = 3;
+// Elements of a chunk, which lies in one tensor.  (Smaller ones where the blocks have less
+// than one each: 3.0 M elements 18.8 us for the two launches, 13.4 with these.)
+constexpr int CHUNK = 16384;
 constexpr int AT_ONCE = 4;               // 16-byte loads of a thread on their way together
 constexpr int MAX_TENSORS = 256;         // of one launch
 constexpr int MAX_BLOCKS = 1024;         // of one launch
@@ -31,7 +32,7 @@ struct Tensor {
 };
 struct Table {
     Tensor t[MAX_TENSORS];
-    int n, chunks, chunk;
+    int n, chunks;
 };
 
 // Calls f(tensor, first element, elements) for the block's share of the chunks, a
@@ -55,12 +56,12 @@ __device__ __forceinline__ void for_chunks(const Table& table, bool reverse, F&&
         } else {
             while (i + 1 < table.n && c >= table.t[i + 1].first_chunk) ++i;
         }
-        const long long at = (long long)(c - table.t[i].first_chunk) * table.chunk;
-        f(table.t[i], at, (int)min((long long)table.chunk, table.t[i].count - at));
+        const long long at = (long long)(c - table.t[i].first_chunk) * CHUNK;
+        f(table.t[i], at, (int)min((long long)CHUNK, table.t[i].count - at));
     }
 }
 
-// Squares of a thread's elements of a chunk, summed in fp32 -- at most MAX_CHUNK / THREADS
+// Squares of a thread's elements of a chunk, summed in fp32 -- at most CHUNK / THREADS
 // of them -- and whether any element is not zero.
 struct Squares {
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
@@ -221,14 +222,10 @@ cudaError_t launch_clip_gradients(const void* const* src, const int32_t* types, 
     // the tensors [a, a + MAX_TENSORS); the launch's blocks
     auto fill = [&](int a) {
         table.n = table.chunks = 0;
-        long long total = 0;
-        for (int i = a; i < std::min(n_tensors, a + MAX_TENSORS); ++i) total += counts[i];
-        table.chunk = MAX_CHUNK;
-        while (table.chunk > MIN_CHUNK && total < (long long)table.chunk * num_sms * BLOCKS_PER_SM) table.chunk /= 2;
         for (int i = a; i < std::min(n_tensors, a + MAX_TENSORS); ++i) {
             if (counts[i] == 0) continue;
             table.t[table.n++] = Tensor{src[i], const_cast<void*>(dst[i]), counts[i], table.chunks, types[i] == TEE_BF16};
-            table.chunks += (int)((counts[i] + table.chunk - 1) / table.chunk);
+            table.chunks += (int)((counts[i] + CHUNK - 1) / CHUNK);
         }
         return std::max(1, std::min(std::min(table.chunks, num_sms * BLOCKS_PER_SM), MAX_BLOCKS));
     };
