@@ -199,9 +199,9 @@ void tee_destroy(tee_ctx* ctx);
 /* Kernel classes timed by the profiling hook. */
 #define TEE_K_EMBED      0   /* token-embedding gather + per-token positions    */
 #define TEE_K_LAYERNORM  1   /* both bias-free LayerNorms of every layer         */
-#define TEE_K_GEMM       2   /* the four projections (QKV, out, Wi, Wo_ffn)      */
-#define TEE_K_ATTENTION  3   /* varlen global / windowed attention               */
-#define TEE_K_ELEMENTWISE 4  /* stand-alone RoPE / GeGLU (when not fused)        */
+#define TEE_K_GEMM       2   /* the four projections (QKV, out, Wi, Wo_ffn); the gated half and its gradients (tee_train.h) */
+#define TEE_K_ATTENTION  3   /* varlen global / windowed attention, its gradients */
+#define TEE_K_ELEMENTWISE 4  /* stand-alone RoPE / GeGLU (when not fused); gradient clipping */
 #define TEE_K_POOL       5   /* mean-pool + L2 normalisation                     */
 #define TEE_K_QUANT      6   /* per-row 7-bit activation quantiser (W8A8)        */
 #define TEE_K_LOSS       7   /* softmax cross entropy over the vocabulary (tee_train.h) */

@@ -221,7 +221,8 @@ int tee_plan_attention_schedule(const int32_t* items, int n_items, int n_heads, 
 int tee_plan_gemm(int M, int N, int K, int epi, int num_sms, int* bn, int* pair);
 
 /* Synchronise the context's device status word: TEE_OK, or TEE_EINVAL if a
- * kernel met an out-of-range token id since the last call (the word is then
+ * kernel met an out-of-range token id, or offsets that are none
+ * (tee_op_attention_forward, _backward), since the last call (the word is then
  * cleared), or TEE_ETIMEOUT if a bounded device wait gave up. */
 int tee_device_status(tee_ctx* ctx);
 
