@@ -331,7 +331,6 @@ __device__ __forceinline__ uint32_t byte_signs(uint32_t v) {
     asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(v), "n"(SELECT));
     return r;
 }
-__device__ __forceinline__ uint32_t ones_below(int n) { return n < 32 ? (1u << n) - 1 : 0xffffffffu; }   // 0 <= n <= 32
 __device__ __forceinline__ int unit_tiles(const int4& it) { return (it.w - it.z + TILE - 1) / TILE; }
 
 // A whole warp's wait for what it has not found done; gives up as mbar_wait does.

@@ -261,6 +261,9 @@ __device__ __forceinline__ void tmem_tie64(float (&r)[64]) {
                  : "memory");
 }
 
+// The lowest n bits, 0 <= n <= 32.
+__device__ __forceinline__ uint32_t ones_below(int n) { return n < 32 ? (1u << n) - 1 : 0xffffffffu; }
+
 // The 32-column form of tmem_ld64_issue / tmem_tie64.
 __device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, float (&r)[32]) {
     asm volatile(
