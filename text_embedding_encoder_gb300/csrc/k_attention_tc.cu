@@ -31,7 +31,8 @@
 //                   keeps descriptors in uniform registers: eight P V MMAs
 //                   take 300 cycles so, 575 from one lane's own loop (window
 //                   layer of 32768 tokens 74 -> 65 us, 8 x 8192 tokens 2.34 ->
-//                   1.93 ms);
+//                   1.93 ms); a barrier found done is left by one vote (1.81
+//                   -> 1.79 ms);
 //   warps 2-9       two threads per query row (a warp may read only its
 //                   32-lane TMEM quadrant, so warps w and w+4 share one and
 //                   split the 128 key columns, and the 64 output dimensions,
@@ -325,7 +326,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const uint64_t q0desc = sw128_desc(sbase + OFF_Q), k0desc = sw128_desc(sbase + OFF_K);
         const uint64_t v0desc = sw128_desc_mn(sbase + OFF_V);
         constexpr uint32_t TILE_DESC = TILE_BYTES >> 4;
-        auto wait = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar(b), parity, abort_flag)) != 0; };
+        auto wait = [&](int b, uint32_t parity) {
+            return __all_sync(0xffffffffu, mbar_try_wait(bar(b), parity)) ||
+                   __all_sync(0xffffffffu, mbar_wait(bar(b), parity, abort_flag));
+        };
         // P_tt V_tt accumulated into the unit's TMEM O buffer; the first
         // tile of a unit overwrites it once the softmax warps have read the
         // unit two back out of that buffer
