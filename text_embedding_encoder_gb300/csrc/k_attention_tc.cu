@@ -84,6 +84,7 @@ constexpr uint32_t OFF_BAR = OFF_V + KV_STAGES * TILE_BYTES;
 constexpr int SP_BUFS = 3;   // TMEM S/P buffers: tile t uses buffer t % 3
 constexpr int B_QF = 0, B_QE = 2, B_KVF = 4, B_KVE = B_KVF + KV_STAGES, B_SF = B_KVE + KV_STAGES,
               B_PF = B_SF + SP_BUFS, B_OE = B_PF + SP_BUFS, B_DONE = B_OE + 2, N_BARS = B_DONE + 1;
+// (behind the barriers three words: the tensor memory's address and two flags)
 constexpr uint32_t OFF_RED = OFF_BAR + N_BARS * 8 + 16;       // row-maximum exchange: [2 tiles][2 halves][128 rows]
 constexpr uint32_t OFF_REDL = OFF_RED + 2 * 2 * 128 * 4;       // row-sum exchange: [2 units][2 halves][128 rows]
 constexpr uint32_t OFF_OUT = (OFF_REDL + 2 * 2 * 128 * 4 + 1023) / 1024 * 1024;   // a 2 KB box per softmax warp: 32 rows of 64 bytes
@@ -199,24 +200,87 @@ struct Slots {
     }
 };
 
-// The output of one row whose products met NaN or infinities of keys that it does not
-// see (their probability is 0, but 0 x NaN is NaN): the row's own keys [lo, hi) again,
-// outside the tensor cores, by a whole warp.  Returns o[half * 32 + lane].
-__device__ __noinline__ float attn_row_again(const AttnParams& p, int row, int head, int half, int lo, int hi, float lse2) {
-    const int lane = threadIdx.x & 31;
+// The keys that a row of an item sees, its text being {tb.x, tb.y}: the window inside the
+// text, or on global layers the text (of the item's where short texts share a tile).
+template <bool WINDOW>
+__device__ __forceinline__ void seen_keys(const AttnParams& p, const int4& it, int row, const int2& tb, int& lo, int& hi) {
+    if constexpr (WINDOW) lo = max(tb.x, row - p.window), hi = min(tb.y, row + p.window + 1);
+    else lo = max(it.z, tb.x), hi = min(it.w, tb.y);
+}
+
+// The output of one row again, from its own keys [lo, hi), outside the tensor cores, by a
+// whole warp: four keys side by side, eight lanes to each, the loads of four such steps on
+// their way together.  It ends early where nothing but NaN can come.
+__device__ __noinline__ void attn_row_again(const AttnParams& p, int row, int head, int lo, int hi, float lse2) {
+    constexpr int AT_ONCE = 4;
+    const int lane = threadIdx.x & 31, part = lane >> 3, col = (lane & 7) * 8;
     const size_t stride = 3 * (size_t)p.hidden;
-    const bf16* at = p.qkv + head * HD;
-    const __nv_bfloat162 q = *reinterpret_cast<const __nv_bfloat162*>(at + row * stride + 2 * lane);
-    float o = 0.f;
-    for (int j = lo; j < hi; ++j) {
-        const bf16* kv = at + j * stride;
-        const __nv_bfloat162 k = *reinterpret_cast<const __nv_bfloat162*>(kv + p.hidden + 2 * lane);
-        float s = __low2float(q) * __low2float(k) + __high2float(q) * __high2float(k);
+    const bf16* at = p.qkv + head * HD + col;
+    float q[8], o[8] = {};
+    load_vec(at + row * stride, q);
+    for (int j0 = lo; j0 < hi; j0 += 4 * AT_ONCE) {
+        uint4 k4[AT_ONCE], v4[AT_ONCE];
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-        o += ex2_approx(fmaf(s, p.scale_log2, -lse2)) * __bfloat162float(kv[2 * p.hidden + half * 32 + lane]);
+        for (int u = 0; u < AT_ONCE; ++u) {
+            const bf16* kv = at + min(j0 + 4 * u + part, hi - 1) * stride + p.hidden;
+            k4[u] = *reinterpret_cast<const uint4*>(kv);
+            v4[u] = *reinterpret_cast<const uint4*>(kv + p.hidden);
+        }
+#pragma unroll
+        for (int u = 0; u < AT_ONCE; ++u) {
+            float k[8], v[8], s = 0.f;
+            unpack_bf16x8(k4[u], k);
+            unpack_bf16x8(v4[u], v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s = fmaf(q[i], k[i], s);
+#pragma unroll
+            for (int d = 4; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+            if (j0 + 4 * u + part < hi) {
+                const float e = ex2_approx(fmaf(s, p.scale_log2, -lse2));
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] = fmaf(e, v[i], o[i]);
+            }
+        }
+        if (each_eighth_has(all_nan(o))) break;
     }
-    return o;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        o[i] += __shfl_xor_sync(0xffffffffu, o[i], 8);
+        o[i] += __shfl_xor_sync(0xffffffffu, o[i], 16);
+    }
+    if (part == 0) store_vec(p.o + (size_t)row * p.hidden + head * HD + col, o);
+}
+
+// Rows whose products met NaN or infinities of keys that they do not see (their probability
+// is 0, but 0 x NaN is NaN) are computed again, once all of the CTA's units are done and no
+// role waits for another any more: 131072 keys for each of a tile's rows would come near the
+// bound of the waits.  Every warp goes through a quarter of every few units, a lane to a row:
+// not rows that see all of the item's keys, whose NaN are their own, and not those that
+// cannot have another output: NaN in the log sum (or -infinity, as of scores that are all
+// that), or a value row that is nothing but NaN.
+template <bool WINDOW>
+__device__ __noinline__ void attn_again(const AttnParams& p, int units) {
+    const int lane = threadIdx.x & 31;
+    for (int task = threadIdx.x >> 5; task < 4 * units; task += NUM_THREADS / 32) {
+        const int unit = attn_unit(task >> 2, blockIdx.x, gridDim.x), head = unit % p.n_heads;
+        const int4 it = p.slots[unit / p.n_heads];
+        const int r = (task & 3) * 32 + lane, row = it.x + r;
+        int lo = 0, hi = 0;
+        float lse2 = 0.f;
+        bool mine = r < it.y;
+        if (mine) {
+            seen_keys<WINDOW>(p, it, row, p.row_tb[row], lo, hi);
+            lse2 = p.lse[(size_t)head * p.T + row] * 1.4426950408889634f;
+            mine = (lo > it.z || hi < it.w) && lse2 > -INFINITY;
+        }
+        if (mine) mine = !all_finite(p.o + (size_t)row * p.hidden + head * HD);
+        if (mine) mine = !all_nan(p.qkv + (size_t)row * 3 * p.hidden + 2 * p.hidden + head * HD);
+        for (unsigned again = __ballot_sync(0xffffffffu, mine); again; again &= again - 1) {
+            const int l = __ffs(again) - 1;
+            attn_row_again(p, __shfl_sync(0xffffffffu, row, l), head, __shfl_sync(0xffffffffu, lo, l),
+                           __shfl_sync(0xffffffffu, hi, l), __shfl_sync(0xffffffffu, lse2, l));
+        }
+    }
 }
 
 // WINDOW: the ±window layers (per-row text bounds, 32-column block skipping);
@@ -225,7 +289,7 @@ __device__ __noinline__ float attn_row_again(const AttnParams& p, int row, int h
 // rows' log sums written beside their outputs, and rows that see no trace of what lies
 // outside their text: rows of V behind the item's keys are zeroed in shared memory
 // (they may be anything, also behind the last text), and a row that is not finite, in
-// items whose rows see different keys, is computed again from its own.
+// items whose rows see different keys, is computed again from its own (attn_again).
 template <bool WINDOW, bool TRAIN>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUtensorMap tm_o,
@@ -236,6 +300,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + N_BARS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile int* not_finite = abort_flag + 1;   // TRAIN: some output is not
     auto bar = [&](int i) { return smem_u32(bars + i); };
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -255,7 +320,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             mbar_init(bar(B_KVE + s), 1);
         }
         mbar_init(bar(B_DONE), 1);
-        *abort_flag = 0;
+        *abort_flag = *not_finite = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm)) : "memory");
     }
@@ -453,8 +518,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         int ub_p = 0;
         bool row_is_p = false;                // the unit has the row
         int row_p = 0, head_p = 0, q_len_p = 0;
-        float m_p = 0.f;                      // TRAIN: the unit's reference maximum, and the keys the row sees
-        int lo_p = 0, hi_p = 0;
+        float m_p = 0.f;                      // TRAIN: the unit's reference maximum
         uint8_t* const box = smem + OFF_OUT + (warp - 2) * 2048;
         auto finalize = [&](bool exchanged) -> bool {
             if (!pv_done(t_p)) return false;
@@ -499,20 +563,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 float z = 0.f;                // not a number where one of the row's outputs is not finite
 #pragma unroll
                 for (int d = 0; d < 32; ++d) z = fmaf(o[d], 0.f, z);
-                unsigned again = __ballot_sync(0xffffffffu, row_is_p && lo_p < hi_p && !(z == 0.f));
-                if (again) {
-                    if (lane == 0) bulk_wait_all();
-                    __syncwarp();
-                }
-                while (again) {
-                    const int l = __ffs(again) - 1;
-                    again &= again - 1;
-                    const int row = __shfl_sync(0xffffffffu, row_p, l);
-                    const float v = attn_row_again(p, row, head_p, half, __shfl_sync(0xffffffffu, lo_p, l),
-                                                   __shfl_sync(0xffffffffu, hi_p, l), __shfl_sync(0xffffffffu, lse2, l));
-                    p.o[(size_t)row * p.hidden + head_p * HD + half * 32 + lane] = __float2bfloat16_rn(v);
-                }
-                __syncwarp();
+                if (row_is_p && !(z == 0.f)) *not_finite = 1;
             }
             pend = false;
             return true;
@@ -538,21 +589,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const int nk = n_kv_tiles(it);
             const int qg = q_start + r;
             const int ub = ui & 1;
-            // keys visible to this row: [vis_lo, vis_hi) -- the row's text on
-            // global layers, the window inside the row's own text otherwise
-            // (nothing for window rows past the end of the sequence)
-            int vis_lo = k_lo, vis_hi = k_hi;
-            if constexpr (WINDOW) {
-                if (r < q_len) {
-                    vis_lo = max(tb.x, qg - p.window);
-                    vis_hi = min(tb.y, qg + p.window + 1);
-                } else {
-                    vis_hi = vis_lo;
-                }
-            } else if (r < q_len) {   // a tile shared by short texts: the row's own text
-                vis_lo = max(k_lo, tb.x);
-                vis_hi = min(k_hi, tb.y);
-            }
+            // keys visible to this row: [vis_lo, vis_hi) (rows behind the item's: all,
+            // or nothing on window layers)
+            int vis_lo = k_lo, vis_hi = WINDOW ? k_lo : k_hi;
+            if (r < q_len) seen_keys<WINDOW>(p, it, qg, tb, vis_lo, vis_hi);
             float m_ref = -INFINITY, l = 0.f;
             for (int kt = 0; kt < nk; ++kt, ++t) {
                 const int sb = t % SP_BUFS;
@@ -691,9 +731,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             row_p = qg, head_p = head, q_len_p = q_len;
             if constexpr (TRAIN) {
                 m_p = m_ref;
-                // rows of one text that all see the same keys meet no others' values
-                const bool alone = !WINDOW && tb.x == k_lo && tb.y == k_hi;
-                lo_p = alone ? 0 : vis_lo, hi_p = alone ? 0 : vis_hi;
             }
             pend = true;
         }
@@ -713,6 +750,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         tmem_dealloc<1>(tmem_base, TMEM_COLS);
     }
     if (threadIdx.x == 0 && *abort_flag && p.status) atomicOr(p.status, TEE_STATUS_TIMEOUT);
+    if constexpr (TRAIN) {
+        if (*not_finite && !*abort_flag) attn_again<WINDOW>(p, i1);
+    }
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;

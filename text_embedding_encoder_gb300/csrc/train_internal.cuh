@@ -46,12 +46,14 @@ __device__ __forceinline__ void load_vec(const bf16* p, float (&v)[4]) {
     unpack_bf16x2(q.x, v[0], v[1]);
     unpack_bf16x2(q.y, v[2], v[3]);
 }
-__device__ __forceinline__ void load_vec(const bf16* p, float (&v)[8]) {
-    const uint4 q = *reinterpret_cast<const uint4*>(p);
+__device__ __forceinline__ void unpack_bf16x8(const uint4& q, float (&v)[8]) {
     unpack_bf16x2(q.x, v[0], v[1]);
     unpack_bf16x2(q.y, v[2], v[3]);
     unpack_bf16x2(q.z, v[4], v[5]);
     unpack_bf16x2(q.w, v[6], v[7]);
+}
+__device__ __forceinline__ void load_vec(const bf16* p, float (&v)[8]) {
+    unpack_bf16x8(*reinterpret_cast<const uint4*>(p), v);
 }
 __device__ __forceinline__ void load_vec(const float* p, float (&v)[2]) {
     const float2 a = *reinterpret_cast<const float2*>(p);
@@ -75,6 +77,44 @@ __device__ __forceinline__ void store_vec(bf16* p, const float (&v)[4]) {
 __device__ __forceinline__ void store_vec(bf16* p, const float (&v)[8]) {
     *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                                               pack_bf16x2(v[6], v[7]));
+}
+
+// ---- values that are not finite -------------------------------------------------
+template <int N>
+__device__ __forceinline__ bool all_nan(const float (&v)[N]) {
+    bool all = true;
+#pragma unroll
+    for (int i = 0; i < N; ++i) all &= v[i] != v[i];
+    return all;
+}
+// Whether the 64 elements of a head's row all are NaN, or all are finite.
+__device__ __forceinline__ bool all_nan(const bf16* row) {
+    bool all = true;
+#pragma unroll
+    for (int c = 0; c < 64; c += 8) {
+        float v[8];
+        load_vec(row + c, v);
+        all &= all_nan(v);
+    }
+    return all;
+}
+__device__ __forceinline__ bool all_finite(const bf16* row) {
+    float z = 0.f;
+#pragma unroll
+    for (int c = 0; c < 64; c += 8) {
+        float v[8];
+        load_vec(row + c, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z = fmaf(v[i], 0.f, z);
+    }
+    return z == 0.f;
+}
+// Of sums that a warp holds in four parts, an eighth of them in each of eight lanes: whether
+// `mine` holds for one part at least of each eighth.
+__device__ __forceinline__ bool each_eighth_has(bool mine) {
+    unsigned b = __ballot_sync(0xffffffffu, mine);
+    b |= b >> 16;
+    return ((b | b >> 8) & 0xffu) == 0xffu;
 }
 
 __device__ __forceinline__ float warp_sum_f32(float v) {
