@@ -137,3 +137,56 @@ def test_forward_beside_nan_with_the_widest_window(enc):
         assert abs(float(lse[0, i]) - float(want_lse)) < 2e-5
         assert_within(o[i], want, off)
     assert took < 1e6, took
+
+
+@pytest.mark.parametrize("lens", LENS, ids=["texts", "one", "ones"])
+@pytest.mark.parametrize("window", [-1, 0, 20, 64])
+@pytest.mark.parametrize("what", ["do", "inf do", "k"])
+def test_backward_of_scattered_values(enc, lens, window, what):
+    """Single elements of do, or of k with what the forward pass makes of it: in the gradients that they reach, and no other.
+    An element of do reaches its own dq, dk of the rows that see it, and column c of their dv; one of k makes every row that
+    sees it NaN, and with it the dk and dv of what those see."""
+    heads, T = 2, sum(lens)
+    H = heads * lu.HD
+    qkv, do = inputs(T, heads, 3)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(11)
+    bad = torch.rand(T, H, generator=g, device="cuda") < 0.0003
+    bad[5, 3] = bad[T - 1, 100] = True
+    cu = lu.offsets(lens)
+    clean, clean_do = qkv.clone(), do.clone()
+    o, lse, _ = lu.attention_forward(enc, qkv, cu, heads, window)
+    clean_o, clean_lse = o, lse
+    if what == "k":
+        qkv[:, H:2 * H][bad] = NAN
+        o, lse, _ = lu.attention_forward(enc, qkv, cu, heads, window)
+    else:
+        do[bad] = INF if what == "inf do" else NAN
+    got = lu.attention_backward(enc, qkv, cu, o, lse, do, heads, window)
+    assert enc.device_status() == binding.TEE_OK
+    a = 0
+    for m in lens:
+        b = a + m
+        att = lu.Attention(clean[a:b], heads, window)
+        grads, bounds = att.backward(clean_o[a:b], clean_lse[:, a:b], clean_do[a:b])
+        want = [lu.packed(x) for x in grads]
+        sees = torch.isfinite(att.s[0]).double()
+        by_head = bad[a:b].view(m, heads, lu.HD).any(2)                       # rows with a bad element, for each head
+        reached = sees @ by_head.double() > 0                                 # rows that see one
+        wide = lambda rows: rows.repeat_interleave(lu.HD, dim=1)              # noqa: E731
+        if what == "k":
+            want[0][wide(reached)] = NAN
+            again = wide(sees @ reached.double() > 0)
+            want[1][again] = want[2][again] = NAN
+        else:
+            want[0][wide(by_head)] = NAN
+            want[1][wide(reached)] = NAN
+            want[2][sees @ bad[a:b].double() > 0] = INF if what == "inf do" else NAN
+        for third in range(3):
+            part, off = got[a:b, third * H:(third + 1) * H], lu.packed(bounds[third])
+            if what == "inf do" and third < 2:      # infinite or NaN, as their differences come out
+                fine = ~torch.isnan(want[third])
+                assert not bool(torch.isfinite(part[~fine].float()).any())
+                part, off, want[third] = part[fine], off[fine], want[third][fine]
+            assert_within(part, want[third], off)
+        a = b

@@ -25,6 +25,7 @@
 #include "train_internal.cuh"
 
 #include <limits.h>
+#include <math.h>
 #include <string.h>
 
 #include <algorithm>
@@ -248,15 +249,20 @@ constexpr int NUM_THREADS = 32 * (FIRST_WORKER + WORKERS);
 constexpr uint32_t TILE_BYTES = TILE * HD * 2;                       // 16 KB
 constexpr uint32_t OFF_ROWS = 0;                                     // 2 buffers of two tiles
 constexpr uint32_t OFF_COLS = OFF_ROWS + 4 * TILE_BYTES;             // STAGES of two tiles
-// Where columns are queries, their lse and delta come as 16 more columns of the
-// operands: the stage's rows hold -8 lse in three bf16 that add up to it, then -delta in
-// three, and the rows' side is ones against the three that S, or dP, is to get.  (Read
-// from shared memory by the workers, a column's two numbers go to 128 threads each: 512
-// bytes a warp for 16 of them, 1024 cycles a tile for what the tensor cores do in 128.)
-constexpr uint32_t EXT_BYTES = TILE * 16 * 2;                        // 4 KB, not swizzled: 8 rows x 16 bytes together
+// Where columns are queries, their lse and delta come as 16 more columns of the operands:
+// for S the stage's rows hold -8 lse in three bf16 that add up to it, for dP -delta in
+// three, and the rows' side is ones against them.  The other columns are zeros on both
+// sides: ones against lse alone, with zeros against delta beside it, would make a P of NaN
+// of a delta that is.  (Read from shared memory by the workers, a column's two numbers go to
+// 128 threads each: 512 bytes a warp for 16 of them, 1024 cycles a tile for what the tensor
+// cores do in 128.)
+// Not swizzled: 8 rows of eight columns are 128 bytes.  A stage has three such pieces for
+// 8 rows, {lse, zeros, delta}, and S takes the first two, dP the last two.
+constexpr uint32_t EXT_PIECES = 3 * 128, EXT_BYTES = TILE / 8 * EXT_PIECES;
+constexpr uint32_t ONES_PIECES = 2 * 128, ONES_BYTES = TILE / 8 * ONES_PIECES;
 constexpr uint32_t OFF_EXT = OFF_COLS + STAGES * 2 * TILE_BYTES;     // STAGES
 constexpr uint32_t OFF_ONES = OFF_EXT + STAGES * EXT_BYTES;          // for S, for dP
-constexpr uint32_t OFF_OUT = OFF_ONES + 2 * EXT_BYTES;               // a 4 KB box per worker warp
+constexpr uint32_t OFF_OUT = OFF_ONES + 2 * ONES_BYTES;              // a 4 KB box per worker warp
 constexpr uint32_t OFF_BAR = OFF_OUT + WORKERS * 4096;
 constexpr int B_RF = 0, B_RE = 2, B_CF = 4, B_CE = B_CF + STAGES, B_SF = B_CE + STAGES, B_XF = B_SF + STAGES, B_X2R = B_XF + 2, B_PF = B_X2R + 1,
               B_OF = B_PF + 2, B_OE = B_OF + 1, B_DONE = B_OE + 1, N_BARS = B_DONE + 1;
@@ -269,19 +275,23 @@ constexpr uint32_t TM_X1 = 0, TM_X2 = 256, TM_O = 384, TMEM_COLS = 512;
 constexpr uint32_t TILE_DESC = TILE_BYTES >> 4, PAIR_DESC = 2 * TILE_DESC;   // a tile, and two, as descriptors count
 constexpr float SCALE_LOG2 = 1.4426950408889634f / 8.0f;
 
-// Descriptor of the 16 further columns: K-major, no swizzle; the two 16-byte columns of
-// 8 rows are 128 bytes apart, 8 rows and the next 8 256.
-__device__ __forceinline__ uint64_t ext_desc(uint32_t saddr) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(128 >> 4) << 16 | (uint64_t)(256 >> 4) << 32 | (uint64_t)1 << 46;
+// Descriptor of 16 further columns: K-major, no swizzle; their two pieces of 8 rows are 128
+// bytes apart, 8 rows and the next 8 `pieces`.
+__device__ __forceinline__ uint64_t ext_desc(uint32_t saddr, uint32_t pieces) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(128 >> 4) << 16 | (uint64_t)(pieces >> 4) << 32 | (uint64_t)1 << 46;
 }
-__device__ __forceinline__ uint32_t ext_offset(int row) { return (row >> 3) * 256 + (row & 7) * 16; }
-// v as three bf16 whose sum is within 2^-24 of it.
-__device__ __forceinline__ void three_bf16(float v, bf16 (&o)[3]) {
+// v as three bf16 whose sum is within 2^-24 of it, one piece of a row; infinities as they are.
+__device__ __forceinline__ uint4 three_bf16(float v) {
+    bf16 o[8] = {};
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
         o[i] = __float2bfloat16_rn(v);
         v -= __bfloat162float(o[i]);
+        if (!(v < INFINITY)) v = 0.f;
     }
+    uint4 q;
+    memcpy(&q, o, 16);
+    return q;
 }
 
 struct BwdParams {
@@ -415,13 +425,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) tmem_alloc<1>(smem_u32(tmem_slot), TMEM_COLS);
-    // ones against -lse, ones against -delta, and the zero halves of the further columns
-    for (int i = threadIdx.x; i < (STAGES + 2) * TILE * 2; i += NUM_THREADS) {
-        const int tile = i / (TILE * 2), row = i / 2 % TILE;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (i % 2 == 0 && tile == STAGES) v = make_uint4(0x3f803f80u, 0x00003f80u, 0, 0);
-        if (i % 2 == 0 && tile == STAGES + 1) v = make_uint4(0, 0x3f800000u, 0x3f803f80u, 0);
-        *reinterpret_cast<uint4*>(smem + OFF_EXT + tile * EXT_BYTES + ext_offset(row) + i % 2 * 128) = v;
+    // the further columns' zeros, and ones against -lse in the first piece of 8 rows, against -delta in the second
+    for (int i = threadIdx.x; i < (int)(STAGES * EXT_BYTES + 2 * ONES_BYTES) / 16; i += NUM_THREADS) {
+        const int at = i * 16 - STAGES * EXT_BYTES, to = at / (int)ONES_BYTES, piece = at % (int)ONES_PIECES / 128;
+        *reinterpret_cast<uint4*>(smem + OFF_EXT + 16 * i) =
+            at >= 0 && piece == to ? make_uint4(0x3f803f80u, 0x00003f80u, 0, 0) : make_uint4(0, 0, 0, 0);
     }
     fence_proxy_async_smem();
     tc_fence_before();
@@ -485,13 +493,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         // S + 8 (-lse), of which log2(e) / 8 is the exponent
-                        bf16 a[3], b[3];
-                        three_bf16(v[0][i] * (1.0f / SCALE_LOG2), a);
-                        three_bf16(v[1][i], b);
-                        const bf16 row[8] = {a[0], a[1], a[2], b[0], b[1], b[2], bf16(0.f), bf16(0.f)};
-                        uint4 q;
-                        memcpy(&q, row, 16);
-                        *reinterpret_cast<uint4*>(smem + OFF_EXT + s * EXT_BYTES + ext_offset(i * 32 + lane)) = q;
+                        uint8_t* const ext = smem + OFF_EXT + s * EXT_BYTES + (4 * i + (lane >> 3)) * EXT_PIECES + (lane & 7) * 16;
+                        *reinterpret_cast<uint4*>(ext) = three_bf16(v[0][i] * (1.0f / SCALE_LOG2));
+                        *reinterpret_cast<uint4*>(ext + 256) = three_bf16(v[1][i]);
                     }
                     fence_proxy_async_smem();
                 }
@@ -518,7 +522,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const bool is_s = warp == 1;
         const uint32_t op = is_s ? 0 : TILE_DESC;
         const uint64_t rows0 = sw128_desc(sbase + OFF_ROWS) + op, cols0 = sw128_desc(sbase + OFF_COLS) + op;
-        const uint64_t ones = ext_desc(sbase + OFF_ONES + (is_s ? 0 : EXT_BYTES)), ext0 = ext_desc(sbase + OFF_EXT);
+        const uint64_t ones = ext_desc(sbase + OFF_ONES + (is_s ? 0 : ONES_BYTES), ONES_PIECES);
+        const uint64_t ext0 = ext_desc(sbase + OFF_EXT + (is_s ? 0 : 128), EXT_PIECES);
         uint32_t t = 0;
         bool ok = true;
         UnitStream units(p, n_units);
