@@ -190,3 +190,66 @@ def test_backward_of_scattered_values(enc, lens, window, what):
                 part, off, want[third] = part[fine], off[fine], want[third][fine]
             assert_within(part, want[third], off)
         a = b
+
+
+@pytest.mark.parametrize("lens,window", [([32768], 64), ([700, 1000, 31068], 40000), ([60] * 500 + [100] * 27, -1)],
+                         ids=["window", "wide", "short"])
+@pytest.mark.parametrize("what", ["all", "k", "v", "do"])
+def test_backward_of_nan_takes_no_longer(enc, lens, window, what):
+    heads = 4
+    H, T = heads * lu.HD, sum(lens)
+    qkv, do = inputs(T, heads, 1)
+    cu = lu.offsets(lens)
+    o, lse, call = forward_call(enc, qkv, cu, heads, window)
+    call()
+    g, call = backward_call(enc, qkv, cu, o, lse, do, heads, window)
+    normal = micros(call)
+    clean = g.clone()
+    if what in ("all", "do"):
+        do[:] = NAN
+    if what != "do":
+        qkv[:, {"all": slice(None), "k": slice(H, 2 * H), "v": slice(2 * H, None)}[what]] = NAN
+        o, lse, call = forward_call(enc, qkv, cu, heads, window)
+        call()
+    g, call = backward_call(enc, qkv, cu, o, lse, do, heads, window)
+    took = micros(call)
+    assert enc.device_status() == binding.TEE_OK
+    assert bool(torch.isnan(g[:, :2 * H].float()).all())
+    if what == "v":      # dv needs none of v
+        assert torch.equal(g[:, 2 * H:], clean[:, 2 * H:])
+    else:
+        assert bool(torch.isnan(g[:, 2 * H:].float()).all())
+    assert took < 5 * normal, (took, normal)
+
+
+def test_backward_beside_nan_with_the_widest_window(enc):
+    """The longest text between two of NaN, with a window as wide: right, and far from the two seconds of a wait."""
+    n = 131072
+    lens = [1, n, 50]
+    T = sum(lens)
+    qkv, do = inputs(T, 1, 5)
+    cu = lu.offsets(lens)
+    o, lse, call = forward_call(enc, qkv, cu, 1, n)
+    call()
+    for x in (qkv, do, o):
+        x[0], x[1 + n:] = NAN, NAN
+    lse[:, 0], lse[:, 1 + n:] = NAN, NAN
+    g, call = backward_call(enc, qkv, cu, o, lse, do, 1, n)
+    took = micros(call)
+    assert enc.device_status() == binding.TEE_OK
+    assert bool(torch.isnan(g[0].float()).all()) and bool(torch.isnan(g[1 + n:].float()).all())
+    assert bool(torch.isfinite(g[1:1 + n].float()).all())
+    x, d = qkv[1:1 + n].double(), do[1:1 + n].double()
+    q, k, v = x[:, :64], x[:, 64:128], x[:, 128:]
+    delta, stat = (d * o[1:1 + n].double()).sum(1), lse[0, 1:1 + n].double()
+    for i in (0, 39, 126, 127, 70000, n - 2, n - 1):
+        p = torch.exp(k @ q[i] / 8 - stat[i])
+        ds = p * (v @ d[i] - delta[i])
+        pc = torch.exp(q @ k[i] / 8 - stat)
+        dsc = pc * (d @ v[i] - delta)
+        # P or dS rounded to bf16 term by term, or not and the sum in fp32 by four chains; dp and delta to 2^-10 of their size
+        for part, w, other in ((g[1 + i, :64], ds / 8, k), (g[1 + i, 64:128], dsc / 8, q), (g[1 + i, 128:], pc, d)):
+            want, size = w @ other, w.abs() @ other.abs()
+            off = (lu.HALF + 2.0 ** -10) * size + lu.mma(n, size)
+            assert_within(part, want, off + lu.HALF * (want.abs() + off))
+    assert took < 1e6, took

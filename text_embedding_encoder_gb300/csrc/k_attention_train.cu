@@ -303,6 +303,10 @@ struct BwdParams {
     unsigned int* status;
 };
 
+// How many units are the CTA's.
+__device__ __forceinline__ int bwd_units(const BwdParams& p) {
+    return attn_units_of(*p.plan.n_items * 2 * p.n_heads, blockIdx.x, gridDim.x);
+}
 // A CTA's units in turn, each read while the one before is worked on: {q_start, q_len |
 // keys << 8 | head << 16, k_lo, k_hi}.  An item's rows as keys, the longer kind, for every
 // head, then as queries, which finds them in L2.  From unit to unit (attn_unit) the steps
@@ -356,39 +360,103 @@ __device__ __noinline__ bool warp_wait_longer(uint32_t bar, uint32_t parity, vol
     }
 }
 
-// What a worker warp writes of one row, 32 columns of dq, or its dk (chunk 0) or dv, again, outside the tensor cores, by a whole
-// warp: of a row whose products met NaN or infinities of rows that it does not see.
-__device__ __noinline__ void bwd_row_again(const BwdParams& p, int row, int head, bool keys, int lo, int hi, int chunk) {
-    const int lane = threadIdx.x & 31, H = p.hidden;
-    auto two = [&](const bf16* base, size_t at) {
-        return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(base + at + head * HD + 2 * lane));
-    };
-    auto dot = [](float2 a, float2 b) {
-        float s = a.x * b.x + a.y * b.y;
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-        return s;
-    };
+// The columns that a row of a unit sees, its text being {tb.x, tb.y}: the text, and in
+// window layers the window in it.
+__device__ __forceinline__ void seen_columns(const BwdParams& p, const int4& it, int row, const int2& tb, int& lo, int& hi) {
+    lo = max(tb.x, it.z), hi = min(tb.y, it.w);
+    if (p.window >= 0) lo = max(lo, row - p.window), hi = min(hi, row + p.window + 1);
+}
+
+// dq of one row, or its dk (`first`) and dv (`second`), again, from the columns that it sees,
+// outside the tensor cores, by a whole warp: four columns side by side, eight lanes to each,
+// the loads of three such steps on their way together.  It ends early where nothing but NaN
+// can come.
+__device__ __noinline__ void bwd_row_again(const BwdParams& p, int row, int head, bool keys, int lo, int hi, bool first, bool second) {
+    constexpr int AT_ONCE = 3;
+    const int lane = threadIdx.x & 31, part = lane >> 3, at = head * HD + (lane & 7) * 8, H = p.hidden;
     const size_t stride = 3 * (size_t)H;
-    const float2 a1 = two(p.qkv, row * stride + (keys ? H : 0));
-    const float2 a2 = keys ? two(p.qkv, row * stride + 2 * H) : two(p.d_o, (size_t)row * H);
-    float2 o1 = make_float2(0.f, 0.f), o2 = o1;
-    for (int j = lo; j < hi; ++j) {
-        const float2 b1 = two(p.qkv, j * stride + (keys ? 0 : H));
-        const float2 b2 = keys ? two(p.d_o, (size_t)j * H) : two(p.qkv, j * stride + 2 * H);
-        const size_t s = (size_t)head * p.T + (keys ? j : row);
-        const float e = ex2_approx(fmaf(dot(a1, b1), SCALE_LOG2, p.plan.nlse2[s]));
-        const float d = e * (dot(a2, b2) + p.plan.ndelta[s]);
-        o1.x = fmaf(d, b1.x, o1.x), o1.y = fmaf(d, b1.y, o1.y);
-        o2.x = fmaf(e, b2.x, o2.x), o2.y = fmaf(e, b2.y, o2.y);
+    const bf16* const qkv = p.qkv + at;
+    const bf16* const d_o = p.d_o + at;
+    float a1[8], a2[8], o1[8] = {}, o2[8] = {};
+    load_vec(qkv + row * stride + (keys ? H : 0), a1);
+    load_vec(keys ? qkv + row * stride + 2 * H : d_o + (size_t)row * H, a2);
+    for (int j0 = lo; j0 < hi; j0 += 4 * AT_ONCE) {
+        uint4 q1[AT_ONCE], q2[AT_ONCE];
+        float nl[AT_ONCE], nd[AT_ONCE];
+#pragma unroll
+        for (int u = 0; u < AT_ONCE; ++u) {
+            const int j = min(j0 + 4 * u + part, hi - 1);
+            const size_t s = (size_t)head * p.T + (keys ? j : row);
+            q1[u] = *reinterpret_cast<const uint4*>(qkv + j * stride + (keys ? 0 : H));
+            q2[u] = *reinterpret_cast<const uint4*>(keys ? d_o + (size_t)j * H : qkv + j * stride + 2 * H);
+            nl[u] = p.plan.nlse2[s], nd[u] = p.plan.ndelta[s];
+        }
+#pragma unroll
+        for (int u = 0; u < AT_ONCE; ++u) {
+            float b1[8], b2[8], s1 = 0.f, s2 = 0.f;
+            unpack_bf16x8(q1[u], b1);
+            unpack_bf16x8(q2[u], b2);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s1 = fmaf(a1[i], b1[i], s1), s2 = fmaf(a2[i], b2[i], s2);
+#pragma unroll
+            for (int d = 4; d > 0; d >>= 1) {
+                s1 += __shfl_xor_sync(0xffffffffu, s1, d);
+                s2 += __shfl_xor_sync(0xffffffffu, s2, d);
+            }
+            if (j0 + 4 * u + part < hi) {
+                const float e = ex2_approx(fmaf(s1, SCALE_LOG2, nl[u])), d = e * (s2 + nd[u]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o1[i] = fmaf(d, b1[i], o1[i]), o2[i] = fmaf(e, b2[i], o2[i]);
+            }
+        }
+        const bool nan1 = each_eighth_has(all_nan(o1)), nan2 = each_eighth_has(all_nan(o2));
+        if ((nan1 || !first) && (nan2 || !second)) break;
     }
-    bf16* dst = p.dqkv + row * stride + head * HD + 2 * lane;
-    if (!keys) {
-        if (lane / 16 == chunk) *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(o1.x * 0.125f, o1.y * 0.125f);
-    } else if (chunk) {
-        *reinterpret_cast<uint32_t*>(dst + 2 * H) = pack_bf16x2(o2.x, o2.y);
-    } else {
-        *reinterpret_cast<uint32_t*>(dst + H) = pack_bf16x2(o1.x * 0.125f, o1.y * 0.125f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+#pragma unroll
+        for (int d = 8; d < 32; d *= 2) {
+            o1[i] += __shfl_xor_sync(0xffffffffu, o1[i], d);
+            o2[i] += __shfl_xor_sync(0xffffffffu, o2[i], d);
+        }
+        o1[i] *= 0.125f;
+    }
+    if (part) return;
+    bf16* const dst = p.dqkv + row * stride + at;
+    if (first) store_vec(dst + (keys ? H : 0), o1);
+    if (second) store_vec(dst + 2 * H, o2);
+}
+
+// Rows whose products met NaN or infinities of rows that they do not see are computed again,
+// as by the forward kernel (attn_again): once all of the CTA's units are done and no role
+// waits for another any more; not those that see all of the item's columns, and not those that
+// cannot have another gradient, as their own term is NaN in all of its columns: dq and dk
+// of a row whose log sum or delta is NaN, dv of one whose log sum is or whose d_o is nothing else.
+__device__ __noinline__ void bwd_again(const BwdParams& p) {
+    const int lane = threadIdx.x & 31, units = bwd_units(p);
+    for (int task = threadIdx.x >> 5; task < 4 * units; task += NUM_THREADS / 32) {
+        const int unit = attn_unit(task >> 2, blockIdx.x, gridDim.x), item = unit / p.n_heads, head = unit - item * p.n_heads;
+        const bool keys = !(item & 1);
+        const int4 it = p.plan.items[item >> 1];
+        const int r = (task & 3) * 32 + lane, row = it.x + r;
+        int lo = 0, hi = 0;
+        bool first = false, second = false;
+        if (r < it.y) {
+            seen_columns(p, it, row, p.plan.row_tb[row], lo, hi);
+            const size_t s = (size_t)head * p.T + row;
+            const float nl = p.plan.nlse2[s], nd = p.plan.ndelta[s];
+            if ((lo > it.z || hi < it.w) && nl == nl) {
+                const bf16* const out = p.dqkv + (size_t)row * 3 * p.hidden + head * HD;
+                first = nd == nd && !all_finite(out + (keys ? p.hidden : 0));
+                second = keys && !all_finite(out + 2 * p.hidden) && !all_nan(p.d_o + (size_t)row * p.hidden + head * HD);
+            }
+        }
+        const unsigned firsts = __ballot_sync(0xffffffffu, first), seconds = __ballot_sync(0xffffffffu, second);
+        for (unsigned again = firsts | seconds; again; again &= again - 1) {
+            const int l = __ffs(again) - 1;
+            bwd_row_again(p, __shfl_sync(0xffffffffu, row, l), head, keys, __shfl_sync(0xffffffffu, lo, l),
+                          __shfl_sync(0xffffffffu, hi, l), firsts >> l & 1, seconds >> l & 1);
+        }
     }
 }
 
@@ -402,6 +470,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + N_BARS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile int* not_finite = abort_flag + 1;   // some output is not
     auto bar = [&](int i) { return smem_u32(bars + i); };
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
@@ -421,7 +490,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         mbar_init(bar(B_OF), 1);
         mbar_init(bar(B_OE), WORKERS);
         mbar_init(bar(B_DONE), 3);            // all issuers
-        *abort_flag = 0;
+        *abort_flag = *not_finite = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) tmem_alloc<1>(smem_u32(tmem_slot), TMEM_COLS);
@@ -439,7 +508,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     pdl_wait();
     pdl_trigger();
 
-    const int n_units = attn_units_of(*p.plan.n_items * 2 * p.n_heads, blockIdx.x, gridDim.x);
+    const int n_units = bwd_units(p);
     // a whole warp's wait: true for all lanes, or false for all
     auto warp_wait = [&](int b, uint32_t parity) -> bool {
         return __all_sync(0xffffffffu, mbar_try_wait(bar(b), parity)) || warp_wait_longer(bar(b), parity, abort_flag);
@@ -610,16 +679,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
         // the text of row r of a unit, {0, 0} behind its rows
         auto text_of = [&](const int4& it) -> int2 { return r < (it.y & 0xff) ? p.plan.row_tb[it.x + r] : make_int2(0, 0); };
-        // the columns that the row sees: its own text, and in window layers the window in it
-        auto seen = [&](const int4& it, const int2& tb, int& lo, int& hi) {
-            const int row = it.x + r;
-            lo = max(tb.x, it.z), hi = min(tb.y, it.w);
-            if (p.window >= 0) lo = max(lo, row - p.window), hi = min(hi, row + p.window + 1);
-        };
         // A unit's outputs, read once the next one's first tile is handed over: dq, half by
         // each warp of the two, or dk by one and dv by the other.  They leave as copies of 32 rows (row by row from the threads, a warp's store touches 32 lines: 1024
         // to 2048 cycles a unit for the 8 warps).
-        auto finish = [&](int ui_p, const int4& it_p, const int2& tb_p) -> bool {
+        auto finish = [&](int ui_p, const int4& it_p) -> bool {
             const int q_len_p = it_p.y & 0xff, row_p = r < q_len_p ? it_p.x + r : -1, head_p = it_p.y >> 16;
             const bool keys_p = it_p.y >> 8 & 1;
             if (!warp_wait(B_OF, ui_p & 1)) return false;
@@ -664,21 +727,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     bulk_commit();
                 }
             }
-            // rows of one text that all see the same columns meet no others' values
-            const bool alone = p.window < 0 && tb_p.x == it_p.z && tb_p.y == it_p.w;
-            unsigned again = __ballot_sync(0xffffffffu, row_p >= 0 && !alone && !(z == 0.f));
-            if (!again) return true;
-            if (lane == 0) bulk_wait_all();
-            __syncwarp();
-            int lo_p, hi_p;
-            seen(it_p, tb_p, lo_p, hi_p);
-            while (again) {
-                const int l = __ffs(again) - 1;
-                again &= again - 1;
-                bwd_row_again(p, __shfl_sync(0xffffffffu, row_p, l), head_p, keys_p, __shfl_sync(0xffffffffu, lo_p, l),
-                              __shfl_sync(0xffffffffu, hi_p, l), chunk);
-            }
-            __syncwarp();
+            if (row_p >= 0 && !(z == 0.f)) *not_finite = 1;
             return true;
         };
 
@@ -695,7 +744,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         statistics();
         for (int ui = 0; ui <= n_units && ok; ++ui) {
             const int4 it_p = it;
-            const int2 tb_p = tb;
             it = it_next, tb = tb_next;
             const float nl = nl_next, nd = nd_next;
             it_next = units.next();
@@ -704,7 +752,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const int q_len = it.y & 0xff, k_lo = it.z, k_hi = it.w, nk = unit_tiles(it);
             const bool keys = it.y >> 8 & 1;
             int vis_lo, vis_hi;
-            seen(it, tb, vis_lo, vis_hi);
+            seen_columns(p, it, it.x + r, tb, vis_lo, vis_hi);
             const uint64_t nl2 = f2_pack(nl, nl), nd2 = f2_pack(nd, nd);
             // Columns that any row of the warp sees, and that all see: a row's first and last column never lie before those
             // of the row before.  A row behind the item's sees them all: what it adds up is not stored, and what it
@@ -809,7 +857,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             for (int part = 0; part < 2 && ok; ++part) {
                 const int from = part ? 1 : 0, to = part ? nk : min(nk, 1);
                 ok = keys ? tiles(std::true_type{}, from, to) : tiles(std::false_type{}, from, to);
-                if (ok && part == 0 && ui > 0) ok = finish(ui - 1, it_p, tb_p);
+                if (ok && part == 0 && ui > 0) ok = finish(ui - 1, it_p);
             }
         }
     }
@@ -822,6 +870,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         tmem_dealloc<1>(tmem_base, TMEM_COLS);
     }
     if (threadIdx.x == 0 && *abort_flag) atomicOr(p.status, TEE_STATUS_TIMEOUT);
+    if (*not_finite && !*abort_flag) bwd_again(p);
 }
 
 // ---------------------------------------------------------------------------
