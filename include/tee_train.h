@@ -205,7 +205,8 @@ long long tee_geglu_backward_workspace(int T, int H, int I);
  * h_grads[i] (where factor is 1 it is then not written); no output may overlap another
  * or another tensor's gradient otherwise.  h_outs NULL: all in place.  Counts may be 0.
  * max_norm >= 0, infinity for the norm alone.  Squares are summed without overflow
- * or underflow whatever the magnitudes.  0 <= n_tensors <= 65536. */
+ * or underflow whatever the magnitudes.  0 <= n_tensors <= 65536.  TEE_ENOMEM where the
+ * host has no memory to compare the tensors' places. */
 int tee_op_clip_gradients(tee_ctx* ctx, const void* const* h_grads, const int32_t* h_types, const int64_t* h_counts,
                           void* const* h_outs, int n_tensors, float max_norm, float* d_norm, void* d_ws,
                           size_t ws_bytes, void* stream);

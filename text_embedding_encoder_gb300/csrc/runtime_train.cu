@@ -1,5 +1,6 @@
 // Entry points of the training operators (tee_train.h): argument checks, the
 // context's device, one launcher call each.
+#include "clip_ranges.h"
 #include "train_internal.cuh"
 
 #include <float.h>
@@ -7,7 +8,6 @@
 
 #include <algorithm>
 #include <initializer_list>
-#include <vector>
 
 namespace {
 
@@ -106,31 +106,6 @@ const char* geglu_sizes(int T, int H, int I) {
     if (H < 8 || H % 8 || H > TEE_GEGLU_MAX_HIDDEN) return "H must be a multiple of 8 within range";
     if (I < 8 || I % 8 || I > TEE_GEGLU_MAX_WIDTH) return "I must be a multiple of 8 within range";
     return nullptr;
-}
-
-// Whether an output overlaps another one or a gradient that is not its own.
-bool clip_overlaps(const void* const* grads, const int32_t* types, const int64_t* counts, void* const* outs, int n) {
-    struct Range {
-        uintptr_t begin, end;
-        bool out;
-    };
-    std::vector<Range> r;
-    r.reserve(2 * (size_t)n);
-    for (int i = 0; i < n; ++i) {
-        if (counts[i] == 0) continue;
-        const uintptr_t bytes = (uintptr_t)counts[i] * type_size(types[i]);
-        const uintptr_t g = (uintptr_t)grads[i], o = (uintptr_t)(outs ? outs[i] : grads[i]);
-        r.push_back({o, o + bytes, true});
-        if (g != o) r.push_back({g, g + bytes, false});
-    }
-    std::sort(r.begin(), r.end(), [](const Range& a, const Range& b) { return a.begin < b.begin; });
-    uintptr_t any = 0, out = 0;   // ends of what lies before
-    for (const Range& x : r) {
-        if (x.begin < (x.out ? any : out)) return true;
-        any = std::max(any, x.end);
-        if (x.out) out = std::max(out, x.end);
-    }
-    return false;
 }
 
 }  // namespace
@@ -399,7 +374,9 @@ int tee_op_clip_gradients(tee_ctx* ctx, const void* const* h_grads, const int32_
         if (h_outs && (rc = check_bufs(ctx, op, {{"an output", h_outs[i], align}}))) return rc;
         bytes += 3.0 * h_counts[i] * align;
     }
-    if (clip_overlaps(h_grads, h_types, h_counts, h_outs, n_tensors)) return bad(ctx, op, "tensors overlap");
+    const int overlap = clip_overlaps(h_grads, h_counts, h_types, TEE_BF16, h_outs, n_tensors);
+    if (overlap < 0) return tee_set_error(ctx, TEE_ENOMEM, "clip_gradients: host allocation failed");
+    if (overlap) return bad(ctx, op, "tensors overlap");
     return launch(ctx, op, TEE_K_ELEMENTWISE, 0, bytes, stream, [&](cudaStream_t s) {
         return launch_clip_gradients(h_grads, h_types, h_counts, h_outs ? (const void* const*)h_outs : h_grads, n_tensors,
                                      max_norm, d_norm, d_ws, s);
