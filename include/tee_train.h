@@ -151,8 +151,12 @@ int tee_op_rope_backward(tee_ctx* ctx, const void* d_dy, int type, const int32_t
  * the DEVICE: cu[0] = 0, cu not decreasing, cu[n_texts] <= T, at most
  * TEE_ATTN_MAX_TEXT_TOKENS tokens to a text.  Other offsets set the device status
  * and leave the outputs as they were.  Texts may be empty.  Rows behind the last
- * text are neither read nor written, whatever they hold, and no text's results
- * depend on another's values, were they NaN.
+ * text are not written, and what they hold has no effect, were it NaN, but all T rows
+ * of every buffer have to be there: tiles reach into them.  No text's results depend
+ * on another's values: they are the same bits whatever finite ones those are.  Next to
+ * values that are not finite a row may be computed another way, to the same error bound.
+ * Values that are not finite give what the formulas give, in the rows and columns
+ * that they reach, and in no others.
  * o bf16[T * 64 n_heads], lse float[n_heads * T], head by head.
  * 0 <= T <= 2^24, 0 <= n_texts <= 2^20.  The host sees neither cu nor the texts'
  * lengths, so one captured graph serves batches of other texts.

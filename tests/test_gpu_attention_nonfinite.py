@@ -1,5 +1,5 @@
 """Attention of a training step over values that are not finite: they stay where the definition has them, whatever shares a
-tile with them, and a batch of nothing else takes about the time of any other."""
+tile with them, and a batch of nothing else takes about the time of any other.  And over neighbours that are finite."""
 import pytest
 import torch
 
@@ -253,3 +253,24 @@ def test_backward_beside_nan_with_the_widest_window(enc):
             off = (lu.HALF + 2.0 ** -10) * size + lu.mma(n, size)
             assert_within(part, want, off + lu.HALF * (want.abs() + off))
     assert took < 1e6, took
+
+
+@pytest.mark.parametrize("window", [-1, 16, 64])
+def test_finite_neighbours_change_no_bit(enc, window):
+    """Another text's values, and those of rows behind the last text, whatever finite ones they are."""
+    lens, heads = [40, 200, 60, 30], 2
+    n, a, b = sum(lens), 40, 240
+    qkv, do = inputs(n + 100, heads, 9)
+    cu = lu.offsets(lens)
+    other, d_other = inputs(n + 100, heads, 10)
+    keep = []
+    for scale in (None, 1.0, 1000.0):
+        q, d = qkv.clone(), do.clone()
+        if scale:
+            for rows in (slice(0, a), slice(b, None)):
+                q[rows], d[rows] = other[rows] * scale, d_other[rows] * scale
+        o, lse, _ = lu.attention_forward(enc, q, cu, heads, window)
+        o[n:], lse[:, n:] = (0.0, 0.0) if scale is None else (scale, -scale)
+        keep.append((o[a:b], lse[:, a:b], lu.attention_backward(enc, q, cu, o, lse, d, heads, window)[a:b]))
+    for other in keep[1:]:
+        assert all(torch.equal(x, y) for x, y in zip(keep[0], other))
