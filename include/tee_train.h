@@ -155,8 +155,8 @@ int tee_op_rope_backward(tee_ctx* ctx, const void* d_dy, int type, const int32_t
  * of every buffer have to be there: tiles reach into them.  No text's results depend
  * on another's values: they are the same bits whatever finite ones those are.  Next to
  * values that are not finite a row may be computed another way, to the same error bound.
- * Values that are not finite give what the formulas give, in the rows and columns
- * that they reach, and in no others.
+ * Values that are not finite give infinities or NaN in the rows and columns that they
+ * reach by the formulas, and in no others.
  * o bf16[T * 64 n_heads], lse float[n_heads * T], head by head.
  * 0 <= T <= 2^24, 0 <= n_texts <= 2^20.  The host sees neither cu nor the texts'
  * lengths, so one captured graph serves batches of other texts.

@@ -14,12 +14,13 @@
 // the operands of the other products already take).
 // Twelve warps: one brings the operands, three issue S, dP and the outputs' products, eight
 // make P and dS of them.
-// Measured, 12 heads: 8 texts of 8192 tokens 4.19 ms, where five products at the burst
+// Measured, 12 heads: 8 texts of 8192 tokens 4.2 ms, where five products at the burst
 // rate would take 2.09.  A pair of tiles takes 1430 cycles of each kind; the products by
 // themselves, issued without a pause, take 1330 (keys) and 920 (queries), as one of K = 16
-// costs 73 cycles with N = 128 and 38 with N = 64; the pipes are 64 to 67 % busy, under the
-// power limit's clock of 1.76 GHz.  +-64 windows, 32768 tokens of 187 texts: 124 us, 100 of
-// them in this kernel (205 + 114 MB of DRAM traffic) and 24 in the plan, which reads o and
+// costs 73 cycles with N = 128 and 38 with N = 64.  So the products set the pace where rows
+// are keys, and the workers where rows are queries; the pipes are 63 to 67 % busy, under the
+// power limit's clock of 1.76 GHz.  +-64 windows, 32768 tokens of 158 texts: 124 us, 98 of
+// them in this kernel (205 + 111 MB of DRAM traffic) and 24 in the plan, which reads o and
 // do (102 MB) for the deltas.
 #include "gemm_tc.cuh"
 #include "train_internal.cuh"
@@ -80,6 +81,9 @@ __device__ __forceinline__ int first_above(const int32_t* cu, int n, int v) {
 // ended: with next(j) the start after one at j, the starts are what is reached from 0,
 // found by doubling the steps (log2 of the number of texts).
 // Items of window layers: 128 rows of the packed batch, whatever texts they are of.
+// Up to PLAN_SHARED_TEXTS texts the lists are in shared memory.  For more, block 0 follows its
+// links through global memory while the others have long ended: 4000 texts of 16 tokens 54 us
+// (windows, which need no starts: 16), 60000 of 8 tokens 1.64 ms (0.11), 2^20 of one 39.7 ms (0.3).
 __global__ void __launch_bounds__(PLAN_THREADS) attn_plan_kernel(const PlanArgs a) {
     __shared__ int lists[3 * (PLAN_SHARED_TEXTS + 1)], offsets[PLAN_SHARED_TEXTS + 1];
     __shared__ int bucket[PLAN_BUCKETS + 1];
@@ -264,8 +268,8 @@ constexpr uint32_t OFF_EXT = OFF_COLS + STAGES * 2 * TILE_BYTES;     // STAGES
 constexpr uint32_t OFF_ONES = OFF_EXT + STAGES * EXT_BYTES;          // for S, for dP
 constexpr uint32_t OFF_OUT = OFF_ONES + 2 * ONES_BYTES;              // a 4 KB box per worker warp
 constexpr uint32_t OFF_BAR = OFF_OUT + WORKERS * 4096;
-constexpr int B_RF = 0, B_RE = 2, B_CF = 4, B_CE = B_CF + STAGES, B_SF = B_CE + STAGES, B_XF = B_SF + STAGES, B_X2R = B_XF + 2, B_PF = B_X2R + 1,
-              B_OF = B_PF + 2, B_OE = B_OF + 1, B_DONE = B_OE + 1, N_BARS = B_DONE + 1;
+constexpr int B_RF = 0, B_RE = 2, B_CF = 4, B_CE = B_CF + STAGES, B_SF = B_CE + STAGES, B_XF = B_SF + STAGES,
+              B_X2R = B_XF + 2, B_PF = B_X2R + 1, B_OF = B_PF + 2, B_OE = B_OF + 1, B_DONE = B_OE + 1, N_BARS = B_DONE + 1;
 constexpr uint32_t SMEM_TOTAL = OFF_BAR + N_BARS * 8 + 16 + 1024;
 static_assert(SMEM_TOTAL <= 227 * 1024, "shared memory");
 // Tensor memory: X1 = S of even and odd tiles, X2 = dP of the current one, the outputs.
@@ -278,7 +282,8 @@ constexpr float SCALE_LOG2 = 1.4426950408889634f / 8.0f;
 // Descriptor of 16 further columns: K-major, no swizzle; their two pieces of 8 rows are 128
 // bytes apart, 8 rows and the next 8 `pieces`.
 __device__ __forceinline__ uint64_t ext_desc(uint32_t saddr, uint32_t pieces) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(128 >> 4) << 16 | (uint64_t)(pieces >> 4) << 32 | (uint64_t)1 << 46;
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(128 >> 4) << 16 | (uint64_t)(pieces >> 4) << 32 |
+           (uint64_t)1 << 46;
 }
 // v as three bf16 whose sum is within 2^-24 of it, one piece of a row; infinities as they are.
 __device__ __forceinline__ uint4 three_bf16(float v) {
@@ -371,7 +376,8 @@ __device__ __forceinline__ void seen_columns(const BwdParams& p, const int4& it,
 // outside the tensor cores, by a whole warp: four columns side by side, eight lanes to each,
 // the loads of three such steps on their way together.  It ends early where nothing but NaN
 // can come.
-__device__ __noinline__ void bwd_row_again(const BwdParams& p, int row, int head, bool keys, int lo, int hi, bool first, bool second) {
+__device__ __noinline__ void bwd_row_again(const BwdParams& p, int row, int head, bool keys, int lo, int hi, bool first,
+                                           bool second) {
     constexpr int AT_ONCE = 3;
     const int lane = threadIdx.x & 31, part = lane >> 3, at = head * HD + (lane & 7) * 8, H = p.hidden;
     const size_t stride = 3 * (size_t)H;
@@ -562,7 +568,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         // S + 8 (-lse), of which log2(e) / 8 is the exponent
-                        uint8_t* const ext = smem + OFF_EXT + s * EXT_BYTES + (4 * i + (lane >> 3)) * EXT_PIECES + (lane & 7) * 16;
+                        uint8_t* const ext =
+                            smem + OFF_EXT + s * EXT_BYTES + (4 * i + (lane >> 3)) * EXT_PIECES + (lane & 7) * 16;
                         *reinterpret_cast<uint4*>(ext) = three_bf16(v[0][i] * (1.0f / SCALE_LOG2));
                         *reinterpret_cast<uint4*>(ext + 256) = three_bf16(v[1][i]);
                     }
@@ -680,8 +687,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // the text of row r of a unit, {0, 0} behind its rows
         auto text_of = [&](const int4& it) -> int2 { return r < (it.y & 0xff) ? p.plan.row_tb[it.x + r] : make_int2(0, 0); };
         // A unit's outputs, read once the next one's first tile is handed over: dq, half by
-        // each warp of the two, or dk by one and dv by the other.  They leave as copies of 32 rows (row by row from the threads, a warp's store touches 32 lines: 1024
-        // to 2048 cycles a unit for the 8 warps).
+        // each warp of the two, or dk by one and dv by the other.  They leave as copies of 32
+        // rows (row by row from the threads, a warp's store touches 32 lines: 1024 to 2048
+        // cycles a unit for the 8 warps).
         auto finish = [&](int ui_p, const int4& it_p) -> bool {
             const int q_len_p = it_p.y & 0xff, row_p = r < q_len_p ? it_p.x + r : -1, head_p = it_p.y >> 16;
             const bool keys_p = it_p.y >> 8 & 1;

@@ -79,7 +79,7 @@ struct Shares {
 };
 
 struct Params {
-    int T, H, I;
+    int H, I;
     // part being made: rows [up0, up0 + up_rows); being multiplied: rows [mul0, mul0 + mul_rows)
     int up0, up_rows, mul0, mul_rows;
     int dx_slices, dw_slices, dx_steps, dw_steps;   // slices, and K steps of each
@@ -642,7 +642,7 @@ cudaError_t launch_geglu_train_forward(const void* x, const void* wi, void* z, i
     TRY(make_tensor_map_2d(&maps.wi, false, wi, 2 * (uint64_t)I, H, H, 128, 64));
     TRY(make_tensor_map_2d(&maps.z, false, z, T, I, I, 32, 64));
     Params p{};
-    p.T = T, p.H = H, p.I = I;
+    p.H = H, p.I = I;
     p.up_rows = T;
     p.status = status;
     const int units = tiles_of(T, TILE) * tiles_of(I, HALF);
@@ -666,7 +666,7 @@ cudaError_t launch_geglu_train_backward(const void* x, const void* wi, const voi
     TRY(make_tensor_map_2d(&maps.wi_mn, false, wi, 2 * (uint64_t)I, H, H, 64, 64));
     TRY(make_tensor_map_2d(&maps.x_mn, false, x, T, H, H, 64, 64));
     Params p{};
-    p.T = T, p.H = H, p.I = I;
+    p.H = H, p.I = I;
     TRY(make_tensor_map_2d(&maps.dz, false, dz, T, I, I, 32, 64));
     p.status = status;
     Sum sum_dx{}, sum_dw{};

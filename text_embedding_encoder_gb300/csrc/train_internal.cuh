@@ -163,7 +163,7 @@ size_t clip_gradients_ws(int n_tensors);
 // What the plan kernel leaves on the device for the attention kernels.
 struct AttnPlan {
     int* n_items;       // work items in use (0 where the texts' offsets are not valid)
-    int4* items;        // {q_start, q_len, k_lo, k_hi}, the longest first: up to 128 rows and the keys they may see
+    int4* items;        // {q_start, q_len, k_lo, k_hi}: up to 128 rows and the keys they may see; of whole texts the longest first
     int2* row_tb;       // per token: {start, end} of its text, {0, 0} behind the last
     int* scratch;
     float* nlse2;       // backward: -lse / ln 2, [n_heads, T]
@@ -171,8 +171,9 @@ struct AttnPlan {
 };
 
 // The units of CTA c of G: one of each round of G, in turn from the first CTA on and
-// from the last on.  Units are listed the longest first, so that evens the sums out
-// without the host knowing the texts.
+// from the last on.  Of whole texts they are listed the longest first, so that evens the sums
+// out without the host knowing the texts; of windows they are in the order of their rows
+// (nearly all alike, but for windows that are wide beside some of the texts).
 __device__ __forceinline__ int attn_unit(int i, int c, int G) { return i * G + ((i & 1) ? G - 1 - c : c); }
 __device__ __forceinline__ int attn_units_of(int n, int c, int G) {
     const int rounds = n / G;
